@@ -374,6 +374,133 @@ int seed_dense_decode_step(const seed_shape *shape, float *S, const void *q, con
                            const void *v, const float *beta, const float *g, void *o,
                            void *stream);
 
+/* ---- the prompt path ---------------------------------------------------------------------------
+ *
+ * What a recurrent layer does to a prompt, and to a token next to the decode step: the short
+ * causal convolution of its projected channels, the scan that builds each head's dense state (then
+ * handed to seed_state_from_dense), and the norm of the read-outs.
+ *
+ * Packed prompts. The prompts of a call are the rows of one buffer, `tokens` rows in all; sequence b
+ * has rows offsets[b] .. offsets[b + 1] - 1 (int32 [batch + 1], device memory, not decreasing, within
+ * 0 .. tokens). A sequence may be empty. Rows before the first sequence and behind the last one are
+ * neither read nor written. The contents of offsets are read on the device and not checked on the
+ * host: entries are clamped into 0 .. tokens and a decreasing pair reads as an empty sequence, so
+ * wrong ones give wrong results but no access outside the buffers.
+ *
+ * Rows. Row buffers take a row stride, in elements, of at least the row's width; inside a row,
+ * heads and values are contiguous, so that q, k and v can be column ranges of one buffer. io_dtype
+ * is SEED_F32 or SEED_BF16. tokens or rows may be 0, and are at most 2^31 - 1 (else
+ * SEED_ERR_UNSUPPORTED). Outputs must not overlap each other or the inputs except where an entry says
+ * so; an overlap is SEED_ERR_ARG (two buffers of different strides whose ranges meet count as
+ * overlapping). Arithmetic is fp32, rounded once to io_dtype.
+ */
+
+/* A short causal convolution, one filter per channel:
+ *     y_t = act(bias + sum_{j < width} weight[j] x_{t - width + 1 + j}).                          */
+typedef struct seed_conv {
+  int32_t batch;     /* requests                                                                 */
+  int32_t channels;  /* any positive number                                                      */
+  int32_t width;     /* taps: 2, 3 or 4 (others SEED_ERR_UNSUPPORTED)                             */
+  int32_t io_dtype;  /* SEED_F32 or SEED_BF16: storage of x, y and the windows                   */
+  int32_t silu;      /* 1: act(y) = y / (1 + exp(-y)); 0: none                                   */
+} seed_conv;
+
+/*
+ * The convolution of packed prompts.
+ *   x, y        [tokens][channels] rows in io_dtype, x_stride and y_stride elements apart.
+ *   weight      float [width][channels]; bias float [channels] or NULL.
+ *   window_in   [batch][width - 1][channels] in io_dtype: the inputs before each sequence's first
+ *               row, oldest first (a prompt that continues), or NULL for zeros.
+ *   window_out  written, same layout: each sequence's last width - 1 inputs, reaching back into
+ *               window_in where it is shorter. An empty sequence's window is window_in's (or zeros).
+ * The windows and x, y must be disjoint, window_in and window_out too.
+ */
+int seed_prefill_conv(const seed_conv *conv, int64_t tokens, const int32_t *offsets, const void *x,
+                      int64_t x_stride, const float *weight, const float *bias, const void *window_in,
+                      void *window_out, void *y, int64_t y_stride, void *stream);
+
+/*
+ * The convolution of one token per request: x, y [batch][channels] rows; the request's window gives
+ * the inputs before it and moves up by one token.
+ *   active      uint8 [batch], device memory, or NULL for all: requests with active[b] == 0 are
+ *               skipped, their rows of y and window_out not written.
+ *   window_in, window_out  [batch][width - 1][channels]; may be the same buffer.
+ * y may be x (same address and stride).
+ */
+int seed_decode_conv(const seed_conv *conv, const uint8_t *active, const void *x, int64_t x_stride,
+                     const float *weight, const float *bias, const void *window_in, void *window_out,
+                     void *y, int64_t y_stride, void *stream);
+
+/* The packed prompts of a scan. */
+typedef struct seed_prompt {
+  int64_t tokens;
+  const int32_t *offsets;                          /* [batch + 1], device memory                 */
+  int32_t key_heads;                               /* heads of q and k; divides shape.heads      */
+  int64_t q_stride, k_stride, v_stride, o_stride;  /* elements between rows                      */
+} seed_prompt;
+
+/* Workspace bytes of seed_prefill_scan for these prompts (0: none needed, or invalid arguments).
+ * Depends on the sizes only. Host-only, pure. */
+size_t seed_prefill_workspace_bytes(const seed_shape *shape, const seed_prompt *prompt);
+
+/*
+ * The dense recurrence of seed_dense_decode_step over every token of packed prompts:
+ *     S_t = G_t S_{t-1} + beta_t k_t (v_t - (G_t S_{t-1})^T k_t)^T   (GDN, KDA)
+ *     S_t = g_t S_{t-1} + beta_t k_t v_t^T                           (Mamba-2)
+ * with the read-out o_t = S_t^T q_t.
+ *   shape   kind, batch (sequences), heads, d_k, d_v and io_dtype; the other fields are ignored.
+ *   q, k    [tokens][key_heads][d_k] rows (io_dtype): head h uses key head h / (heads / key_heads).
+ *   v, o    [tokens][heads][d_v] rows (io_dtype); o is written.
+ *   beta    float [tokens][heads]; g float [tokens][heads] (GDN, Mamba-2) or [tokens][heads][d_k]
+ *           (KDA), 0 <= g.
+ *   S0      float [batch][heads][d_k][d_v]: the states the sequences start from, or NULL for zeros.
+ *   S       written, same layout: the states after each sequence's last token (S0's, or zeros, for
+ *           an empty one). May be S0 itself.
+ *   ws      workspace of seed_prefill_workspace_bytes bytes, 16-byte aligned (NULL when that is 0);
+ *           it must not be shared by calls that may run at the same time.
+ * q, k, v, o, S0, S (and KDA's g) must be 16-byte aligned and the row strides multiples of 16 bytes,
+ * else SEED_ERR_ARG. States are fp32 and every product with a state or a value takes fp32 operands;
+ * sums are fp32.
+ * Source: picx.dev summary, "Introduction and Theoretical Foundation" (the dense recurrence), and
+ * thelatestinai.com figures & tables, overview table (the prefill whose states are compressed when
+ * they leave it).
+ */
+int seed_prefill_scan(const seed_shape *shape, const seed_prompt *prompt, const void *q,
+                      const void *k, const void *v, const float *beta, const float *g, const float *S0,
+                      float *S, void *o, void *ws, size_t ws_bytes, void *stream);
+
+/* Packed rows of heads x dim values for seed_norm_rows; the strides of absent buffers are ignored. */
+typedef struct seed_rows {
+  int64_t rows;
+  int32_t heads, dim;  /* groups of a row and values of a group, both any positive number */
+  int32_t io_dtype;    /* SEED_F32 or SEED_BF16: x, y, gate, skip and total               */
+  int64_t x_stride, y_stride, gate_stride, skip_stride, total_stride;
+} seed_rows;
+
+/* A residual branch: x + scale[head] * skip takes the place of x (NULL scale: 1), and is written to
+ * total, rounded to io_dtype, unless that is NULL. scale without skip is SEED_ERR_ARG. */
+typedef struct seed_residual {
+  const void *skip;
+  const float *scale;  /* float [heads] */
+  void *total;
+} seed_residual;
+
+/*
+ * The head normalisation of seed_decode_step_normed for rows of read-outs: with x' = x, or x +
+ * scale skip when a residual is given, and u = x' silu(gate) when gate_first, else x',
+ *     y = weight[h] * u / sqrt(mean over dim of u^2 + eps)     (then * silu(gate) when a gate is given
+ *                                                               and !gate_first).
+ * One group per head (dim = d_v) normalises prompt read-outs, Mamba-2's D x skip included; one
+ * group per row (heads = 1) is the norm before a block, the residual stream kept in total.
+ *   norm      weight float [heads][dim] (required), gate rows in io_dtype or NULL, eps, gate_first.
+ *   residual  NULL for none.
+ * y may be x, gate or skip, and total may be x or skip (same address and stride); the norm is that of the
+ * sum before its rounding into total.
+ * Source: picx.dev summary, "Theoretical and Practical Implications" (the head's normalisation).
+ */
+int seed_norm_rows(const seed_rows *rows, const void *x, const seed_head_norm *norm,
+                   const seed_residual *residual, void *y, void *stream);
+
 /*
  * Streams restricted to a set of compute units, for schedules that run the HBM-bound decode and
  * the arithmetic-bound compression side by side on disjoint parts of the chip. These are the

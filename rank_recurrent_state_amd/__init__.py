@@ -22,6 +22,8 @@ _NAMES = {
     "seed_decode_chunk_ragged", "seed_compress_units",
     "SEED_SPECTRUM_LEN", "CUMaskedStream", "hip_runtimes_mapped", "seed_head_norm",
     "seed_decode_step_normed", "seed_decode_step_ragged_normed",
+    "make_conv", "seed_conv", "seed_decode_conv", "seed_norm_rows", "seed_prefill_conv", "seed_prefill_scan",
+    "seed_prefill_workspace_bytes", "seed_prompt", "seed_residual", "seed_rows",
     "seed_scale_len", "seed_shape", "seed_state", "seed_state_bytes", "seed_state_from_dense",
     "seed_status_string", "seed_version", "seed_workspace_bytes",
 }

@@ -25,7 +25,8 @@ EXPORTS = [
     "seed_compress_ragged", "seed_state_energy", "seed_dense_decode_step", "seed_decode_chunk",
     "seed_chunk_max_tokens", "seed_decode_chunk_ragged", "seed_state_spectrum", "seed_compress_units",
     "seed_stream_create_cu_masked", "seed_stream_destroy", "seed_decode_step_normed",
-    "seed_decode_step_ragged_normed", "seed_status_string", "seed_version",
+    "seed_decode_step_ragged_normed", "seed_prefill_conv", "seed_decode_conv", "seed_prefill_scan",
+    "seed_prefill_workspace_bytes", "seed_norm_rows", "seed_status_string", "seed_version",
 ]
 
 SEED_SPECTRUM_LEN = 33
@@ -50,6 +51,27 @@ class seed_shape(ctypes.Structure):
 class seed_head_norm(ctypes.Structure):
     _fields_ = [("weight", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("eps", ctypes.c_float),
                 ("gate_first", ctypes.c_int32)]
+
+
+class seed_conv(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("channels", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("silu", ctypes.c_int32)]
+
+
+class seed_prompt(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("key_heads", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("o_stride", ctypes.c_int64)]
+
+
+class seed_rows(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64), ("skip_stride", ctypes.c_int64), ("total_stride", ctypes.c_int64)]
+
+
+class seed_residual(ctypes.Structure):
+    _fields_ = [("skip", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("total", ctypes.c_void_p)]
 
 
 class seed_state(ctypes.Structure):
@@ -94,6 +116,7 @@ def _load():
     if len(rts) > 1:
         raise ImportError(f"more than one HIP runtime is mapped into this process: {rts}")
     P = ctypes.c_void_p
+    I64 = ctypes.c_int64
     Sp = ctypes.POINTER(seed_shape)
     Stp = ctypes.POINTER(seed_state)
     sig = {
@@ -120,6 +143,13 @@ def _load():
                                                    ctypes.POINTER(seed_head_norm), P, P]),
         "seed_decode_step_ragged_normed": (ctypes.c_int, [Sp, Stp, P, P, P, P, P, P, P,
                                                           ctypes.POINTER(seed_head_norm), P, P]),
+        "seed_prefill_conv": (ctypes.c_int, [ctypes.POINTER(seed_conv), I64, P, P, I64, P, P, P, P, P, I64, P]),
+        "seed_decode_conv": (ctypes.c_int, [ctypes.POINTER(seed_conv), P, P, I64, P, P, P, P, P, I64, P]),
+        "seed_prefill_workspace_bytes": (ctypes.c_size_t, [Sp, ctypes.POINTER(seed_prompt)]),
+        "seed_prefill_scan": (ctypes.c_int, [Sp, ctypes.POINTER(seed_prompt), P, P, P, P, P, P, P, P, P,
+                                             ctypes.c_size_t, P]),
+        "seed_norm_rows": (ctypes.c_int, [ctypes.POINTER(seed_rows), P, ctypes.POINTER(seed_head_norm),
+                                          ctypes.POINTER(seed_residual), P, P]),
         "seed_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "seed_version": (ctypes.c_char_p, []),
     }
@@ -480,3 +510,180 @@ def seed_dense_decode_step(shape: seed_shape, S, q, k, v, beta, g, o, stream=Non
     _check("seed_dense_decode_step", LIB.seed_dense_decode_step(
         ctypes.byref(shape), _ptr(S), _ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(o),
         _stream_ptr(stream)))
+
+
+# ---- the prompt path ------------------------------------------------------------------------------
+
+
+def make_conv(batch: int, channels: int, width: int, io_dtype: int = SEED_BF16, silu: bool = True) -> seed_conv:
+    """A seed_conv: `width` taps per channel, SiLU behind them unless silu is False."""
+    return seed_conv(batch, channels, width, io_dtype, int(silu))
+
+
+def _expect_rows(name, t, rows, inner, code):
+    """Marshalling check of a row buffer [rows, *inner] whose rows may be strided: returns the row
+    stride in elements."""
+    width = 1
+    for n in inner:
+        width *= n
+    if t is None or not hasattr(t, "is_cuda"):
+        return width
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a device tensor")
+    if tuple(t.shape) != (rows, *inner):
+        raise ValueError(f"{name}: expected shape {(rows, *inner)}, got {tuple(t.shape)}")
+    if t.dtype != _torch_dt(code):
+        raise ValueError(f"{name}: expected dtype {_torch_dt(code)}, got {t.dtype}")
+    if rows == 0 or width == 0:
+        return width
+    want = 1
+    for n, s in zip(reversed(inner), reversed(t.stride()[1:])):
+        if n != 1 and s != want:
+            raise ValueError(f"{name}: expected contiguous values inside a row")
+        want *= n
+    if rows == 1:
+        return width
+    if t.stride(0) < width:
+        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)}, width {width})")
+    return t.stride(0)
+
+
+def _expect_index(name, t, numel, dtype):
+    if t is None or not hasattr(t, "is_cuda"):
+        return
+    _expect(name, t, numel)
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+
+
+class _Launch:
+    """Runs a call on the device of its tensors: checks that they share one, makes it the current
+    device for the call, and gives the stream (the device's current one unless one is given)."""
+
+    def __init__(self, stream, tensors):
+        import torch
+        devices = {t.device for t in tensors if t is not None and hasattr(t, "is_cuda")}
+        if len(devices) > 1:
+            raise ValueError(f"tensors on more than one device: {sorted(map(str, devices))}")
+        self.device = devices.pop() if devices else None
+        self.given = stream
+        self.guard = None
+        if self.device is not None and self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream_ptr(self.given)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _expect_conv(conv, x, weight, bias, window_in, window_out, y, rows):
+    ch, n = conv.channels, conv.batch * (conv.width - 1) * conv.channels
+    xs = _expect_rows("x", x, rows, (ch,), conv.io_dtype)
+    ys = _expect_rows("y", y, rows, (ch,), conv.io_dtype)
+    _expect("weight", weight, conv.width * ch, SEED_F32)
+    _expect("bias", bias, ch, SEED_F32)
+    _expect("window_in", window_in, n, conv.io_dtype)
+    _expect("window_out", window_out, n, conv.io_dtype)
+    return xs, ys
+
+
+def seed_prefill_conv(conv: seed_conv, x, offsets, weight, bias, window_out, y, window_in=None, stream=None) -> None:
+    """The short causal convolution of packed prompts: x, y [tokens, channels] (rows may be strided),
+    offsets int32 [batch + 1] on the device, weight float [width, channels], bias float [channels] or
+    None; window_in / window_out [batch, width - 1, channels] hold the inputs before and the last
+    inputs of each sequence (window_in None: zeros)."""
+    import torch
+    tokens = x.shape[0]
+    xs, ys = _expect_conv(conv, x, weight, bias, window_in, window_out, y, tokens)
+    _expect_index("offsets", offsets, conv.batch + 1, torch.int32)
+    with _Launch(stream, (x, offsets, weight, bias, window_in, window_out, y)) as st:
+        _check("seed_prefill_conv", LIB.seed_prefill_conv(
+            ctypes.byref(conv), tokens, _ptr(offsets), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(window_in),
+            _ptr(window_out), _ptr(y), ys, st))
+
+
+def seed_decode_conv(conv: seed_conv, x, weight, bias, window, y, window_out=None, active=None, stream=None) -> None:
+    """The short causal convolution of one token per request: x, y [batch, channels]; window
+    [batch, width - 1, channels] gives the inputs before and moves up by one token, in place or into
+    window_out; active (uint8 [batch] on the device, or None for all) masks requests out."""
+    import torch
+    out = window if window_out is None else window_out
+    xs, ys = _expect_conv(conv, x, weight, bias, window, out, y, conv.batch)
+    _expect_index("active", active, conv.batch, torch.uint8)
+    with _Launch(stream, (x, weight, bias, window, out, active, y)) as st:
+        _check("seed_decode_conv", LIB.seed_decode_conv(
+            ctypes.byref(conv), _ptr(active), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(window), _ptr(out),
+            _ptr(y), ys, st))
+
+
+def seed_prefill_workspace_bytes(shape: seed_shape, prompt: seed_prompt) -> int:
+    return int(LIB.seed_prefill_workspace_bytes(ctypes.byref(shape), ctypes.byref(prompt)))
+
+
+def seed_prefill_scan(shape: seed_shape, offsets, q, k, v, beta, g, S, o, S0=None, ws=None, stream=None) -> None:
+    """The dense recurrence over packed prompts: q, k [tokens, key_heads, d_k], v, o [tokens, heads,
+    d_v] (rows may be strided), beta float [tokens, heads], g float [tokens, heads] (KDA: [tokens,
+    heads, d_k]), offsets int32 [batch + 1] on the device. S [batch, heads, d_k, d_v] receives the
+    states after the last tokens, from S0 (None: zeros; S itself: in place). ws: a workspace of
+    seed_prefill_workspace_bytes bytes; without one, one is taken from torch's allocator when the
+    call needs it."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [tokens, key_heads, d_k], got {tuple(q.shape)}")
+    tokens, kh = q.shape[0], q.shape[1]
+    if kh < 1 or shape.heads % kh != 0:
+        raise ValueError(f"q: {kh} key heads do not divide {shape.heads} heads")
+    qs = _expect_rows("q", q, tokens, (kh, shape.d_k), shape.io_dtype)
+    ks = _expect_rows("k", k, tokens, (kh, shape.d_k), shape.io_dtype)
+    vs = _expect_rows("v", v, tokens, (shape.heads, shape.d_v), shape.io_dtype)
+    os_ = _expect_rows("o", o, tokens, (shape.heads, shape.d_v), shape.io_dtype)
+    n = tokens * shape.heads
+    _expect("beta", beta, n, SEED_F32)
+    _expect("g", g, n * (shape.d_k if shape.kind == SEED_KDA else 1), SEED_F32)
+    _expect("S", S, shape.units * shape.d_k * shape.d_v, SEED_F32)
+    _expect("S0", S0, shape.units * shape.d_k * shape.d_v, SEED_F32)
+    _expect_index("offsets", offsets, shape.batch + 1, torch.int32)
+    prompt = seed_prompt(tokens, offsets.data_ptr(), kh, qs, ks, vs, os_)
+    with _Launch(stream, (offsets, q, k, v, beta, g, S, o, S0, ws)) as st:
+        need = seed_prefill_workspace_bytes(shape, prompt)
+        if ws is None and need > 0:
+            if stream is not None:  # made on the stream that uses it, so that its reuse is ordered behind
+                on = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+                with torch.cuda.stream(on):
+                    ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            else:
+                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+        _check("seed_prefill_scan", LIB.seed_prefill_scan(
+            ctypes.byref(shape), ctypes.byref(prompt), _ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(S0),
+            _ptr(S), _ptr(o), _ptr(ws), ws_bytes, st))
+
+
+def seed_norm_rows(x, weight, y, gate=None, eps: float = 1e-6, gate_first: bool = False, skip=None, skip_scale=None,
+                   total=None, stream=None) -> None:
+    """The head norm of rows x [rows, heads, dim] into y: with x + skip_scale[h] * skip in the place
+    of x when skip is given (written to total, unless None), weight [heads, dim] times u / sqrt(mean
+    u^2 + eps), times silu(gate) after, or u = x silu(gate) when gate_first."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError(f"x: expected [rows, heads, dim], got {tuple(x.shape)}")
+    rows, heads, dim = x.shape
+    code = {torch.float32: SEED_F32, torch.bfloat16: SEED_BF16}.get(x.dtype)
+    if code is None:
+        raise ValueError(f"x: expected dtype float32 or bfloat16, got {x.dtype}")
+    strides = [_expect_rows(n, t, rows, (heads, dim), code)
+               for n, t in (("x", x), ("y", y), ("gate", gate), ("skip", skip), ("total", total))]
+    _expect("weight", weight, heads * dim, SEED_F32)
+    _expect("skip_scale", skip_scale, heads, SEED_F32)
+    shape = seed_rows(rows, heads, dim, code, *strides)
+    norm = seed_head_norm(None if weight is None else weight.data_ptr(), None if gate is None else gate.data_ptr(),
+                          float(eps), int(gate_first))
+    res = seed_residual(*(None if t is None else t.data_ptr() for t in (skip, skip_scale, total)))
+    with _Launch(stream, (x, weight, y, gate, skip, skip_scale, total)) as st:
+        _check("seed_norm_rows", LIB.seed_norm_rows(ctypes.byref(shape), _ptr(x), ctypes.byref(norm),
+                                                    ctypes.byref(res), _ptr(y), st))

@@ -1,0 +1,155 @@
+// Gated scan of packed prompts over dense fp32 states, one token after another:
+//   S_t = G_t S_{t-1} + beta_t k_t (v_t - [delta] (G_t S_{t-1})^T k_t)^T,   o_t = S_t^T q_t
+// (the dense recurrences of GDN, KDA and Mamba-2; picx.dev summary, "Introduction and Theoretical
+// Foundation" and "Exact Update (Lemma 2)").
+//
+// Every column of S follows its own recurrence given q, k, g and beta, so the d_v columns split
+// freely. A wavefront holds 16 columns of one unit's state in registers: lane l has columns
+// 4 (l / 16) .. + 3 and rows (d_k / 16) (l % 16) .. of them, and the two column sums S^T k and S^T q of
+// a token are reduced over 16 lanes with DPP adds. The next kAhead tokens' rows are in flight while
+// one block of them runs. The state is read and written once, whatever the prompt's length.
+#include "common.hpp"
+#include "prompt.hpp"
+
+namespace seed {
+
+namespace {
+
+constexpr int kThreads = 256;      // 4 wavefronts: 64 columns of one unit
+constexpr int kAhead = 4;          // tokens loaded ahead
+constexpr int kCols = 4;           // columns per lane
+
+}  // namespace
+
+template <int KIND, int DK, int DV, int IDT>
+__global__ __launch_bounds__(kThreads) void k_scan_tokens(const ScanArgs A, int64_t units) {
+  using IT = stor_t<IDT>;
+  constexpr int R = DK / 16;       // rows per lane
+  constexpr int SPLIT = DV / 64;   // workgroups per unit
+  constexpr bool DELTA = KIND != SEED_MAMBA2;
+  constexpr bool DIAG = KIND == SEED_KDA;
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int row0 = (lane & 15) * R;
+  for (int64_t item = blockIdx.x; item < units * SPLIT; item += gridDim.x) {
+    const int64_t unit = item / SPLIT;
+    const int col0 = static_cast<int>(item % SPLIT) * 64 + wave * 16 + (lane >> 4) * kCols;
+    const int b = static_cast<int>(unit / A.heads), h = static_cast<int>(unit % A.heads);
+    const int kh = h / (A.heads / A.key_heads);
+    int64_t lo, hi;
+    sequence_rows(A.offsets, b, A.tokens, lo, hi);
+
+    float S[R][kCols];
+    const int64_t sbase = unit * DK * DV + static_cast<int64_t>(row0) * DV + col0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (A.S0 != nullptr) {
+        load_f32<0, kCols>(A.S0 + sbase + i * DV, S[i]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) S[i][c] = 0.f;
+      }
+    }
+
+    const IT* __restrict__ qp = static_cast<const IT*>(A.q) + static_cast<int64_t>(kh) * DK + row0;
+    const IT* __restrict__ kp = static_cast<const IT*>(A.k) + static_cast<int64_t>(kh) * DK + row0;
+    const IT* __restrict__ vp = static_cast<const IT*>(A.v) + static_cast<int64_t>(h) * DV + col0;
+    IT* __restrict__ op = static_cast<IT*>(A.o) + static_cast<int64_t>(h) * DV + col0;
+
+    struct Token {
+      float q[R], k[R], v[kCols], g[DIAG ? R : 1], beta;
+    };
+    Token next[kAhead];
+    // rows past the end load the last row again: never used, always inside the sequence
+    auto fetch = [&](Token& t, int64_t r) {
+      r = r < hi ? r : hi - 1;
+      load_f32<IDT, R>(qp + r * A.q_stride, t.q);
+      load_f32<IDT, R>(kp + r * A.k_stride, t.k);
+      load_f32<IDT, kCols>(vp + r * A.v_stride, t.v);
+      const int64_t at = r * A.heads + h;
+      t.beta = A.beta[at];
+      if constexpr (DIAG) load_f32<0, R>(A.g + at * DK + row0, t.g);
+      else t.g[0] = A.g[at];
+    };
+
+    if (hi > lo) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) fetch(next[a], lo + a);
+    }
+    for (int64_t r0 = lo; r0 < hi; r0 += kAhead) {
+      Token now[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) now[a] = next[a];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) fetch(next[a], r0 + kAhead + a);
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        if (r0 + a >= hi) break;  // the same for the whole wavefront
+        const Token& t = now[a];
+        float sk[kCols] = {}, sq[kCols] = {}, kq = 0.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const float gi = DIAG ? t.g[i] : t.g[0];
+          kq = fmaf(t.k[i], t.q[i], kq);
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            S[i][c] *= gi;
+            if constexpr (DELTA) sk[c] = fmaf(t.k[i], S[i][c], sk[c]);
+            sq[c] = fmaf(t.q[i], S[i][c], sq[c]);
+          }
+        }
+        kq = group_sum<16>(kq);
+        float w[kCols], o[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          sq[c] = group_sum<16>(sq[c]);
+          w[c] = t.v[c];
+          if constexpr (DELTA) w[c] -= group_sum<16>(sk[c]);
+          w[c] *= t.beta;
+          o[c] = fmaf(kq, w[c], sq[c]);
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) S[i][c] = fmaf(t.k[i], w[c], S[i][c]);
+        if ((lane & 15) == 0) store_f32<IDT, kCols>(op + (r0 + a) * A.o_stride, o);
+      }
+    }
+
+#pragma unroll
+    for (int i = 0; i < R; ++i) store_f32<0, kCols>(A.S + sbase + i * DV, S[i]);
+  }
+}
+
+namespace {
+
+using ScanFn = void (*)(const ScanArgs, int64_t);
+
+template <int KIND, int DK, int DV>
+ScanFn pick_io(int io) {
+  return io == SEED_BF16 ? k_scan_tokens<KIND, DK, DV, 1> : k_scan_tokens<KIND, DK, DV, 0>;
+}
+
+template <int KIND>
+ScanFn pick_dims(int dk, int dv, int io) {
+  if (dk == 128) return dv == 128 ? pick_io<KIND, 128, 128>(io) : pick_io<KIND, 128, 64>(io);
+  return dv == 128 ? pick_io<KIND, 64, 128>(io) : pick_io<KIND, 64, 64>(io);
+}
+
+ScanFn pick_scan(const seed_shape& sh) {
+  switch (sh.kind) {
+    case SEED_GDN: return pick_dims<SEED_GDN>(sh.d_k, sh.d_v, sh.io_dtype);
+    case SEED_KDA: return pick_dims<SEED_KDA>(sh.d_k, sh.d_v, sh.io_dtype);
+    default: return pick_dims<SEED_MAMBA2>(sh.d_k, sh.d_v, sh.io_dtype);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_prefill_scan(const seed_shape& sh, const ScanArgs& a, hipStream_t s) {
+  const int64_t units = static_cast<int64_t>(a.batch) * a.heads;
+  hipLaunchKernelGGL(pick_scan(sh), dim3(loop_blocks(units * (sh.d_v / 64))), dim3(kThreads), 0, s, a, units);
+  return hipGetLastError();
+}
+
+}  // namespace seed
