@@ -20,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libseed.so")
 SOURCES = ["api.cpp", "decode.hip", "dense.hip", "compress.hip", "compress_wave.hip", "energy.hip", "chunk.hip",
-           "prompt_api.cpp", "conv.hip", "scan.hip", "norm_rows.hip"]
+           "prompt_api.cpp", "conv.hip", "scan.hip", "scan_chunk.hip", "norm_rows.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -58,6 +58,8 @@ struct NormArgs {
 hipError_t launch_prefill_conv(const seed_conv& c, const ConvArgs& a, hipStream_t s);
 hipError_t launch_decode_conv(const seed_conv& c, const ConvArgs& a, hipStream_t s);
 hipError_t launch_prefill_scan(const seed_shape& sh, const ScanArgs& a, hipStream_t s);
+// The chunked scan on the matrix cores: bf16 io, scalar gates (GDN, Mamba-2).
+hipError_t launch_scan_chunk(const seed_shape& sh, const ScanArgs& a, hipStream_t s);
 hipError_t launch_norm_rows(int32_t io_dtype, const NormArgs& a, hipStream_t s);
 
 // Whether p and a row stride (in elements of `bytes`) let every row be accessed 16 bytes at a time.

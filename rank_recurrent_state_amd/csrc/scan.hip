@@ -147,6 +147,8 @@ ScanFn pick_scan(const seed_shape& sh) {
 }  // namespace
 
 hipError_t launch_prefill_scan(const seed_shape& sh, const ScanArgs& a, hipStream_t s) {
+  if (sh.io_dtype == SEED_BF16 && sh.kind != SEED_KDA && a.tokens >= 16 * static_cast<int64_t>(a.batch))
+    return launch_scan_chunk(sh, a, s);
   const int64_t units = static_cast<int64_t>(a.batch) * a.heads;
   hipLaunchKernelGGL(pick_scan(sh), dim3(loop_blocks(units * (sh.d_v / 64))), dim3(kThreads), 0, s, a, units);
   return hipGetLastError();
