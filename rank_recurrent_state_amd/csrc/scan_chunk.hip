@@ -35,10 +35,10 @@ using bf16x2 = __attribute__((ext_vector_type(2))) __bf16;
 using f32x2 = __attribute__((ext_vector_type(2))) float;
 using f32x4 = __attribute__((ext_vector_type(4))) float;
 using f32x16 = __attribute__((ext_vector_type(16))) float;
+using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
 using s16x4 = __attribute__((ext_vector_type(4))) short;
 
 constexpr int C = 32;       // tokens per chunk
-constexpr int kPad = 8;     // bf16 row padding: rows 16 bytes apart in the banks
 constexpr int LT = C + 8;   // row length of the T and P pieces
 constexpr int LF = C + 4;   // row length of the fp32 L and T
 
@@ -79,20 +79,72 @@ __device__ __forceinline__ s16x4 read_tr(const uint16_t* p) {
       (__attribute__((address_space(3))) s16x4*)(const_cast<uint16_t*>(p)));
 }
 
+// Rows c0 .. hi - 1 of a row buffer as a bounds-checked buffer: loads behind the last row's `width`
+// bytes return zeros. Offsets inside a chunk stay below 2^31 (kChunkStride).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const uint16_t* base, int64_t stride, int64_t c0, int64_t hi,
+                                                             int width) {
+  const int n = static_cast<int>(hi - c0 < C ? hi - c0 : C);
+  const int bytes = n > 0 ? static_cast<int>((n - 1) * stride * 2) + width : 0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + c0 * stride), 0, bytes, 0x00027000);
+}
+
+// 16 bytes per lane from memory straight to LDS, lane l's at lds + 16 l; lanes outside the buffer
+// write zeros. lds is the same for the whole wavefront. The compiler does not see the write: it is
+// waited for with wait_loads before the barrier in front of the tile's first use.
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rows, int voffset, int soffset, const uint16_t* lds) {
+  const uint32_t to = __builtin_amdgcn_readfirstlane(
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint16_t*)lds)));
+  uint32_t m0;  // M0 holds the LDS address; what it held is put back
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %2, %3, %4 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(to), "v"(voffset), "s"(rows), "s"(soffset)
+      : "memory");
+}
+// Waits until at most N of the wavefront's memory operations, the youngest, are under way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// A copy of x that the compiler takes for a new value.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// A tile of C rows of D bf16 values as the loads to LDS lay it out: rows back to back, the 16-byte
+// pieces of row r exchanged by an XOR with swz(r). 16 consecutive rows (in any order) then read one
+// piece each from 16 different bank groups, and the 4 rows of a transposing read keep apart.
+template <int D>
+struct Tile {
+  static constexpr int PIECES = D / 8;
+  uint16_t x[C * D];
+  static __device__ __forceinline__ int swz(int r) {
+    return D == 128 ? (2 * (r & 7) + ((r >> 3) & 1)) : (2 * ((r >> 1) & 3) + ((r >> 3) & 1));
+  }
+  // element (r, c), and the 8 that start there when c is a multiple of 8
+  __device__ __forceinline__ uint16_t* at(int r, int c) { return x + r * D + ((((c >> 3) ^ swz(r)) << 3) | (c & 7)); }
+};
+
 template <int KIND, int DK, int DV>
 struct Tiles {
   static constexpr bool DELTA = KIND != SEED_MAMBA2;
-  static constexpr int LK = DK + kPad, LV = DV + kPad;
-  uint16_t K[C * LK];
-  uint16_t Q[C * LK];
-  uint16_t V[C * LV];             // v, then o
+  Tile<DK> K[2], Q[2];            // by the chunk's parity: the next chunk's rows arrive during this one
+  Tile<DV> V[2];                  // v, then o
   uint16_t P[2][C * LT];
   uint16_t T[DELTA ? 3 : 1][DELTA ? C * LT : 8];
   float L[DELTA ? C * LF : 4];
   float Tf[DELTA ? C * LF : 4];
-  float ch[C], cl[C];             // c as a sum of two floats
-  float head[C], tail[C];         // 2^c_t, 2^(c_end - c_t)
-  float beta[C], g[C];
+  struct Gates {
+    float ch[C], cl[C];           // c as a sum of two floats
+    float head[C], tail[C];       // 2^c_t, 2^(c_end - c_t)
+    float beta[C], g[C];
+  } gates[2];
 };
 
 }  // namespace
@@ -102,15 +154,14 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
   using TL = Tiles<KIND, DK, DV>;
   constexpr bool DELTA = TL::DELTA;
   constexpr int NW = DV / 32, NT = NW * 64;
-  constexpr int LK = TL::LK, LV = TL::LV;
   constexpr int RT = DK / 32;                 // row tiles of the state
   constexpr int KP = C * DK / 8 / NT;         // 16-byte pieces of K (and Q) per thread
   constexpr int VP = C * DV / 8 / NT;
+  constexpr int KR = C / KP, VR = C / VP;     // rows that one piece of every thread covers
   __shared__ TL sh;
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int l32 = lane & 31, half = lane >> 5;
-  const int prow = perm(l32);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half0 = (threadIdx.x & 63) >> 5;
 
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int b = static_cast<int>(unit / A.heads), h = static_cast<int>(unit % A.heads);
@@ -125,58 +176,64 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
 
     // the state: register i of row tile r is row 32 r + 16 (i / 8) + 8 half + i % 8, column 32 wave + l32
     f32x16 S[RT];
-    const int64_t sbase = unit * DK * DV + static_cast<int64_t>(8 * half) * DV + 32 * wave + l32;
+    constexpr int SB = DK * DV * 4;
+    const int s_at = (8 * half0 * DV + 32 * wave + (threadIdx.x & 31)) * 4;
+    if (A.S0 != nullptr) {
+      const auto sr = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(A.S0 + unit * DK * DV), 0, SB, 0x00027000);
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        S[r][i] = A.S0 != nullptr ? A.S0[sbase + (32 * r + 16 * (i / 8) + i % 8) * DV] : 0.f;
+        for (int i = 0; i < 16; ++i)
+          S[r][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sr, s_at, (32 * r + 16 * (i / 8) + i % 8) * DV * 4, 0));
+    } else {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) S[r] = f32x16{};
+    }
 
-    // the next chunk's rows, on their way from memory; rows past the end read as zeros, g as 1
-    uint4 nk[KP], nq[KP], nv[VP];
+    // The next chunk's rows go straight to LDS; rows past the end arrive as zeros, g as 1. A thread
+    // loads the 16 bytes at place (thread) of every KR (VR) rows, that is piece place ^ swz(row).
     float ng = 1.f, nb = 0.f;
-    auto fetch = [&](int64_t c0) {
-      const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto fetch = [&](int64_t f0, int to) {
+      const int tid = fresh(threadIdx.x);
+      const int krow = tid / (DK / 8), vrow = tid / (DV / 8);
+      const auto kr = chunk_rows(kp, A.k_stride, f0, hi, DK * 2), qr = chunk_rows(qp, A.q_stride, f0, hi, DK * 2);
+      const auto vr = chunk_rows(vp, A.v_stride, f0, hi, DV * 2);
 #pragma unroll
       for (int p = 0; p < KP; ++p) {
-        const int at = p * NT + threadIdx.x, row = at / (DK / 8), col = at % (DK / 8) * 8;
-        const bool in = c0 + row < hi;
-        const int64_t rr = in ? c0 + row : hi - 1;
-        const uint4 x = *reinterpret_cast<const uint4*>(kp + rr * A.k_stride + col);
-        const uint4 y = *reinterpret_cast<const uint4*>(qp + rr * A.q_stride + col);
-        nk[p] = in ? x : zero;
-        nq[p] = in ? y : zero;
+        const int row = krow + p * KR, piece = (tid % (DK / 8)) ^ Tile<DK>::swz(row);
+        const int lds = (p * NT + wave * 64) * 8;
+        load_lds(kr, (krow * static_cast<int>(A.k_stride) + 8 * piece) * 2, p * KR * static_cast<int>(A.k_stride) * 2, sh.K[to].x + lds);
+        load_lds(qr, (krow * static_cast<int>(A.q_stride) + 8 * piece) * 2, p * KR * static_cast<int>(A.q_stride) * 2, sh.Q[to].x + lds);
       }
 #pragma unroll
       for (int p = 0; p < VP; ++p) {
-        const int at = p * NT + threadIdx.x, row = at / (DV / 8), col = at % (DV / 8) * 8;
-        const bool in = c0 + row < hi;
-        const int64_t rr = in ? c0 + row : hi - 1;
-        const uint4 x = *reinterpret_cast<const uint4*>(vp + rr * A.v_stride + col);
-        nv[p] = in ? x : zero;
+        const int row = vrow + p * VR, piece = (tid % (DV / 8)) ^ Tile<DV>::swz(row);
+        load_lds(vr, (vrow * static_cast<int>(A.v_stride) + 8 * piece) * 2, p * VR * static_cast<int>(A.v_stride) * 2,
+                 sh.V[to].x + (p * NT + wave * 64) * 8);
       }
       if (wave == NW - 1) {
-        const bool in = c0 + l32 < hi;
-        const int64_t at = (in ? c0 + l32 : hi - 1) * A.heads + h;
+        const int64_t f1 = f0 + (threadIdx.x & 31);
+        const bool in = f1 < hi;
+        const int64_t at = (in ? f1 : hi - 1) * A.heads + h;
         ng = in ? A.g[at] : 1.f;
         nb = in ? A.beta[at] : 0.f;
       }
     };
-    if (lo < hi) fetch(lo);
+    int now = 0;
+    __syncthreads();  // the last unit's tiles have been read
+    if (lo < hi) fetch(lo, 0);
 
-    for (int64_t c0 = lo; c0 < hi; c0 += C) {
-      // ---- the chunk into LDS, and its gates -------------------------------------------------------
-#pragma unroll
-      for (int p = 0; p < KP; ++p) {
-        const int at = p * NT + threadIdx.x, row = at / (DK / 8), col = at % (DK / 8) * 8;
-        *reinterpret_cast<uint4*>(sh.K + row * LK + col) = nk[p];
-        *reinterpret_cast<uint4*>(sh.Q + row * LK + col) = nq[p];
-      }
-#pragma unroll
-      for (int p = 0; p < VP; ++p) {
-        const int at = p * NT + threadIdx.x, row = at / (DV / 8), col = at % (DV / 8) * 8;
-        *reinterpret_cast<uint4*>(sh.V + row * LV + col) = nv[p];
-      }
+    for (int64_t c0 = lo; c0 < hi; c0 += C, now ^= 1) {
+      // lane numbers that the compiler takes for new ones in every chunk, so that the addresses made
+      // of them cost an instruction each instead of a register each
+      const int lane = fresh(threadIdx.x & 63);
+      const int l32 = lane & 31, half = lane >> 5;
+      const int prow = perm(l32);
+      auto& K = sh.K[now];
+      auto& Q = sh.Q[now];
+      auto& V = sh.V[now];
+      auto& G = sh.gates[now];
+      // ---- the chunk's gates -------------------------------------------------------------------------
       if (wave == NW - 1) {
         // g = 0 counts as 2^-200: across it every weight underflows to 0, as it should
         const float lg = log2f(ng);
@@ -191,32 +248,35 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
         const float rh = static_cast<float>(rest), rl = static_cast<float>(rest - static_cast<double>(rh));
         const float eh = exp2f(hi32), et = exp2f(rh);
         if (lane < C) {
-          sh.ch[lane] = hi32;
-          sh.cl[lane] = lo32;
-          sh.head[lane] = fmaf(eh, 0.693147181f * lo32, eh);
-          sh.tail[lane] = fmaf(et, 0.693147181f * rl, et);
-          sh.beta[lane] = nb;
-          sh.g[lane] = ng;
+          G.ch[lane] = hi32;
+          G.cl[lane] = lo32;
+          G.head[lane] = fmaf(eh, 0.693147181f * lo32, eh);
+          G.tail[lane] = fmaf(et, 0.693147181f * rl, et);
+          G.beta[lane] = nb;
+          G.g[lane] = ng;
         }
       }
+      // the chunk's rows are here: everything older than the last chunk's two read-out stores
+      if (c0 == lo) wait_loads<0>();
+      else wait_loads<2>();
       __syncthreads();
-      if (c0 + C < hi) fetch(c0 + C);
+      if (c0 + C < hi) fetch(c0 + C, now ^ 1);
 
       // ---- P, and T by another wavefront ------------------------------------------------------------
       // 2^(c_t - c_s) for t = l32 and the 16 s of the lane's accumulator registers
       auto weights = [&](float (&e)[16]) {
-        const float th = sh.ch[l32], tl = sh.cl[l32];
+        const float th = G.ch[l32], tl = G.cl[l32];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int s = 16 * (i / 8) + 8 * half + i % 8;
-          e[i] = __builtin_amdgcn_exp2f((th - sh.ch[s]) + (tl - sh.cl[s]));
+          e[i] = __builtin_amdgcn_exp2f((th - G.ch[s]) + (tl - G.cl[s]));
         }
       };
       if (wave == NW - 1) {
         f32x16 acc = {};
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks)
-          acc = mma(frag(sh.K + prow * LK + 16 * ks + 8 * half), frag(sh.Q + l32 * LK + 16 * ks + 8 * half), acc);
+          acc = mma(frag(K.at(prow, 16 * ks + 8 * half)), frag(Q.at(l32, 16 * ks + 8 * half)), acc);
         float e[16];
         weights(e);
 #pragma unroll
@@ -226,7 +286,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
           for (int j = 0; j < 8; ++j) {
             const int s = 16 * s8 + 8 * half + j;
             float w = acc[8 * s8 + j] * e[8 * s8 + j];
-            if constexpr (!DELTA) w *= sh.beta[s];
+            if constexpr (!DELTA) w *= G.beta[s];
             x[j] = s <= l32 ? w : 0.f;
           }
           bf16x8 pc[2];
@@ -235,16 +295,17 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
           for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(sh.P[n] + l32 * LT + 16 * s8 + 8 * half) = pc[n];
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
       if constexpr (DELTA) {
         if (wave == 0) {
           f32x16 acc = {};
 #pragma unroll
           for (int ks = 0; ks < DK / 16; ++ks)
-            acc = mma(frag(sh.K + prow * LK + 16 * ks + 8 * half), frag(sh.K + l32 * LK + 16 * ks + 8 * half), acc);
+            acc = mma(frag(K.at(prow, 16 * ks + 8 * half)), frag(K.at(l32, 16 * ks + 8 * half)), acc);
           float e[16];
           weights(e);
-          const float bt = sh.beta[l32];
-#pragma unroll
+          const float bt = G.beta[l32];
+  #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int s = 16 * (i / 8) + 8 * half + i % 8;
             e[i] = s < l32 ? bt * (acc[i] * e[i]) : 0.f;
@@ -263,6 +324,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
 #pragma unroll
             for (int s = 0; s < t; ++s) a0 = fmaf(-sh.L[(blk + t) * LF + blk + s], x[s], a0);
             x[t] = a0;
+            if (t % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // a few rows of L in registers at a time
           }
           if (lane < C) {
 #pragma unroll
@@ -291,7 +353,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
             const int col = 16 * s8 + 8 * half;
             float y[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = col + j <= l32 ? sh.Tf[l32 * LF + col + j] * sh.beta[col + j] : 0.f;
+            for (int j = 0; j < 8; ++j) y[j] = col + j <= l32 ? sh.Tf[l32 * LF + col + j] * G.beta[col + j] : 0.f;
             bf16x8 pc[3];
             split<3>(y, pc);
 #pragma unroll
@@ -300,6 +362,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
         }
       }
 
+      __builtin_amdgcn_sched_barrier(0);
       // ---- K S and Q S ------------------------------------------------------------------------------
       f32x16 ks = {}, qs = {};
 #pragma unroll
@@ -310,11 +373,11 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = S[r][8 * s + j];
           const int col = 32 * r + 16 * s + 8 * half;
-          const bf16x8 aq = frag(sh.Q + prow * LK + col);
+          const bf16x8 aq = frag(Q.at(prow, col));
           if constexpr (DELTA) {
             bf16x8 pc[3];
             split<3>(x, pc);
-            const bf16x8 ak = frag(sh.K + prow * LK + col);
+            const bf16x8 ak = frag(K.at(prow, col));
             ks = mma(ak, pc[2], ks);
             qs = mma(aq, pc[1], qs);
             ks = mma(ak, pc[1], ks);
@@ -326,13 +389,14 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
             qs = mma(aq, pc[1], qs);
             qs = mma(aq, pc[0], qs);
           }
+          if (s == 1) __builtin_amdgcn_sched_barrier(0);
         }
       // v in accumulator layout, and as the bf16 right operand it already is
       bf16x8 vb[2];
-      const uint16_t* vt = sh.V + (8 * half + (lane & 15) / 4) * LV + 32 * wave + (lane & 16) + 4 * (lane & 3);
+      const int vr4 = 8 * half + (lane & 15) / 4, vc4 = 32 * wave + (lane & 16) + 4 * (lane & 3);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const s16x4 x0 = read_tr(vt + 16 * s * LV), x1 = read_tr(vt + (16 * s + 4) * LV);
+        const s16x4 x0 = read_tr(V.at(vr4 + 16 * s, vc4)), x1 = read_tr(V.at(vr4 + 16 * s + 4, vc4));
         const __attribute__((ext_vector_type(8))) short x = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
         vb[s] = __builtin_bit_cast(bf16x8, x);
       }
@@ -342,7 +406,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
       f32x16 w;
       float hd[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) hd[i] = sh.head[16 * (i / 8) + 8 * half + i % 8];
+      for (int i = 0; i < 16; ++i) hd[i] = G.head[16 * (i / 8) + 8 * half + i % 8];
       if constexpr (DELTA) {
         w = f32x16{};
 #pragma unroll
@@ -363,7 +427,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = static_cast<float>(vb[i / 8][i % 8]) * sh.beta[16 * (i / 8) + 8 * half + i % 8];
+        for (int i = 0; i < 16; ++i) w[i] = static_cast<float>(vb[i / 8][i % 8]) * G.beta[16 * (i / 8) + 8 * half + i % 8];
       }
 
       // A value that is not finite would reach the tokens before its own through the zeros of T and P:
@@ -375,32 +439,41 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
         const int n = static_cast<int>(hi - c0 < C ? hi - c0 : C);
 #pragma unroll 1
         for (int t = 0; t < n; ++t) {
-          const float gt = sh.g[t];
+          const float gt = G.g[t];
           float sk = 0.f, sq = 0.f, kq = 0.f;
 #pragma unroll
           for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int col = 32 * r + 16 * (i / 8) + 8 * half + i % 8;
-              const float kv = bf16_to_f32(sh.K[t * LK + col]), qv = bf16_to_f32(sh.Q[t * LK + col]);
-              S[r][i] *= gt;
-              sk = fmaf(kv, S[r][i], sk);
-              sq = fmaf(qv, S[r][i], sq);
-              kq = fmaf(kv, qv, kq);
+            for (int s8 = 0; s8 < 2; ++s8) {
+              const int col = 32 * r + 16 * s8 + 8 * half;
+              const bf16x8 kv = frag(K.at(t, col)), qv = frag(Q.at(t, col));
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float kf = static_cast<float>(kv[j]), qf = static_cast<float>(qv[j]);
+                S[r][8 * s8 + j] *= gt;
+                sk = fmaf(kf, S[r][8 * s8 + j], sk);
+                sq = fmaf(qf, S[r][8 * s8 + j], sq);
+                kq = fmaf(kf, qf, kq);
+              }
+              __builtin_amdgcn_sched_barrier(0);  // one piece of k and q in registers at a time
             }
           sk += __shfl_xor(sk, 32, 64);
           sq += __shfl_xor(sq, 32, 64);
           kq += __shfl_xor(kq, 32, 64);
-          float x = bf16_to_f32(sh.V[t * LV + 32 * wave + l32]);
+          float x = bf16_to_f32(*V.at(t, 32 * wave + l32));
           if constexpr (DELTA) x -= sk;
-          x *= sh.beta[t];
+          x *= G.beta[t];
 #pragma unroll
           for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              S[r][i] = fmaf(bf16_to_f32(sh.K[t * LK + 32 * r + 16 * (i / 8) + 8 * half + i % 8]), x, S[r][i]);
+            for (int s8 = 0; s8 < 2; ++s8) {
+              const bf16x8 kv = frag(K.at(t, 32 * r + 16 * s8 + 8 * half));
+#pragma unroll
+              for (int j = 0; j < 8; ++j) S[r][8 * s8 + j] = fmaf(static_cast<float>(kv[j]), x, S[r][8 * s8 + j]);
+              __builtin_amdgcn_sched_barrier(0);
+            }
           wave_lds_sync();  // both halves have read v
-          if (half == 0) sh.V[t * LV + 32 * wave + l32] = f32_to_bf16(fmaf(kq, x, sq));
+          if (half == 0) *V.at(t, 32 * wave + l32) = f32_to_bf16(fmaf(kq, x, sq));
         }
       } else {
         // ---- O = H Q S + P W --------------------------------------------------------------------------
@@ -425,23 +498,23 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
           }
         }
         // ---- S = 2^(c_end) S + K^T diag(tail) W ----------------------------------------------------------
-        const float ge = sh.head[C - 1];
+        const float ge = G.head[C - 1];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
           for (int i = 0; i < 16; ++i) S[r][i] *= ge;
         // lane i of 16 passes row i / 4 of 4 tokens and the channels that perm puts at 4 (i % 4)
-        const uint16_t* kt = sh.K + (8 * half + (lane & 15) / 4) * LK + perm(4 * (lane & 3)) + (lane & 16);
+        const int kr4 = 8 * half + (lane & 15) / 4, kc4 = perm(4 * (lane & 3)) + (lane & 16);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           float x[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = w[8 * s + j] * sh.tail[16 * s + 8 * half + j];
+          for (int j = 0; j < 8; ++j) x[j] = w[8 * s + j] * G.tail[16 * s + 8 * half + j];
           bf16x8 wp[3];
           split<3>(x, wp);
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
-            const s16x4 x0 = read_tr(kt + 16 * s * LK + 32 * r), x1 = read_tr(kt + (16 * s + 4) * LK + 32 * r);
+            const s16x4 x0 = read_tr(K.at(kr4 + 16 * s, kc4 + 32 * r)), x1 = read_tr(K.at(kr4 + 16 * s + 4, kc4 + 32 * r));
             const __attribute__((ext_vector_type(8))) short y = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
             const bf16x8 a = __builtin_bit_cast(bf16x8, y);
             S[r] = mma(a, wp[2], S[r]);
@@ -451,23 +524,25 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          sh.V[(16 * (i / 8) + 8 * half + i % 8) * LV + 32 * wave + l32] = f32_to_bf16(o[i]);
+          *V.at(16 * (i / 8) + 8 * half + i % 8, 32 * wave + l32) = f32_to_bf16(o[i]);
       }
       // ---- the read-outs: a wavefront's 32 columns of a row are 64 bytes, 16 per lane ----------------
       wave_lds_sync();
+      const auto orow = chunk_rows(op, A.o_stride, c0, hi, DV * 2);  // stores behind the last row are dropped
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const int row = 16 * p + lane / 4, col = 32 * wave + 8 * (lane & 3);
-        if (c0 + row < hi)
-          *reinterpret_cast<uint4*>(op + (c0 + row) * A.o_stride + col) = *reinterpret_cast<const uint4*>(sh.V + row * LV + col);
+        const int o_at = (lane / 4 * static_cast<int>(A.o_stride) + 32 * wave + 8 * (lane & 3)) * 2;
+        const u32x4 x = *reinterpret_cast<const u32x4*>(V.at(16 * p + lane / 4, 32 * wave + 8 * (lane & 3)));
+        __builtin_amdgcn_raw_buffer_store_b128(x, orow, o_at, p * 16 * static_cast<int>(A.o_stride) * 2, 0);
       }
-      __syncthreads();
     }
 
+    const auto sr = __builtin_amdgcn_make_buffer_rsrc(A.S + unit * DK * DV, 0, SB, 0x00027000);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) A.S[sbase + (32 * r + 16 * (i / 8) + i % 8) * DV] = S[r][i];
+      for (int i = 0; i < 16; ++i)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[r][i]), sr, s_at, (32 * r + 16 * (i / 8) + i % 8) * DV * 4, 0);
   }
 }
 
