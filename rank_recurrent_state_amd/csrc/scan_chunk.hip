@@ -40,7 +40,7 @@ using s16x4 = __attribute__((ext_vector_type(4))) short;
 
 constexpr int C = 32;       // tokens per chunk
 constexpr int LT = C + 8;   // row length of the T and P pieces
-constexpr int LF = C + 4;   // row length of the fp32 L and T
+constexpr int LF = 16 + 4;  // row length of the fp32 block of T
 
 // Row m of a 32-row operand tile holds token or channel perm(m), which puts 8 consecutive ones into
 // a lane's accumulator registers 0..7 and 8..15: register i of lane half h is 16 (i / 8) + 8 h + i % 8.
@@ -111,6 +111,32 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// By value: a conditional between two elements of an array would put the array in memory.
+__device__ __forceinline__ float pick(bool c, float a, float b) { return c ? a : b; }
+
+// Lane N of the lane's 16, to all of them.
+template <int N>
+__device__ __forceinline__ float bcast16(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x150 + N, 0xF, 0xF, true));
+}
+
+// x = (I + L)^-1 e_j for a 16 x 16 strictly lower L: lane i of 16 holds row i of L and gets column i of
+// the inverse. Step S takes x[S], final by then, out of the rows below.
+template <int S, int R>
+__device__ __forceinline__ void solve_row(const float (&L)[16], float (&x)[16]) {
+  if constexpr (R < 16) {
+    x[R] = fmaf(-bcast16<R>(L[S]), x[S], x[R]);
+    solve_row<S, R + 1>(L, x);
+  }
+}
+template <int S = 0>
+__device__ __forceinline__ void solve16(const float (&L)[16], float (&x)[16]) {
+  if constexpr (S < 15) {
+    solve_row<S, S + 1>(L, x);
+    solve16<S + 1>(L, x);
+  }
+}
+
 // A copy of x that the compiler takes for a new value.
 __device__ __forceinline__ int fresh(int x) {
   asm volatile("" : "+v"(x));
@@ -138,8 +164,7 @@ struct Tiles {
   Tile<DV> V[2];                  // v, then o
   uint16_t P[2][C * LT];
   uint16_t T[DELTA ? 3 : 1][DELTA ? C * LT : 8];
-  float L[DELTA ? C * LF : 4];
-  float Tf[DELTA ? C * LF : 4];
+  float T11[DELTA ? 16 * LF : 4]; // column-major: the lower diagonal block of T
   struct Gates {
     float ch[C], cl[C];           // c as a sum of two floats
     float head[C], tail[C];       // 2^c_t, 2^(c_end - c_t)
@@ -157,6 +182,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
   constexpr int RT = DK / 32;                 // row tiles of the state
   constexpr int KP = C * DK / 8 / NT;         // 16-byte pieces of K (and Q) per thread
   constexpr int VP = C * DV / 8 / NT;
+  constexpr int GW = NW == 4 ? 1 : (DELTA ? 1 : 0);  // forms the gates; wavefront 0 forms T, the last one P
   constexpr int KR = C / KP, VR = C / VP;     // rows that one piece of every thread covers
   __shared__ TL sh;
 
@@ -192,7 +218,6 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
 
     // The next chunk's rows go straight to LDS; rows past the end arrive as zeros, g as 1. A thread
     // loads the 16 bytes at place (thread) of every KR (VR) rows, that is piece place ^ swz(row).
-    float ng = 1.f, nb = 0.f;
     auto fetch = [&](int64_t f0, int to) {
       const int tid = fresh(threadIdx.x);
       const int krow = tid / (DK / 8), vrow = tid / (DV / 8);
@@ -211,17 +236,52 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
         load_lds(vr, (vrow * static_cast<int>(A.v_stride) + 8 * piece) * 2, p * VR * static_cast<int>(A.v_stride) * 2,
                  sh.V[to].x + (p * NT + wave * 64) * 8);
       }
-      if (wave == NW - 1) {
-        const int64_t f1 = f0 + (threadIdx.x & 31);
-        const bool in = f1 < hi;
-        const int64_t at = (in ? f1 : hi - 1) * A.heads + h;
-        ng = in ? A.g[at] : 1.f;
-        nb = in ? A.beta[at] : 0.f;
+    };
+    // The gates of the chunk at f0, by one wavefront: loads early, sums and exponentials late.
+    float ng = 1.f, nb = 0.f;
+    auto load_gates = [&](int64_t f0) {
+      const int64_t f1 = f0 + (threadIdx.x & 31);
+      const int64_t at = (f1 < hi ? f1 : hi - 1) * A.heads + h;
+      const float g1 = A.g[at], b1 = A.beta[at];
+      ng = f1 < hi ? g1 : 1.f;
+      nb = f1 < hi ? b1 : 0.f;
+    };
+    auto sum_gates = [&](typename TL::Gates& G) {
+      const int l = fresh(threadIdx.x & 63), l32 = l & 31;
+      // g = 0 counts as 2^-200: across it every weight underflows to 0, as it should
+      const float lg = log2f(ng);
+      double c = lg < -200.f ? -200.0 : static_cast<double>(lg);
+#pragma unroll
+      for (int d = 1; d < C; d <<= 1) {
+        const double up = __shfl_up(c, d, C);
+        if (l32 >= d) c += up;
+      }
+      const float ch = static_cast<float>(c), cl = static_cast<float>(c - static_cast<double>(ch));
+      const double rest = __shfl(c, C - 1, C) - c;
+      const float rh = static_cast<float>(rest), rl = static_cast<float>(rest - static_cast<double>(rh));
+      const float eh = exp2f(ch), et = exp2f(rh);
+      if (l < C) {
+        G.ch[l] = ch;
+        G.cl[l] = cl;
+        G.head[l] = fmaf(eh, 0.693147181f * cl, eh);
+        G.tail[l] = fmaf(et, 0.693147181f * rl, et);
+        G.beta[l] = nb;
+        G.g[l] = ng;
       }
     };
     int now = 0;
     __syncthreads();  // the last unit's tiles have been read
-    if (lo < hi) fetch(lo, 0);
+    if (lo < hi) {
+      fetch(lo, 0);
+      if (wave == GW) {
+        load_gates(lo);
+        sum_gates(sh.gates[0]);
+      }
+    }
+    if constexpr (DELTA) {  // the block of T above the diagonal
+      for (int i = threadIdx.x; i < 3 * 16; i += NT)
+        for (int j = 0; j < 16; ++j) sh.T[i / 16][(i % 16) * LT + 16 + j] = 0;
+    }
 
     for (int64_t c0 = lo; c0 < hi; c0 += C, now ^= 1) {
       // lane numbers that the compiler takes for new ones in every chunk, so that the addresses made
@@ -233,34 +293,14 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
       auto& Q = sh.Q[now];
       auto& V = sh.V[now];
       auto& G = sh.gates[now];
-      // ---- the chunk's gates -------------------------------------------------------------------------
-      if (wave == NW - 1) {
-        // g = 0 counts as 2^-200: across it every weight underflows to 0, as it should
-        const float lg = log2f(ng);
-        double c = lg < -200.f ? -200.0 : static_cast<double>(lg);
-#pragma unroll
-        for (int d = 1; d < C; d <<= 1) {
-          const double up = __shfl_up(c, d, C);
-          if (l32 >= d) c += up;
-        }
-        const float hi32 = static_cast<float>(c), lo32 = static_cast<float>(c - static_cast<double>(hi32));
-        const double rest = __shfl(c, C - 1, C) - c;
-        const float rh = static_cast<float>(rest), rl = static_cast<float>(rest - static_cast<double>(rh));
-        const float eh = exp2f(hi32), et = exp2f(rh);
-        if (lane < C) {
-          G.ch[lane] = hi32;
-          G.cl[lane] = lo32;
-          G.head[lane] = fmaf(eh, 0.693147181f * lo32, eh);
-          G.tail[lane] = fmaf(et, 0.693147181f * rl, et);
-          G.beta[lane] = nb;
-          G.g[lane] = ng;
-        }
-      }
       // the chunk's rows are here: everything older than the last chunk's two read-out stores
       if (c0 == lo) wait_loads<0>();
       else wait_loads<2>();
       __syncthreads();
-      if (c0 + C < hi) fetch(c0 + C, now ^ 1);
+      if (c0 + C < hi) {
+        fetch(c0 + C, now ^ 1);
+        if (wave == GW) load_gates(c0 + C);
+      }
 
       // ---- P, and T by another wavefront ------------------------------------------------------------
       // 2^(c_t - c_s) for t = l32 and the 16 s of the lane's accumulator registers
@@ -305,59 +345,66 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
           float e[16];
           weights(e);
           const float bt = G.beta[l32];
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int s = 16 * (i / 8) + 8 * half + i % 8;
             e[i] = s < l32 ? bt * (acc[i] * e[i]) : 0.f;
           }
+          // row l32 of its diagonal block, from both halves of the wavefront
+          float Lr[16], x[16];
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(sh.L + l32 * LF + 16 * (i / 8) + 8 * half + i % 8) =
-                make_float4(e[i], e[i + 1], e[i + 2], e[i + 3]);
-          wave_lds_sync();
-          // the two diagonal blocks: lane l32 solves for column l32 % 16 of block l32 / 16
-          const int blk = l32 & 16, jj = l32 & 15;
-          float x[16];
-#pragma unroll
-          for (int t = 0; t < 16; ++t) {
-            float a0 = t == jj ? 1.f : 0.f;
-#pragma unroll
-            for (int s = 0; s < t; ++s) a0 = fmaf(-sh.L[(blk + t) * LF + blk + s], x[s], a0);
-            x[t] = a0;
-            if (t % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // a few rows of L in registers at a time
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t z = __float_as_uint(pick(l32 & 16, e[8 + j], e[j]));
+            const auto r = __builtin_amdgcn_permlane32_swap(z, z, false, false);
+            Lr[j] = __uint_as_float(r[0]);
+            Lr[8 + j] = __uint_as_float(r[1]);
           }
-          if (lane < C) {
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-              sh.Tf[(blk + t) * LF + blk + jj] = x[t];
-              if (blk) sh.Tf[t * LF + 16 + jj] = 0.f;
-            }
-          }
-          wave_lds_sync();
-          // the block below: -T11 (L10 T00), fp32 matrix instructions (k slot lane / 16 of step i is 4 (lane / 16) + i)
+          for (int t = 0; t < 16; ++t) x[t] = t == (l32 & 15) ? 1.f : 0.f;
+          solve16(Lr, x);  // both halves: lane l32 has column l32 % 16 of block l32 / 16
+          // the block below the diagonal: -T11 (L10 T00) in fp32 matrix instructions, whose k slot lane / 16
+          // of step i is taken as 4 (lane / 16) + i
           const int r16 = lane & 15, g4 = lane >> 4;
+          if (l32 & 16) {
+#pragma unroll
+            for (int t = 0; t < 16; t += 4)
+              *reinterpret_cast<f32x4*>(sh.T11 + r16 * LF + t) = f32x4{x[t], x[t + 1], x[t + 2], x[t + 3]};
+          }
           f32x4 m1 = {}, m2 = {};
-          const f32x4 a1 = *reinterpret_cast<const f32x4*>(sh.L + (16 + r16) * LF + 4 * g4);
-          const f32x4 a2 = *reinterpret_cast<const f32x4*>(sh.Tf + (16 + r16) * LF + 16 + 4 * g4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a0 = e[i], a1 = e[4 + i];  // L10[r16][8 half + i], [8 half + 4 + i] in the odd rows of lanes
+            lane_swap16(a0, a1);             // a1: L10[r16][4 g4 + i]
+            float b0 = pick(half, x[8 + i], x[i]), b1 = pick(half, x[12 + i], x[4 + i]);
+            lane_swap16(b0, b1);             // b0: T00[4 g4 + i][r16]
+            m1 = __builtin_amdgcn_mfma_f32_16x16x4f32(a1, b0, m1, 0, 0, 0);
+          }
+          wave_lds_sync();
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            m1 = __builtin_amdgcn_mfma_f32_16x16x4f32(a1[i], sh.Tf[(4 * g4 + i) * LF + r16], m1, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m2 = __builtin_amdgcn_mfma_f32_16x16x4f32(a2[i], m1[i], m2, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sh.Tf[(16 + 4 * g4 + i) * LF + r16] = -m2[i];
-          wave_lds_sync();
-          // T diag(beta) in pieces
-#pragma unroll
-          for (int s8 = 0; s8 < 2; ++s8) {
-            const int col = 16 * s8 + 8 * half;
+            m2 = __builtin_amdgcn_mfma_f32_16x16x4f32(sh.T11[(4 * g4 + i) * LF + r16], m1[i], m2, 0, 0, 0);
+          // T diag(beta) in pieces: each half writes 8 rows of the diagonal blocks' columns, then the block below
+          {
+            const int blk = l32 & 16;
             float y[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = col + j <= l32 ? sh.Tf[l32 * LF + col + j] * G.beta[col + j] : 0.f;
+            for (int j = 0; j < 8; ++j) y[j] = pick(half, x[8 + j], x[j]) * bt;
             bf16x8 pc[3];
             split<3>(y, pc);
 #pragma unroll
-            for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(sh.T[n] + l32 * LT + col) = pc[n];
+            for (int n = 0; n < 3; ++n)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                sh.T[n][(blk + 8 * half + j) * LT + l32] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(pc[n][j]));
+            const float b0 = G.beta[r16];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = j < 4 ? -m2[j & 3] * b0 : 0.f;
+            split<3>(y, pc);
+#pragma unroll
+            for (int n = 0; n < 3; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                sh.T[n][(16 + 4 * g4 + j) * LT + r16] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(pc[n][j]));
           }
         }
       }
@@ -391,6 +438,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
           }
           if (s == 1) __builtin_amdgcn_sched_barrier(0);
         }
+      if (wave == GW && c0 + C < hi) sum_gates(sh.gates[now ^ 1]);
       // v in accumulator layout, and as the bf16 right operand it already is
       bf16x8 vb[2];
       const int vr4 = 8 * half + (lane & 15) / 4, vc4 = 32 * wave + (lane & 16) + 4 * (lane & 3);
@@ -507,20 +555,22 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
         const int kr4 = 8 * half + (lane & 15) / 4, kc4 = perm(4 * (lane & 3)) + (lane & 16);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
+          bf16x8 ka[RT];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const s16x4 x0 = read_tr(K.at(kr4 + 16 * s, kc4 + 32 * r)), x1 = read_tr(K.at(kr4 + 16 * s + 4, kc4 + 32 * r));
+            const __attribute__((ext_vector_type(8))) short y = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+            ka[r] = __builtin_bit_cast(bf16x8, y);
+          }
           float x[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = w[8 * s + j] * G.tail[16 * s + 8 * half + j];
           bf16x8 wp[3];
           split<3>(x, wp);
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const s16x4 x0 = read_tr(K.at(kr4 + 16 * s, kc4 + 32 * r)), x1 = read_tr(K.at(kr4 + 16 * s + 4, kc4 + 32 * r));
-            const __attribute__((ext_vector_type(8))) short y = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
-            const bf16x8 a = __builtin_bit_cast(bf16x8, y);
-            S[r] = mma(a, wp[2], S[r]);
-            S[r] = mma(a, wp[1], S[r]);
-            S[r] = mma(a, wp[0], S[r]);
-          }
+          for (int n = 2; n >= 0; --n)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) S[r] = mma(ka[r], wp[n], S[r]);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -551,7 +601,7 @@ namespace {
 using ChunkFn = void (*)(const ScanArgs, int64_t);
 
 template <int KIND>
-ChunkFn pick(int dk, int dv) {
+ChunkFn pick_dims(int dk, int dv) {
   if (dk == 128) return dv == 128 ? k_scan_chunk<KIND, 128, 128> : k_scan_chunk<KIND, 128, 64>;
   return dv == 128 ? k_scan_chunk<KIND, 64, 128> : k_scan_chunk<KIND, 64, 64>;
 }
@@ -560,7 +610,7 @@ ChunkFn pick(int dk, int dv) {
 
 hipError_t launch_scan_chunk(const seed_shape& sh, const ScanArgs& a, hipStream_t s) {
   const int64_t units = static_cast<int64_t>(a.batch) * a.heads;
-  const ChunkFn fn = sh.kind == SEED_GDN ? pick<SEED_GDN>(sh.d_k, sh.d_v) : pick<SEED_MAMBA2>(sh.d_k, sh.d_v);
+  const ChunkFn fn = sh.kind == SEED_GDN ? pick_dims<SEED_GDN>(sh.d_k, sh.d_v) : pick_dims<SEED_MAMBA2>(sh.d_k, sh.d_v);
   hipLaunchKernelGGL(fn, dim3(loop_blocks(units)), dim3(sh.d_v * 2), 0, s, a, units);
   return hipGetLastError();
 }
