@@ -72,11 +72,15 @@ __device__ __forceinline__ void split(const float (&x)[8], bf16x8 (&p)[N]) {
 
 __device__ __forceinline__ bf16x8 frag(const uint16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
+// The LDS address of a pointer into shared memory: the low half of the generic one.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+}
+
 // Four rows of a row-major 16-bit tile, transposed: lane i of 16 passes the address of row i / 4,
 // columns 4 (i % 4) .. + 3 and receives column i, rows 0 .. 3.
 __device__ __forceinline__ s16x4 read_tr(const uint16_t* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (__attribute__((address_space(3))) s16x4*)(const_cast<uint16_t*>(p)));
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)lds_offset(p));
 }
 
 // Rows c0 .. hi - 1 of a row buffer as a bounds-checked buffer: loads behind the last row's `width`
@@ -92,8 +96,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const uint16_t* bas
 // write zeros. lds is the same for the whole wavefront. The compiler does not see the write: it is
 // waited for with wait_loads before the barrier in front of the tile's first use.
 __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rows, int voffset, int soffset, const uint16_t* lds) {
-  const uint32_t to = __builtin_amdgcn_readfirstlane(
-      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint16_t*)lds)));
+  const uint32_t to = __builtin_amdgcn_readfirstlane(lds_offset(lds));
   uint32_t m0;  // M0 holds the LDS address; what it held is put back
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
@@ -160,50 +163,252 @@ struct Tile {
 template <int KIND, int DK, int DV>
 struct Tiles {
   static constexpr bool DELTA = KIND != SEED_MAMBA2;
-  Tile<DK> K[2], Q[2];            // by the chunk's parity: the next chunk's rows arrive during this one
-  Tile<DV> V[2];                  // v, then o
-  uint16_t P[2][C * LT];
-  uint16_t T[DELTA ? 3 : 1][DELTA ? C * LT : 8];
-  float T11[DELTA ? 16 * LF : 4]; // column-major: the lower diagonal block of T
+  // by the chunk's number modulo 3: one in use, one that T and P are formed of, one arriving
+  Tile<DK> K[3], Q[3];
+  Tile<DV> V[3];                  // v, then o
   struct Gates {
     float ch[C], cl[C];           // c as a sum of two floats
     float head[C], tail[C];       // 2^c_t, 2^(c_end - c_t)
     float beta[C], g[C];
-  } gates[2];
+  } gates[3];
+  // by the chunk's number modulo 2
+  uint16_t P[2][2][C * LT];
+  uint16_t T[DELTA ? 2 : 1][DELTA ? 3 : 1][DELTA ? C * LT : 8];
+  float T11[DELTA ? 16 * LF : 4]; // column-major: the lower diagonal block of T
 };
+
+// The 32 rows of a tile at row f0 on, by one wavefront.
+template <int D>
+__device__ __forceinline__ void fetch_tile(const uint16_t* base, int64_t stride, int64_t f0, int64_t hi, Tile<D>& to) {
+  constexpr int RPI = 512 / D;    // rows per load: 64 lanes of 16 bytes
+  const auto rows = chunk_rows(base, stride, f0, hi, D * 2);
+  const int st = static_cast<int>(stride) * 2;
+  const int lane = fresh(threadIdx.x & 63);
+#pragma unroll
+  for (int j = 0; j < C / RPI; ++j) {
+    const int r = lane / (D / 8), piece = (lane % (D / 8)) ^ Tile<D>::swz(j * RPI + r);
+    load_lds(rows, r * st + piece * 16, j * RPI * st, to.x + j * 512);
+  }
+}
+
+// The gates of the chunk at f0: log2 g summed over the chunk, and the weights that follow.
+__device__ __forceinline__ void load_gates(const ScanArgs& A, int h, int64_t f0, int64_t hi, float& g, float& beta) {
+  const int64_t f1 = f0 + (threadIdx.x & 31);
+  const int64_t at = (f1 < hi ? f1 : hi - 1) * A.heads + h;
+  const float g1 = A.g[at], b1 = A.beta[at];
+  g = f1 < hi ? g1 : 1.f;
+  beta = f1 < hi ? b1 : 0.f;
+}
+template <class Gates>
+__device__ __forceinline__ void sum_gates(Gates& G, float g, float beta) {
+  const int l = fresh(threadIdx.x & 63), l32 = l & 31;
+  // g = 0 counts as 2^-200: across it every weight underflows to 0, as it should
+  const float lg = log2f(g);
+  double c = lg < -200.f ? -200.0 : static_cast<double>(lg);
+#pragma unroll
+  for (int d = 1; d < C; d <<= 1) {
+    const double up = __shfl_up(c, d, C);
+    if (l32 >= d) c += up;
+  }
+  const float ch = static_cast<float>(c), cl = static_cast<float>(c - static_cast<double>(ch));
+  const double rest = __shfl(c, C - 1, C) - c;
+  const float rh = static_cast<float>(rest), rl = static_cast<float>(rest - static_cast<double>(rh));
+  const float eh = exp2f(ch), et = exp2f(rh);
+  if (l < C) {
+    G.ch[l] = ch;
+    G.cl[l] = cl;
+    G.head[l] = fmaf(eh, 0.693147181f * cl, eh);
+    G.tail[l] = fmaf(et, 0.693147181f * rl, et);
+    G.beta[l] = beta;
+    G.g[l] = g;
+  }
+}
+
+// 2^(c_t - c_s) for t = l32 and the 16 s of the lane's accumulator registers.
+template <class Gates>
+__device__ __forceinline__ void weights(const Gates& G, int l32, int half, float (&e)[16]) {
+  const float th = G.ch[l32], tl = G.cl[l32];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int s = 16 * (i / 8) + 8 * half + i % 8;
+    e[i] = __builtin_amdgcn_exp2f((th - G.ch[s]) + (tl - G.cl[s]));
+  }
+}
+
+// P (Mamba-2: times diag(beta)) in two pieces, by one wavefront.
+template <bool DELTA, int DK, class Gates>
+__device__ __forceinline__ void form_P(Tile<DK>& K, Tile<DK>& Q, const Gates& G, uint16_t (&P)[2][C * LT]) {
+  const int lane = fresh(threadIdx.x & 63), l32 = lane & 31, half = lane >> 5, prow = perm(l32);
+  f32x16 acc = {};
+#pragma unroll
+  for (int ks = 0; ks < DK / 16; ++ks)
+    acc = mma(frag(K.at(prow, 16 * ks + 8 * half)), frag(Q.at(l32, 16 * ks + 8 * half)), acc);
+  float e[16];
+  weights(G, l32, half, e);
+#pragma unroll
+  for (int s8 = 0; s8 < 2; ++s8) {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = 16 * s8 + 8 * half + j;
+      float w = acc[8 * s8 + j] * e[8 * s8 + j];
+      if constexpr (!DELTA) w *= G.beta[s];
+      x[j] = s <= l32 ? w : 0.f;
+    }
+    bf16x8 pc[2];
+    split<2>(x, pc);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(P[n] + l32 * LT + 16 * s8 + 8 * half) = pc[n];
+  }
+}
+
+// (I + L)^-1 diag(beta) in three pieces, by one wavefront. The block above the diagonal stays zero.
+template <int DK, class Gates>
+__device__ __forceinline__ void form_T(Tile<DK>& K, const Gates& G, uint16_t (&T)[3][C * LT], float* T11) {
+  const int lane = fresh(threadIdx.x & 63), l32 = lane & 31, half = lane >> 5, prow = perm(l32);
+  f32x16 acc = {};
+#pragma unroll
+  for (int ks = 0; ks < DK / 16; ++ks)
+    acc = mma(frag(K.at(prow, 16 * ks + 8 * half)), frag(K.at(l32, 16 * ks + 8 * half)), acc);
+  float e[16];
+  weights(G, l32, half, e);
+  const float bt = G.beta[l32];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int s = 16 * (i / 8) + 8 * half + i % 8;
+    e[i] = s < l32 ? bt * (acc[i] * e[i]) : 0.f;
+  }
+  // row l32 of its diagonal block, from both halves of the wavefront
+  float Lr[16], x[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t z = __float_as_uint(pick(l32 & 16, e[8 + j], e[j]));
+    const auto r = __builtin_amdgcn_permlane32_swap(z, z, false, false);
+    Lr[j] = __uint_as_float(r[0]);
+    Lr[8 + j] = __uint_as_float(r[1]);
+  }
+#pragma unroll
+  for (int t = 0; t < 16; ++t) x[t] = t == (l32 & 15) ? 1.f : 0.f;
+  solve16(Lr, x);  // both halves: lane l32 has column l32 % 16 of block l32 / 16
+  // the block below the diagonal: -T11 (L10 T00) in fp32 matrix instructions, whose k slot lane / 16 of
+  // step i is taken as 4 (lane / 16) + i
+  const int r16 = lane & 15, g4 = lane >> 4;
+  if (l32 & 16) {
+#pragma unroll
+    for (int t = 0; t < 16; t += 4)
+      *reinterpret_cast<f32x4*>(T11 + r16 * LF + t) = f32x4{x[t], x[t + 1], x[t + 2], x[t + 3]};
+  }
+  f32x4 m1 = {}, m2 = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a0 = e[i], a1 = e[4 + i];  // L10[r16][8 half + i], [8 half + 4 + i] in the odd rows of lanes
+    lane_swap16(a0, a1);             // a1: L10[r16][4 g4 + i]
+    float b0 = pick(half, x[8 + i], x[i]), b1 = pick(half, x[12 + i], x[4 + i]);
+    lane_swap16(b0, b1);             // b0: T00[4 g4 + i][r16]
+    m1 = __builtin_amdgcn_mfma_f32_16x16x4f32(a1, b0, m1, 0, 0, 0);
+  }
+  wave_lds_sync();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m2 = __builtin_amdgcn_mfma_f32_16x16x4f32(T11[(4 * g4 + i) * LF + r16], m1[i], m2, 0, 0, 0);
+  // each half writes 8 rows of the diagonal blocks' columns, then the block below
+  const int blk = l32 & 16;
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = pick(half, x[8 + j], x[j]) * bt;
+  bf16x8 pc[3];
+  split<3>(y, pc);
+#pragma unroll
+  for (int n = 0; n < 3; ++n)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      T[n][(blk + 8 * half + j) * LT + l32] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(pc[n][j]));
+  const float b16 = G.beta[r16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = j < 4 ? -m2[j & 3] * b16 : 0.f;
+  split<3>(y, pc);
+#pragma unroll
+  for (int n = 0; n < 3; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      T[n][(16 + 4 * g4 + j) * LT + r16] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(pc[n][j]));
+  wave_lds_sync();  // T11 has been read
+}
 
 }  // namespace
 
+// Wavefronts 0 .. NW - 1 hold 32 columns of the state each and run a chunk while the NH others prepare:
+// T and P of the next chunk, and rows and gates of the one after it.
 template <int KIND, int DK, int DV>
-__global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int64_t units) {
+__global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, int64_t units) {
   using TL = Tiles<KIND, DK, DV>;
   constexpr bool DELTA = TL::DELTA;
-  constexpr int NW = DV / 32, NT = NW * 64;
+  constexpr int NW = DV / 32, NH = NW, NT = (NW + NH) * 64;
   constexpr int RT = DK / 32;                 // row tiles of the state
-  constexpr int KP = C * DK / 8 / NT;         // 16-byte pieces of K (and Q) per thread
-  constexpr int VP = C * DV / 8 / NT;
-  constexpr int GW = NW == 4 ? 1 : (DELTA ? 1 : 0);  // forms the gates; wavefront 0 forms T, the last one P
-  constexpr int KR = C / KP, VR = C / VP;     // rows that one piece of every thread covers
   __shared__ TL sh;
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int half0 = (threadIdx.x & 63) >> 5;
+  const int role = wave - NW;                 // of the helpers
+  // which helper does what
+  constexpr int kT = 0, kP = 1, kK = NH == 4 ? 2 : (DELTA ? 1 : 0), kQV = NH == 4 ? 3 : kK, kG = kK;
+
+  if constexpr (DELTA) {  // the block of T above the diagonal
+    for (int i = threadIdx.x; i < 2 * 3 * 16 * 16; i += NT)
+      sh.T[i / 768][i / 256 % 3][(i / 16 % 16) * LT + 16 + i % 16] = 0;
+  }
 
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int b = static_cast<int>(unit / A.heads), h = static_cast<int>(unit % A.heads);
     const int kh = h / (A.heads / A.key_heads);
     int64_t lo, hi;
     sequence_rows(A.offsets, b, A.tokens, lo, hi);
+    lo = __builtin_amdgcn_readfirstlane(static_cast<int>(lo));  // rows are below 2^31
+    hi = __builtin_amdgcn_readfirstlane(static_cast<int>(hi));
+    const int n = static_cast<int>((hi - lo + C - 1) / C);  // chunks
 
     const uint16_t* __restrict__ qp = static_cast<const uint16_t*>(A.q) + static_cast<int64_t>(kh) * DK;
     const uint16_t* __restrict__ kp = static_cast<const uint16_t*>(A.k) + static_cast<int64_t>(kh) * DK;
     const uint16_t* __restrict__ vp = static_cast<const uint16_t*>(A.v) + static_cast<int64_t>(h) * DV;
     uint16_t* __restrict__ op = static_cast<uint16_t*>(A.o) + static_cast<int64_t>(h) * DV;
 
-    // the state: register i of row tile r is row 32 r + 16 (i / 8) + 8 half + i % 8, column 32 wave + l32
+    if (role >= 0) {
+      // ---- helpers ------------------------------------------------------------------------------------
+      // chunk j's rows go to buffer `to`; its gates are loaded at once and summed when `sum` is called
+      float g = 1.f, beta = 0.f;
+      auto fetch = [&](int j, int to) {
+        const int64_t f0 = lo + static_cast<int64_t>(j) * C;
+        if (role == kG) load_gates(A, h, f0, hi, g, beta);
+        if (role == kK) fetch_tile<DK>(kp, A.k_stride, f0, hi, sh.K[to]);
+        if (role == kQV) {
+          fetch_tile<DK>(qp, A.q_stride, f0, hi, sh.Q[to]);
+          fetch_tile<DV>(vp, A.v_stride, f0, hi, sh.V[to]);
+        }
+        if (role == kG) sum_gates(sh.gates[to], g, beta);
+      };
+      if (n > 0) fetch(0, 0);
+      wait_loads<0>();
+      __syncthreads();
+      int next = 0, far = 1;  // buffers of chunks j + 1 and j + 2
+      for (int j = -1; j < n; ++j) {
+        if (j + 2 < n) fetch(j + 2, far);
+        if (j + 1 < n) {
+          if constexpr (DELTA) {
+            if (role == kT) form_T<DK>(sh.K[next], sh.gates[next], sh.T[(j + 1) & 1], sh.T11);
+          }
+          if (role == kP) form_P<DELTA, DK>(sh.K[next], sh.Q[next], sh.gates[next], sh.P[(j + 1) & 1]);
+        }
+        wait_loads<0>();
+        __syncthreads();
+        next = far;
+        far = far == 2 ? 0 : far + 1;
+      }
+      continue;
+    }
+
+    // ---- the state: register i of row tile r is row 32 r + 16 (i / 8) + 8 half + i % 8, column 32 wave + l32
     f32x16 S[RT];
     constexpr int SB = DK * DV * 4;
-    const int s_at = (8 * half0 * DV + 32 * wave + (threadIdx.x & 31)) * 4;
+    const int s_at = (8 * ((threadIdx.x & 63) >> 5) * DV + 32 * wave + (threadIdx.x & 31)) * 4;
     if (A.S0 != nullptr) {
       const auto sr = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(A.S0 + unit * DK * DV), 0, SB, 0x00027000);
 #pragma unroll
@@ -215,75 +420,12 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
 #pragma unroll
       for (int r = 0; r < RT; ++r) S[r] = f32x16{};
     }
+    __syncthreads();  // chunk 0's rows and gates
+    __syncthreads();  // its T and P
 
-    // The next chunk's rows go straight to LDS; rows past the end arrive as zeros, g as 1. A thread
-    // loads the 16 bytes at place (thread) of every KR (VR) rows, that is piece place ^ swz(row).
-    auto fetch = [&](int64_t f0, int to) {
-      const int tid = fresh(threadIdx.x);
-      const int krow = tid / (DK / 8), vrow = tid / (DV / 8);
-      const auto kr = chunk_rows(kp, A.k_stride, f0, hi, DK * 2), qr = chunk_rows(qp, A.q_stride, f0, hi, DK * 2);
-      const auto vr = chunk_rows(vp, A.v_stride, f0, hi, DV * 2);
-#pragma unroll
-      for (int p = 0; p < KP; ++p) {
-        const int row = krow + p * KR, piece = (tid % (DK / 8)) ^ Tile<DK>::swz(row);
-        const int lds = (p * NT + wave * 64) * 8;
-        load_lds(kr, (krow * static_cast<int>(A.k_stride) + 8 * piece) * 2, p * KR * static_cast<int>(A.k_stride) * 2, sh.K[to].x + lds);
-        load_lds(qr, (krow * static_cast<int>(A.q_stride) + 8 * piece) * 2, p * KR * static_cast<int>(A.q_stride) * 2, sh.Q[to].x + lds);
-      }
-#pragma unroll
-      for (int p = 0; p < VP; ++p) {
-        const int row = vrow + p * VR, piece = (tid % (DV / 8)) ^ Tile<DV>::swz(row);
-        load_lds(vr, (vrow * static_cast<int>(A.v_stride) + 8 * piece) * 2, p * VR * static_cast<int>(A.v_stride) * 2,
-                 sh.V[to].x + (p * NT + wave * 64) * 8);
-      }
-    };
-    // The gates of the chunk at f0, by one wavefront: loads early, sums and exponentials late.
-    float ng = 1.f, nb = 0.f;
-    auto load_gates = [&](int64_t f0) {
-      const int64_t f1 = f0 + (threadIdx.x & 31);
-      const int64_t at = (f1 < hi ? f1 : hi - 1) * A.heads + h;
-      const float g1 = A.g[at], b1 = A.beta[at];
-      ng = f1 < hi ? g1 : 1.f;
-      nb = f1 < hi ? b1 : 0.f;
-    };
-    auto sum_gates = [&](typename TL::Gates& G) {
-      const int l = fresh(threadIdx.x & 63), l32 = l & 31;
-      // g = 0 counts as 2^-200: across it every weight underflows to 0, as it should
-      const float lg = log2f(ng);
-      double c = lg < -200.f ? -200.0 : static_cast<double>(lg);
-#pragma unroll
-      for (int d = 1; d < C; d <<= 1) {
-        const double up = __shfl_up(c, d, C);
-        if (l32 >= d) c += up;
-      }
-      const float ch = static_cast<float>(c), cl = static_cast<float>(c - static_cast<double>(ch));
-      const double rest = __shfl(c, C - 1, C) - c;
-      const float rh = static_cast<float>(rest), rl = static_cast<float>(rest - static_cast<double>(rh));
-      const float eh = exp2f(ch), et = exp2f(rh);
-      if (l < C) {
-        G.ch[l] = ch;
-        G.cl[l] = cl;
-        G.head[l] = fmaf(eh, 0.693147181f * cl, eh);
-        G.tail[l] = fmaf(et, 0.693147181f * rl, et);
-        G.beta[l] = nb;
-        G.g[l] = ng;
-      }
-    };
     int now = 0;
-    __syncthreads();  // the last unit's tiles have been read
-    if (lo < hi) {
-      fetch(lo, 0);
-      if (wave == GW) {
-        load_gates(lo);
-        sum_gates(sh.gates[0]);
-      }
-    }
-    if constexpr (DELTA) {  // the block of T above the diagonal
-      for (int i = threadIdx.x; i < 3 * 16; i += NT)
-        for (int j = 0; j < 16; ++j) sh.T[i / 16][(i % 16) * LT + 16 + j] = 0;
-    }
-
-    for (int64_t c0 = lo; c0 < hi; c0 += C, now ^= 1) {
+    for (int ci = 0; ci < n; ++ci, now = now == 2 ? 0 : now + 1) {
+      const int64_t c0 = lo + static_cast<int64_t>(ci) * C;
       // lane numbers that the compiler takes for new ones in every chunk, so that the addresses made
       // of them cost an instruction each instead of a register each
       const int lane = fresh(threadIdx.x & 63);
@@ -293,123 +435,8 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
       auto& Q = sh.Q[now];
       auto& V = sh.V[now];
       auto& G = sh.gates[now];
-      // the chunk's rows are here: everything older than the last chunk's two read-out stores
-      if (c0 == lo) wait_loads<0>();
-      else wait_loads<2>();
-      __syncthreads();
-      if (c0 + C < hi) {
-        fetch(c0 + C, now ^ 1);
-        if (wave == GW) load_gates(c0 + C);
-      }
+      auto& P = sh.P[ci & 1];
 
-      // ---- P, and T by another wavefront ------------------------------------------------------------
-      // 2^(c_t - c_s) for t = l32 and the 16 s of the lane's accumulator registers
-      auto weights = [&](float (&e)[16]) {
-        const float th = G.ch[l32], tl = G.cl[l32];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int s = 16 * (i / 8) + 8 * half + i % 8;
-          e[i] = __builtin_amdgcn_exp2f((th - G.ch[s]) + (tl - G.cl[s]));
-        }
-      };
-      if (wave == NW - 1) {
-        f32x16 acc = {};
-#pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks)
-          acc = mma(frag(K.at(prow, 16 * ks + 8 * half)), frag(Q.at(l32, 16 * ks + 8 * half)), acc);
-        float e[16];
-        weights(e);
-#pragma unroll
-        for (int s8 = 0; s8 < 2; ++s8) {
-          float x[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int s = 16 * s8 + 8 * half + j;
-            float w = acc[8 * s8 + j] * e[8 * s8 + j];
-            if constexpr (!DELTA) w *= G.beta[s];
-            x[j] = s <= l32 ? w : 0.f;
-          }
-          bf16x8 pc[2];
-          split<2>(x, pc);
-#pragma unroll
-          for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(sh.P[n] + l32 * LT + 16 * s8 + 8 * half) = pc[n];
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (DELTA) {
-        if (wave == 0) {
-          f32x16 acc = {};
-#pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks)
-            acc = mma(frag(K.at(prow, 16 * ks + 8 * half)), frag(K.at(l32, 16 * ks + 8 * half)), acc);
-          float e[16];
-          weights(e);
-          const float bt = G.beta[l32];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int s = 16 * (i / 8) + 8 * half + i % 8;
-            e[i] = s < l32 ? bt * (acc[i] * e[i]) : 0.f;
-          }
-          // row l32 of its diagonal block, from both halves of the wavefront
-          float Lr[16], x[16];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t z = __float_as_uint(pick(l32 & 16, e[8 + j], e[j]));
-            const auto r = __builtin_amdgcn_permlane32_swap(z, z, false, false);
-            Lr[j] = __uint_as_float(r[0]);
-            Lr[8 + j] = __uint_as_float(r[1]);
-          }
-#pragma unroll
-          for (int t = 0; t < 16; ++t) x[t] = t == (l32 & 15) ? 1.f : 0.f;
-          solve16(Lr, x);  // both halves: lane l32 has column l32 % 16 of block l32 / 16
-          // the block below the diagonal: -T11 (L10 T00) in fp32 matrix instructions, whose k slot lane / 16
-          // of step i is taken as 4 (lane / 16) + i
-          const int r16 = lane & 15, g4 = lane >> 4;
-          if (l32 & 16) {
-#pragma unroll
-            for (int t = 0; t < 16; t += 4)
-              *reinterpret_cast<f32x4*>(sh.T11 + r16 * LF + t) = f32x4{x[t], x[t + 1], x[t + 2], x[t + 3]};
-          }
-          f32x4 m1 = {}, m2 = {};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float a0 = e[i], a1 = e[4 + i];  // L10[r16][8 half + i], [8 half + 4 + i] in the odd rows of lanes
-            lane_swap16(a0, a1);             // a1: L10[r16][4 g4 + i]
-            float b0 = pick(half, x[8 + i], x[i]), b1 = pick(half, x[12 + i], x[4 + i]);
-            lane_swap16(b0, b1);             // b0: T00[4 g4 + i][r16]
-            m1 = __builtin_amdgcn_mfma_f32_16x16x4f32(a1, b0, m1, 0, 0, 0);
-          }
-          wave_lds_sync();
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            m2 = __builtin_amdgcn_mfma_f32_16x16x4f32(sh.T11[(4 * g4 + i) * LF + r16], m1[i], m2, 0, 0, 0);
-          // T diag(beta) in pieces: each half writes 8 rows of the diagonal blocks' columns, then the block below
-          {
-            const int blk = l32 & 16;
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = pick(half, x[8 + j], x[j]) * bt;
-            bf16x8 pc[3];
-            split<3>(y, pc);
-#pragma unroll
-            for (int n = 0; n < 3; ++n)
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                sh.T[n][(blk + 8 * half + j) * LT + l32] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(pc[n][j]));
-            const float b0 = G.beta[r16];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = j < 4 ? -m2[j & 3] * b0 : 0.f;
-            split<3>(y, pc);
-#pragma unroll
-            for (int n = 0; n < 3; ++n)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                sh.T[n][(16 + 4 * g4 + j) * LT + r16] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(pc[n][j]));
-          }
-        }
-      }
-
-      __builtin_amdgcn_sched_barrier(0);
       // ---- K S and Q S ------------------------------------------------------------------------------
       f32x16 ks = {}, qs = {};
 #pragma unroll
@@ -436,9 +463,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
             qs = mma(aq, pc[1], qs);
             qs = mma(aq, pc[0], qs);
           }
-          if (s == 1) __builtin_amdgcn_sched_barrier(0);
         }
-      if (wave == GW && c0 + C < hi) sum_gates(sh.gates[now ^ 1]);
       // v in accumulator layout, and as the bf16 right operand it already is
       bf16x8 vb[2];
       const int vr4 = 8 * half + (lane & 15) / 4, vc4 = 32 * wave + (lane & 16) + 4 * (lane & 3);
@@ -448,7 +473,6 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
         const __attribute__((ext_vector_type(8))) short x = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
         vb[s] = __builtin_bit_cast(bf16x8, x);
       }
-      __syncthreads();
 
       // ---- W ----------------------------------------------------------------------------------------
       f32x16 w;
@@ -465,7 +489,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
           bf16x8 rp[3], tp[3];
           split<3>(x, rp);
 #pragma unroll
-          for (int n = 0; n < 3; ++n) tp[n] = frag(sh.T[n] + prow * LT + 16 * s + 8 * half);
+          for (int n = 0; n < 3; ++n) tp[n] = frag(sh.T[ci & 1][n] + prow * LT + 16 * s + 8 * half);
           w = mma(tp[2], rp[0], w);
           w = mma(tp[1], rp[1], w);
           w = mma(tp[0], rp[2], w);
@@ -484,9 +508,9 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
 #pragma unroll
       for (int i = 0; i < 16; ++i) fin = fmaf(w[i], 0.f, fin);
       if (__builtin_expect(__any(!(fin == 0.f)), 0)) {
-        const int n = static_cast<int>(hi - c0 < C ? hi - c0 : C);
+        const int live = static_cast<int>(hi - c0 < C ? hi - c0 : C);
 #pragma unroll 1
-        for (int t = 0; t < n; ++t) {
+        for (int t = 0; t < live; ++t) {
           const float gt = G.g[t];
           float sk = 0.f, sq = 0.f, kq = 0.f;
 #pragma unroll
@@ -530,7 +554,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
         for (int i = 0; i < 16; ++i) o[i] = hd[i] * qs[i];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const bf16x8 p0 = frag(sh.P[0] + prow * LT + 16 * s + 8 * half), p1 = frag(sh.P[1] + prow * LT + 16 * s + 8 * half);
+          const bf16x8 p0 = frag(P[0] + prow * LT + 16 * s + 8 * half), p1 = frag(P[1] + prow * LT + 16 * s + 8 * half);
           if constexpr (DELTA) {
             float x[8];
 #pragma unroll
@@ -585,6 +609,7 @@ __global__ __launch_bounds__(DV * 2, 2) void k_scan_chunk(const ScanArgs A, int6
         const u32x4 x = *reinterpret_cast<const u32x4*>(V.at(16 * p + lane / 4, 32 * wave + 8 * (lane & 3)));
         __builtin_amdgcn_raw_buffer_store_b128(x, orow, o_at, p * 16 * static_cast<int>(A.o_stride) * 2, 0);
       }
+      __syncthreads();
     }
 
     const auto sr = __builtin_amdgcn_make_buffer_rsrc(A.S + unit * DK * DV, 0, SB, 0x00027000);
@@ -611,7 +636,7 @@ ChunkFn pick_dims(int dk, int dv) {
 hipError_t launch_scan_chunk(const seed_shape& sh, const ScanArgs& a, hipStream_t s) {
   const int64_t units = static_cast<int64_t>(a.batch) * a.heads;
   const ChunkFn fn = sh.kind == SEED_GDN ? pick_dims<SEED_GDN>(sh.d_k, sh.d_v) : pick_dims<SEED_MAMBA2>(sh.d_k, sh.d_v);
-  hipLaunchKernelGGL(fn, dim3(loop_blocks(units)), dim3(sh.d_v * 2), 0, s, a, units);
+  hipLaunchKernelGGL(fn, dim3(loop_blocks(units)), dim3(sh.d_v * 4), 0, s, a, units);
   return hipGetLastError();
 }
 
