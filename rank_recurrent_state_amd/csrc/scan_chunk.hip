@@ -37,8 +37,10 @@ using f32x4 = __attribute__((ext_vector_type(4))) float;
 using f32x16 = __attribute__((ext_vector_type(16))) float;
 using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
 using s16x4 = __attribute__((ext_vector_type(4))) short;
+using lds_s16x4 = __attribute__((address_space(3))) s16x4;
 
 constexpr int C = 32;       // tokens per chunk
+constexpr int kRanked = 512;  // sequences that are put in order of length
 constexpr int LT = C + 8;   // row length of the T and P pieces
 constexpr int LF = 16 + 4;  // row length of the fp32 block of T
 
@@ -80,7 +82,7 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // Four rows of a row-major 16-bit tile, transposed: lane i of 16 passes the address of row i / 4,
 // columns 4 (i % 4) .. + 3 and receives column i, rows 0 .. 3.
 __device__ __forceinline__ s16x4 read_tr(const uint16_t* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)lds_offset(p));
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(static_cast<uintptr_t>(lds_offset(p))));
 }
 
 // Rows c0 .. hi - 1 of a row buffer as a bounds-checked buffer: loads behind the last row's `width`
@@ -117,27 +119,34 @@ __device__ __forceinline__ void wait_loads() {
 // By value: a conditional between two elements of an array would put the array in memory.
 __device__ __forceinline__ float pick(bool c, float a, float b) { return c ? a : b; }
 
-// Lane N of the lane's 16, to all of them.
+// a += (b of lane N of the lane's 16) c, in one instruction.
 template <int N>
-__device__ __forceinline__ float bcast16(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x150 + N, 0xF, 0xF, true));
+__device__ __forceinline__ void fmac_bcast16(float& a, float b, float c) {
+  asm("v_fmac_f32_dpp %0, %1, %2 row_newbcast:%3 row_mask:0xf bank_mask:0xf" : "+v"(a) : "v"(b), "v"(c), "n"(N));
 }
 
-// x = (I + L)^-1 e_j for a 16 x 16 strictly lower L: lane i of 16 holds row i of L and gets column i of
+// x = (I - L)^-1 e_j for a 16 x 16 strictly lower L: lane i of 16 holds row i of L and gets column i of
 // the inverse. Step S takes x[S], final by then, out of the rows below.
 template <int S, int R>
 __device__ __forceinline__ void solve_row(const float (&L)[16], float (&x)[16]) {
   if constexpr (R < 16) {
-    x[R] = fmaf(-bcast16<R>(L[S]), x[S], x[R]);
+    fmac_bcast16<R>(x[R], L[S], x[S]);
     solve_row<S, R + 1>(L, x);
   }
 }
-template <int S = 0>
-__device__ __forceinline__ void solve16(const float (&L)[16], float (&x)[16]) {
+template <int S>
+__device__ __forceinline__ void solve_from(const float (&L)[16], float (&x)[16]) {
   if constexpr (S < 15) {
     solve_row<S, S + 1>(L, x);
-    solve16<S + 1>(L, x);
+    solve_from<S + 1>(L, x);
   }
+}
+__device__ __forceinline__ void solve16(float (&L)[16], float (&x)[16]) {
+  // a lane broadcast may read a register two instructions after its write at the earliest
+  asm("s_nop 1"
+      : "+v"(L[0]), "+v"(L[1]), "+v"(L[2]), "+v"(L[3]), "+v"(L[4]), "+v"(L[5]), "+v"(L[6]), "+v"(L[7]), "+v"(L[8]),
+        "+v"(L[9]), "+v"(L[10]), "+v"(L[11]), "+v"(L[12]), "+v"(L[13]), "+v"(L[14]));
+  solve_from<0>(L, x);
 }
 
 // A copy of x that the compiler takes for a new value.
@@ -175,6 +184,7 @@ struct Tiles {
   uint16_t P[2][2][C * LT];
   uint16_t T[DELTA ? 2 : 1][DELTA ? 3 : 1][DELTA ? C * LT : 8];
   float T11[DELTA ? 16 * LF : 4]; // column-major: the lower diagonal block of T
+  int32_t len[kRanked], found;    // of ranked_sequence
 };
 
 // The 32 rows of a tile at row f0 on, by one wavefront.
@@ -276,7 +286,7 @@ __device__ __forceinline__ void form_T(Tile<DK>& K, const Gates& G, uint16_t (&T
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int s = 16 * (i / 8) + 8 * half + i % 8;
-    e[i] = s < l32 ? bt * (acc[i] * e[i]) : 0.f;
+    e[i] = s < l32 ? -bt * (acc[i] * e[i]) : 0.f;  // -L
   }
   // row l32 of its diagonal block, from both halves of the wavefront
   float Lr[16], x[16];
@@ -290,7 +300,7 @@ __device__ __forceinline__ void form_T(Tile<DK>& K, const Gates& G, uint16_t (&T
 #pragma unroll
   for (int t = 0; t < 16; ++t) x[t] = t == (l32 & 15) ? 1.f : 0.f;
   solve16(Lr, x);  // both halves: lane l32 has column l32 % 16 of block l32 / 16
-  // the block below the diagonal: -T11 (L10 T00) in fp32 matrix instructions, whose k slot lane / 16 of
+  // the block below the diagonal: T11 (-L10 T00) in fp32 matrix instructions, whose k slot lane / 16 of
   // step i is taken as 4 (lane / 16) + i
   const int r16 = lane & 15, g4 = lane >> 4;
   if (l32 & 16) {
@@ -301,8 +311,8 @@ __device__ __forceinline__ void form_T(Tile<DK>& K, const Gates& G, uint16_t (&T
   f32x4 m1 = {}, m2 = {};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float a0 = e[i], a1 = e[4 + i];  // L10[r16][8 half + i], [8 half + 4 + i] in the odd rows of lanes
-    lane_swap16(a0, a1);             // a1: L10[r16][4 g4 + i]
+    float a0 = e[i], a1 = e[4 + i];  // -L10[r16][8 half + i], [8 half + 4 + i] in the odd rows of lanes
+    lane_swap16(a0, a1);             // a1: -L10[r16][4 g4 + i]
     float b0 = pick(half, x[8 + i], x[i]), b1 = pick(half, x[12 + i], x[4 + i]);
     lane_swap16(b0, b1);             // b0: T00[4 g4 + i][r16]
     m1 = __builtin_amdgcn_mfma_f32_16x16x4f32(a1, b0, m1, 0, 0, 0);
@@ -325,7 +335,7 @@ __device__ __forceinline__ void form_T(Tile<DK>& K, const Gates& G, uint16_t (&T
       T[n][(blk + 8 * half + j) * LT + l32] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(pc[n][j]));
   const float b16 = G.beta[r16];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = j < 4 ? -m2[j & 3] * b16 : 0.f;
+  for (int j = 0; j < 8; ++j) y[j] = j < 4 ? m2[j & 3] * b16 : 0.f;
   split<3>(y, pc);
 #pragma unroll
   for (int n = 0; n < 3; ++n)
@@ -336,6 +346,30 @@ __device__ __forceinline__ void form_T(Tile<DK>& K, const Gates& G, uint16_t (&T
 }
 
 }  // namespace
+
+// The sequence that is `rank`-th by length, longest first (the earlier of two equal ones first); with
+// more than kRanked sequences simply sequence `rank`. Workgroups start in block order, and a long
+// sequence started last would be run by a few of them alone: 16 prompts of 0 to 3646 tokens x 64
+// Mamba-2 heads take 528 us in the order given and 460 us longest first. Called by the whole workgroup.
+template <int NT>
+__device__ __forceinline__ int ranked_sequence(const ScanArgs& A, int rank, int32_t (&len)[kRanked], int32_t& found) {
+  if (A.batch > kRanked) return rank;
+  __syncthreads();  // the buffers' last use
+  for (int i = threadIdx.x; i < A.batch; i += NT) {
+    int64_t lo, hi;
+    sequence_rows(A.offsets, i, A.tokens, lo, hi);
+    len[i] = static_cast<int32_t>(hi - lo);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < A.batch; i += NT) {
+    const int32_t mine = len[i];
+    int before = 0;
+    for (int k = 0; k < A.batch; ++k) before += len[k] > mine || (len[k] == mine && k < i);
+    if (before == rank) found = i;
+  }
+  __syncthreads();
+  return found;
+}
 
 // Wavefronts 0 .. NW - 1 hold 32 columns of the state each and run a chunk while the NH others prepare:
 // T and P of the next chunk, and rows and gates of the one after it.
@@ -357,8 +391,10 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, int6
       sh.T[i / 768][i / 256 % 3][(i / 16 % 16) * LT + 16 + i % 16] = 0;
   }
 
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int b = static_cast<int>(unit / A.heads), h = static_cast<int>(unit % A.heads);
+  for (int64_t item = blockIdx.x; item < units; item += gridDim.x) {
+    const int h = static_cast<int>(item % A.heads);
+    const int b = __builtin_amdgcn_readfirstlane(ranked_sequence<NT>(A, static_cast<int>(item / A.heads), sh.len, sh.found));
+    const int64_t unit = static_cast<int64_t>(b) * A.heads + h;
     const int kh = h / (A.heads / A.key_heads);
     int64_t lo, hi;
     sequence_rows(A.offsets, b, A.tokens, lo, hi);
