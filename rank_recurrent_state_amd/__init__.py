@@ -34,10 +34,13 @@ _OVERLAP = {"OverlappedStack", "StaggeredStack", "partition_streams", "under_pro
 
 def __getattr__(name):
     if name in _NAMES:
-        return getattr(importlib.import_module("._lib", __name__), name)
-    if name in _OVERLAP:
-        return getattr(importlib.import_module(".overlap", __name__), name)
-    raise AttributeError(name)
+        value = getattr(importlib.import_module("._lib", __name__), name)
+    elif name in _OVERLAP:
+        value = getattr(importlib.import_module(".overlap", __name__), name)
+    else:
+        raise AttributeError(name)
+    globals()[name] = value  # found directly from now on
+    return value
 
 
 __all__ = sorted(_NAMES | _OVERLAP)

@@ -513,83 +513,99 @@ def seed_dense_decode_step(shape: seed_shape, S, q, k, v, beta, g, o, stream=Non
 
 
 # ---- the prompt path ------------------------------------------------------------------------------
+# These calls are a few microseconds of GPU work for a single token, so their wrappers keep to one
+# pass over the tensors: torch's own types are looked up once, pointers go to ctypes as integers.
+
+_IO = None  # (torch, {io code: dtype})
+_RAW_STREAM = None  # device index -> its current stream's handle
+
+
+def _io():
+    global _IO, _RAW_STREAM
+    if _IO is None:
+        import torch
+        _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream",  # without a Stream object around it
+                              lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _IO = (torch, {SEED_F32: torch.float32, SEED_BF16: torch.bfloat16, SEED_F16: torch.float16})
+    return _IO
 
 
 def make_conv(batch: int, channels: int, width: int, io_dtype: int = SEED_BF16, silu: bool = True) -> seed_conv:
     """A seed_conv: `width` taps per channel, SiLU behind them unless silu is False."""
-    return seed_conv(batch, channels, width, io_dtype, int(silu))
+    return seed_conv(batch, channels, width, io_dtype, 1 if silu else 0)
 
 
-def _expect_rows(name, t, rows, inner, code):
-    """Marshalling check of a row buffer [rows, *inner] whose rows may be strided: returns the row
-    stride in elements."""
-    width = 1
-    for n in inner:
-        width *= n
-    if t is None or not hasattr(t, "is_cuda"):
-        return width
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a device tensor")
-    if tuple(t.shape) != (rows, *inner):
-        raise ValueError(f"{name}: expected shape {(rows, *inner)}, got {tuple(t.shape)}")
-    if t.dtype != _torch_dt(code):
-        raise ValueError(f"{name}: expected dtype {_torch_dt(code)}, got {t.dtype}")
-    if rows == 0 or width == 0:
-        return width
-    want = 1
-    for n, s in zip(reversed(inner), reversed(t.stride()[1:])):
-        if n != 1 and s != want:
-            raise ValueError(f"{name}: expected contiguous values inside a row")
-        want *= n
-    if rows == 1:
-        return width
-    if t.stride(0) < width:
-        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)}, width {width})")
-    return t.stride(0)
+class _Args:
+    """Marshalling checks of one call's tensors: on one GPU, of the right size and type. Gives their
+    addresses, and the device and stream to launch on."""
 
+    __slots__ = ("torch", "device", "guard")
 
-def _expect_index(name, t, numel, dtype):
-    if t is None or not hasattr(t, "is_cuda"):
-        return
-    _expect(name, t, numel)
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    def __init__(self, torch):
+        self.torch, self.device, self.guard = torch, -1, None
 
+    def _on(self, name, t):
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a device tensor")
+        d = t.get_device()
+        if d != self.device:
+            if self.device >= 0:
+                raise ValueError(f"{name}: on device {d}, the tensors before it on device {self.device}")
+            self.device = d
 
-class _Launch:
-    """Runs a call on the device of its tensors: checks that they share one, makes it the current
-    device for the call, and gives the stream (the device's current one unless one is given)."""
+    def dense(self, name, t, numel, dtype):
+        """A contiguous tensor of numel elements, or None."""
+        if t is None:
+            return None
+        self._on(name, t)
+        if t.dtype is not dtype:
+            raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+        if t.numel() != numel:
+            raise ValueError(f"{name}: expected {numel} elements, got {t.numel()}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+        return t.data_ptr()
 
-    def __init__(self, stream, tensors):
-        import torch
-        devices = {t.device for t in tensors if t is not None and hasattr(t, "is_cuda")}
-        if len(devices) > 1:
-            raise ValueError(f"tensors on more than one device: {sorted(map(str, devices))}")
-        self.device = devices.pop() if devices else None
-        self.given = stream
-        self.guard = None
-        if self.device is not None and self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
+    def rows(self, name, t, shape, width, dtype):
+        """Rows [shape[0], ...] of `width` contiguous elements each, which may be strided: the address
+        and the row stride in elements. (None, width) for None."""
+        if t is None:
+            return None, width
+        self._on(name, t)
+        if t.dtype is not dtype:
+            raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.is_contiguous():
+            return t.data_ptr(), width
+        want, stride = 1, t.stride()
+        for n, s in zip(reversed(shape[1:]), reversed(stride[1:])):
+            if n != 1 and s != want:
+                raise ValueError(f"{name}: expected contiguous values inside a row")
+            want *= n
+        if shape[0] == 1:
+            return t.data_ptr(), width
+        if stride[0] < width:
+            raise ValueError(f"{name}: rows overlap (stride {stride[0]}, width {width})")
+        return t.data_ptr(), stride[0]
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream_ptr(self.given)
+    def launch(self, fn_name, stream, *args):
+        """Calls the entry point on the tensors' device, with its current stream unless one is given."""
+        cuda = self.torch.cuda
+        if self.device >= 0 and self.device != cuda.current_device():
+            with cuda.device(self.device):
+                self._call(fn_name, stream, args)
+        else:
+            self._call(fn_name, stream, args)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _expect_conv(conv, x, weight, bias, window_in, window_out, y, rows):
-    ch, n = conv.channels, conv.batch * (conv.width - 1) * conv.channels
-    xs = _expect_rows("x", x, rows, (ch,), conv.io_dtype)
-    ys = _expect_rows("y", y, rows, (ch,), conv.io_dtype)
-    _expect("weight", weight, conv.width * ch, SEED_F32)
-    _expect("bias", bias, ch, SEED_F32)
-    _expect("window_in", window_in, n, conv.io_dtype)
-    _expect("window_out", window_out, n, conv.io_dtype)
-    return xs, ys
+    def _call(self, fn_name, stream, args):
+        if stream is None:
+            stream = _RAW_STREAM(self.device) if self.device >= 0 else None
+        elif not isinstance(stream, int):
+            stream = stream.cuda_stream
+        status = getattr(LIB, fn_name)(*args, stream)
+        if status != SEED_OK:
+            raise SeedError(fn_name, status)
 
 
 def seed_prefill_conv(conv: seed_conv, x, offsets, weight, bias, window_out, y, window_in=None, stream=None) -> None:
@@ -597,28 +613,29 @@ def seed_prefill_conv(conv: seed_conv, x, offsets, weight, bias, window_out, y, 
     offsets int32 [batch + 1] on the device, weight float [width, channels], bias float [channels] or
     None; window_in / window_out [batch, width - 1, channels] hold the inputs before and the last
     inputs of each sequence (window_in None: zeros)."""
-    import torch
-    tokens = x.shape[0]
-    xs, ys = _expect_conv(conv, x, weight, bias, window_in, window_out, y, tokens)
-    _expect_index("offsets", offsets, conv.batch + 1, torch.int32)
-    with _Launch(stream, (x, offsets, weight, bias, window_in, window_out, y)) as st:
-        _check("seed_prefill_conv", LIB.seed_prefill_conv(
-            ctypes.byref(conv), tokens, _ptr(offsets), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(window_in),
-            _ptr(window_out), _ptr(y), ys, st))
+    torch, io = _io()
+    a, dt, ch, f32 = _Args(torch), io.get(conv.io_dtype), conv.channels, torch.float32
+    shape, n = (x.shape[0], ch), conv.batch * (conv.width - 1) * ch
+    xp, xs = a.rows("x", x, shape, ch, dt)
+    yp, ys = a.rows("y", y, shape, ch, dt)
+    a.launch("seed_prefill_conv", stream, ctypes.byref(conv), shape[0], a.dense("offsets", offsets, conv.batch + 1, torch.int32),
+             xp, xs, a.dense("weight", weight, conv.width * ch, f32), a.dense("bias", bias, ch, f32),
+             a.dense("window_in", window_in, n, dt), a.dense("window_out", window_out, n, dt), yp, ys)
 
 
 def seed_decode_conv(conv: seed_conv, x, weight, bias, window, y, window_out=None, active=None, stream=None) -> None:
     """The short causal convolution of one token per request: x, y [batch, channels]; window
     [batch, width - 1, channels] gives the inputs before and moves up by one token, in place or into
     window_out; active (uint8 [batch] on the device, or None for all) masks requests out."""
-    import torch
-    out = window if window_out is None else window_out
-    xs, ys = _expect_conv(conv, x, weight, bias, window, out, y, conv.batch)
-    _expect_index("active", active, conv.batch, torch.uint8)
-    with _Launch(stream, (x, weight, bias, window, out, active, y)) as st:
-        _check("seed_decode_conv", LIB.seed_decode_conv(
-            ctypes.byref(conv), _ptr(active), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(window), _ptr(out),
-            _ptr(y), ys, st))
+    torch, io = _io()
+    a, dt, ch, f32 = _Args(torch), io.get(conv.io_dtype), conv.channels, torch.float32
+    shape, n = (conv.batch, ch), conv.batch * (conv.width - 1) * ch
+    xp, xs = a.rows("x", x, shape, ch, dt)
+    yp, ys = a.rows("y", y, shape, ch, dt)
+    win = a.dense("window", window, n, dt)
+    out = win if window_out is None else a.dense("window_out", window_out, n, dt)
+    a.launch("seed_decode_conv", stream, ctypes.byref(conv), a.dense("active", active, conv.batch, torch.uint8), xp, xs,
+             a.dense("weight", weight, conv.width * ch, f32), a.dense("bias", bias, ch, f32), win, out, yp, ys)
 
 
 def seed_prefill_workspace_bytes(shape: seed_shape, prompt: seed_prompt) -> int:
@@ -632,36 +649,32 @@ def seed_prefill_scan(shape: seed_shape, offsets, q, k, v, beta, g, S, o, S0=Non
     states after the last tokens, from S0 (None: zeros; S itself: in place). ws: a workspace of
     seed_prefill_workspace_bytes bytes; without one, one is taken from torch's allocator when the
     call needs it."""
-    import torch
+    torch, io = _io()
     if q.dim() != 3:
         raise ValueError(f"q: expected [tokens, key_heads, d_k], got {tuple(q.shape)}")
-    tokens, kh = q.shape[0], q.shape[1]
-    if kh < 1 or shape.heads % kh != 0:
-        raise ValueError(f"q: {kh} key heads do not divide {shape.heads} heads")
-    qs = _expect_rows("q", q, tokens, (kh, shape.d_k), shape.io_dtype)
-    ks = _expect_rows("k", k, tokens, (kh, shape.d_k), shape.io_dtype)
-    vs = _expect_rows("v", v, tokens, (shape.heads, shape.d_v), shape.io_dtype)
-    os_ = _expect_rows("o", o, tokens, (shape.heads, shape.d_v), shape.io_dtype)
-    n = tokens * shape.heads
-    _expect("beta", beta, n, SEED_F32)
-    _expect("g", g, n * (shape.d_k if shape.kind == SEED_KDA else 1), SEED_F32)
-    _expect("S", S, shape.units * shape.d_k * shape.d_v, SEED_F32)
-    _expect("S0", S0, shape.units * shape.d_k * shape.d_v, SEED_F32)
-    _expect_index("offsets", offsets, shape.batch + 1, torch.int32)
-    prompt = seed_prompt(tokens, offsets.data_ptr(), kh, qs, ks, vs, os_)
-    with _Launch(stream, (offsets, q, k, v, beta, g, S, o, S0, ws)) as st:
-        need = seed_prefill_workspace_bytes(shape, prompt)
-        if ws is None and need > 0:
-            if stream is not None:  # made on the stream that uses it, so that its reuse is ordered behind
-                on = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-                with torch.cuda.stream(on):
-                    ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-            else:
-                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-        _check("seed_prefill_scan", LIB.seed_prefill_scan(
-            ctypes.byref(shape), ctypes.byref(prompt), _ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(S0),
-            _ptr(S), _ptr(o), _ptr(ws), ws_bytes, st))
+    a, dt, f32 = _Args(torch), io.get(shape.io_dtype), torch.float32
+    tokens, kh, heads, dk, dv = q.shape[0], q.shape[1], shape.heads, shape.d_k, shape.d_v
+    if kh < 1 or heads % kh != 0:
+        raise ValueError(f"q: {kh} key heads do not divide {heads} heads")
+    ks, vs, n, sn = (tokens, kh, dk), (tokens, heads, dv), tokens * heads, shape.units * dk * dv
+    qp, q_stride = a.rows("q", q, ks, kh * dk, dt)
+    kp, k_stride = a.rows("k", k, ks, kh * dk, dt)
+    vp, v_stride = a.rows("v", v, vs, heads * dv, dt)
+    op, o_stride = a.rows("o", o, vs, heads * dv, dt)
+    prompt = seed_prompt(tokens, a.dense("offsets", offsets, shape.batch + 1, torch.int32), kh, q_stride, k_stride,
+                         v_stride, o_stride)
+    ptrs = (qp, kp, vp, a.dense("beta", beta, n, f32), a.dense("g", g, n * dk if shape.kind == SEED_KDA else n, f32),
+            a.dense("S0", S0, sn, f32), a.dense("S", S, sn, f32), op)
+    sp, pp = ctypes.byref(shape), ctypes.byref(prompt)
+    if ws is None:
+        need = LIB.seed_prefill_workspace_bytes(sp, pp)
+        if need > 0:
+            # made on the stream that uses it, so that its memory's next use is ordered behind
+            on = torch.cuda.ExternalStream(stream, device=a.device) if isinstance(stream, int) else stream
+            with torch.cuda.device(a.device), torch.cuda.stream(on):
+                ws = torch.empty(need, dtype=torch.uint8, device=a.device)
+    size = 0 if ws is None else ws.numel() * ws.element_size()
+    a.launch("seed_prefill_scan", stream, sp, pp, *ptrs, None if ws is None else a.dense("ws", ws, ws.numel(), ws.dtype), size)
 
 
 def seed_norm_rows(x, weight, y, gate=None, eps: float = 1e-6, gate_first: bool = False, skip=None, skip_scale=None,
@@ -669,21 +682,24 @@ def seed_norm_rows(x, weight, y, gate=None, eps: float = 1e-6, gate_first: bool 
     """The head norm of rows x [rows, heads, dim] into y: with x + skip_scale[h] * skip in the place
     of x when skip is given (written to total, unless None), weight [heads, dim] times u / sqrt(mean
     u^2 + eps), times silu(gate) after, or u = x silu(gate) when gate_first."""
-    import torch
-    if x.dim() != 3:
-        raise ValueError(f"x: expected [rows, heads, dim], got {tuple(x.shape)}")
-    rows, heads, dim = x.shape
-    code = {torch.float32: SEED_F32, torch.bfloat16: SEED_BF16}.get(x.dtype)
-    if code is None:
-        raise ValueError(f"x: expected dtype float32 or bfloat16, got {x.dtype}")
-    strides = [_expect_rows(n, t, rows, (heads, dim), code)
-               for n, t in (("x", x), ("y", y), ("gate", gate), ("skip", skip), ("total", total))]
-    _expect("weight", weight, heads * dim, SEED_F32)
-    _expect("skip_scale", skip_scale, heads, SEED_F32)
-    shape = seed_rows(rows, heads, dim, code, *strides)
-    norm = seed_head_norm(None if weight is None else weight.data_ptr(), None if gate is None else gate.data_ptr(),
-                          float(eps), int(gate_first))
-    res = seed_residual(*(None if t is None else t.data_ptr() for t in (skip, skip_scale, total)))
-    with _Launch(stream, (x, weight, y, gate, skip, skip_scale, total)) as st:
-        _check("seed_norm_rows", LIB.seed_norm_rows(ctypes.byref(shape), _ptr(x), ctypes.byref(norm),
-                                                    ctypes.byref(res), _ptr(y), st))
+    torch, _ = _io()
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError(f"x: expected [rows, heads, dim], got {tuple(shape)}")
+    rows, heads, dim = shape
+    dt, f32 = x.dtype, torch.float32
+    if dt is not torch.bfloat16 and dt is not f32:
+        raise ValueError(f"x: expected dtype float32 or bfloat16, got {dt}")
+    a, width = _Args(torch), heads * dim
+    xp, xs = a.rows("x", x, shape, width, dt)
+    yp, ys = a.rows("y", y, shape, width, dt)
+    gp, gs = a.rows("gate", gate, shape, width, dt)
+    sp, ss = a.rows("skip", skip, shape, width, dt)
+    tp, ts = a.rows("total", total, shape, width, dt)
+    norm = seed_head_norm(a.dense("weight", weight, width, f32), gp, eps, 1 if gate_first else 0)
+    res = None
+    if skip is not None or total is not None or skip_scale is not None:
+        res = ctypes.byref(seed_residual(sp, a.dense("skip_scale", skip_scale, heads, f32), tp))
+    a.launch("seed_norm_rows", stream, ctypes.byref(seed_rows(rows, heads, dim, SEED_F32 if dt is f32 else SEED_BF16, xs, ys,
+                                                              gs, ss, ts)),
+             xp, ctypes.byref(norm), res, yp)
