@@ -38,6 +38,7 @@ struct ScanArgs {
   const float* S0;         // [batch][heads][d_k][d_v] or nullptr (zeros)
   float* S;
   void* o;                 // [tokens][heads][d_v]
+  void* ws;                // of prefill_scan_workspace bytes
 };
 
 struct NormArgs {
@@ -58,8 +59,10 @@ struct NormArgs {
 hipError_t launch_prefill_conv(const seed_conv& c, const ConvArgs& a, hipStream_t s);
 hipError_t launch_decode_conv(const seed_conv& c, const ConvArgs& a, hipStream_t s);
 hipError_t launch_prefill_scan(const seed_shape& sh, const ScanArgs& a, hipStream_t s);
+size_t prefill_scan_workspace(const seed_shape& sh, const seed_prompt& p);
 // The chunked scan on the matrix cores: bf16 io, scalar gates (GDN, Mamba-2).
 hipError_t launch_scan_chunk(const seed_shape& sh, const ScanArgs& a, hipStream_t s);
+size_t scan_chunk_workspace(const seed_shape& sh, int64_t tokens);
 hipError_t launch_norm_rows(int32_t io_dtype, const NormArgs& a, hipStream_t s);
 
 // Whether p and a row stride (in elements of `bytes`) let every row be accessed 16 bytes at a time.

@@ -143,7 +143,7 @@ int seed_decode_conv(const seed_conv* conv, const uint8_t* active, const void* x
 
 size_t seed_prefill_workspace_bytes(const seed_shape* sh, const seed_prompt* prompt) {
   if (check_scan(sh, prompt) != SEED_OK) return 0;
-  return 0;
+  return seed::prefill_scan_workspace(*sh, *prompt);
 }
 
 int seed_prefill_scan(const seed_shape* sh, const seed_prompt* prompt, const void* q, const void* k, const void* v,
@@ -167,6 +167,13 @@ int seed_prefill_scan(const seed_shape* sh, const seed_prompt* prompt, const voi
     return SEED_ERR_ARG;
   const size_t need = seed_prefill_workspace_bytes(sh, prompt);
   if (need > 0 && (!ws || ws_bytes < need)) return SEED_ERR_WORKSPACE;
+  if (need > 0) {
+    if (!aligned(ws, 16)) return SEED_ERR_ARG;
+    const int64_t nb = static_cast<int64_t>(need), gw = static_cast<int64_t>(sh->heads) * 4 * (sh->kind == SEED_KDA ? sh->d_k : 1);
+    const Rows rw{ws, 1, nb, nb}, rb{beta, 1, n * sh->heads * 4, n * sh->heads * 4}, rg{g, 1, n * gw, n * gw};
+    for (const Rows& r : {rq, rk, rv, ro, s0, s1, rb, rg})
+      if (overlap(rw, r)) return SEED_ERR_ARG;
+  }
   seed::ScanArgs a{};
   a.tokens = n;
   a.batch = sh->batch;
@@ -185,6 +192,7 @@ int seed_prefill_scan(const seed_shape* sh, const seed_prompt* prompt, const voi
   a.S0 = S0;
   a.S = S;
   a.o = o;
+  a.ws = ws;
   return hip_status(seed::launch_prefill_scan(*sh, a, static_cast<hipStream_t>(stream)));
 }
 

@@ -146,9 +146,26 @@ ScanFn pick_scan(const seed_shape& sh) {
 
 }  // namespace
 
+namespace {
+// Whether the chunked kernel takes the call: bf16 rows and a gate per head, prompts that fill chunks,
+// and rows near enough for 32 of them to lie within a 31-bit offset.
+bool takes_chunks(const seed_shape& sh, int64_t tokens, int64_t longest_stride) {
+  return sh.io_dtype == SEED_BF16 && sh.kind != SEED_KDA && tokens >= 16 * static_cast<int64_t>(sh.batch) &&
+         longest_stride < (int64_t{1} << 24);
+}
+int64_t longest(int64_t a, int64_t b, int64_t c, int64_t d) {
+  const int64_t x = a > b ? a : b, y = c > d ? c : d;
+  return x > y ? x : y;
+}
+}  // namespace
+
+size_t prefill_scan_workspace(const seed_shape& sh, const seed_prompt& p) {
+  if (!takes_chunks(sh, p.tokens, longest(p.q_stride, p.k_stride, p.v_stride, p.o_stride))) return 0;
+  return scan_chunk_workspace(sh, p.tokens);
+}
+
 hipError_t launch_prefill_scan(const seed_shape& sh, const ScanArgs& a, hipStream_t s) {
-  if (sh.io_dtype == SEED_BF16 && sh.kind != SEED_KDA && a.tokens >= 16 * static_cast<int64_t>(a.batch))
-    return launch_scan_chunk(sh, a, s);
+  if (takes_chunks(sh, a.tokens, longest(a.q_stride, a.k_stride, a.v_stride, a.o_stride))) return launch_scan_chunk(sh, a, s);
   const int64_t units = static_cast<int64_t>(a.batch) * a.heads;
   hipLaunchKernelGGL(pick_scan(sh), dim3(loop_blocks(units * (sh.d_v / 64))), dim3(kThreads), 0, s, a, units);
   return hipGetLastError();

@@ -40,6 +40,15 @@ using s16x4 = __attribute__((ext_vector_type(4))) short;
 using lds_s16x4 = __attribute__((address_space(3))) s16x4;
 
 constexpr int C = 32;       // tokens per chunk
+// Long prompts of few units, cut into segments (plan_split).
+struct Split {
+  int32_t pass;    // 0: whole sequences; 1: every segment's A and B; 2: the read-outs
+  int32_t tokens;  // of a segment, a multiple of C
+  int64_t slots;   // segments at most
+  float* A;        // [slots][heads][d_k][d_k]
+  float* B;        // [slots][heads][d_k][d_v]
+};
+
 constexpr int kRanked = 512;  // sequences that are put in order of length
 constexpr int LT = C + 8;   // row length of the T and P pieces
 constexpr int LF = 16 + 4;  // row length of the fp32 block of T
@@ -371,10 +380,43 @@ __device__ __forceinline__ int ranked_sequence(const ScanArgs& A, int rank, int3
   return found;
 }
 
+// Segments of a sequence with `rows` rows.
+__device__ __forceinline__ int segments_of(const Split& W, int64_t rows) {
+  return rows > W.tokens ? static_cast<int>((rows + W.tokens - 1) / W.tokens) : 1;
+}
+// The sequence, the segment and its rows that slot `slot` stands for, the sequences' segments counted one
+// after the other; A.batch when there are fewer. The same for all threads.
+__device__ __forceinline__ int find_segment(const ScanArgs& A, const Split& W, int64_t slot, int64_t& lo, int64_t& hi,
+                                            int& seg, int& segs) {
+  int b = 0;
+  for (; b < A.batch; ++b) {
+    sequence_rows(A.offsets, b, A.tokens, lo, hi);
+    segs = segments_of(W, hi - lo);
+    if (slot < segs) break;
+    slot -= segs;
+  }
+  seg = static_cast<int>(slot);
+  if (b < A.batch) {
+    lo += seg * static_cast<int64_t>(W.tokens);
+    if (hi > lo + W.tokens) hi = lo + W.tokens;
+  }
+  return __builtin_amdgcn_readfirstlane(b);
+}
+// Sequence b's first slot, number of segments and rows.
+__device__ __forceinline__ int first_segment(const ScanArgs& A, const Split& W, int b, int64_t& base, int64_t& lo, int64_t& hi) {
+  base = 0;
+  for (int i = 0; i < b; ++i) {
+    sequence_rows(A.offsets, i, A.tokens, lo, hi);
+    base += segments_of(W, hi - lo);
+  }
+  sequence_rows(A.offsets, b, A.tokens, lo, hi);
+  return segments_of(W, hi - lo);
+}
+
 // Wavefronts 0 .. NW - 1 hold 32 columns of the state each and run a chunk while the NH others prepare:
 // T and P of the next chunk, and rows and gates of the one after it.
 template <int KIND, int DK, int DV>
-__global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, int64_t units) {
+__global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, const Split W, int64_t items) {
   using TL = Tiles<KIND, DK, DV>;
   constexpr bool DELTA = TL::DELTA;
   constexpr int NW = DV / 32, NH = NW, NT = (NW + NH) * 64;
@@ -391,13 +433,43 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, int6
       sh.T[i / 768][i / 256 % 3][(i / 16 % 16) * LT + 16 + i % 16] = 0;
   }
 
-  for (int64_t item = blockIdx.x; item < units; item += gridDim.x) {
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int h = static_cast<int>(item % A.heads);
-    const int b = __builtin_amdgcn_readfirstlane(ranked_sequence<NT>(A, static_cast<int>(item / A.heads), sh.len, sh.found));
-    const int64_t unit = static_cast<int64_t>(b) * A.heads + h;
+    int b;                       // sequence
+    int64_t lo, hi;              // its rows to run over
+    const float* init = nullptr; // the state to start from (nullptr: zeros, or the identity when v counts as zero)
+    float* dest;                 // where the state goes (nullptr: nowhere)
+    bool out = true, has_v = true;  // without read-outs, q and P are whatever LDS holds and o is dropped
+    if (W.pass == 0) {
+      b = __builtin_amdgcn_readfirstlane(ranked_sequence<NT>(A, static_cast<int>(item / A.heads), sh.len, sh.found));
+      sequence_rows(A.offsets, b, A.tokens, lo, hi);
+      const int64_t at = (static_cast<int64_t>(b) * A.heads + h) * (DK * DV);
+      if (A.S0 != nullptr) init = A.S0 + at;
+      dest = A.S + at;
+    } else {
+      int64_t slot = item / A.heads;
+      if (DELTA && W.pass == 1) {
+        has_v = (slot & 1) == 0;
+        slot >>= 1;
+      }
+      int seg, segs;
+      b = find_segment(A, W, slot, lo, hi, seg, segs);
+      if (b >= A.batch) continue;
+      const int64_t at = (static_cast<int64_t>(b) * A.heads + h) * (DK * DV), in_ws = (slot * A.heads + h) * (DK * DV);
+      const bool last = seg == segs - 1;
+      if (W.pass == 1) {
+        // the first segment is run for good; of the others all but the last leave their matrices
+        if (seg == 0 ? !has_v : last) continue;
+        if (seg == 0 && A.S0 != nullptr) init = A.S0 + at;
+        out = seg == 0;
+        dest = seg == 0 && last ? A.S + at : (has_v ? W.B : W.A) + in_ws;
+      } else {
+        if (seg == 0) continue;
+        init = W.B + in_ws - static_cast<int64_t>(A.heads) * (DK * DV);
+        dest = last ? A.S + at : nullptr;
+      }
+    }
     const int kh = h / (A.heads / A.key_heads);
-    int64_t lo, hi;
-    sequence_rows(A.offsets, b, A.tokens, lo, hi);
     lo = __builtin_amdgcn_readfirstlane(static_cast<int>(lo));  // rows are below 2^31
     hi = __builtin_amdgcn_readfirstlane(static_cast<int>(hi));
     const int n = static_cast<int>((hi - lo + C - 1) / C);  // chunks
@@ -416,8 +488,8 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, int6
         if (role == kG) load_gates(A, h, f0, hi, g, beta);
         if (role == kK) fetch_tile<DK>(kp, A.k_stride, f0, hi, sh.K[to]);
         if (role == kQV) {
-          fetch_tile<DK>(qp, A.q_stride, f0, hi, sh.Q[to]);
-          fetch_tile<DV>(vp, A.v_stride, f0, hi, sh.V[to]);
+          if (out) fetch_tile<DK>(qp, A.q_stride, f0, hi, sh.Q[to]);
+          fetch_tile<DV>(vp, A.v_stride, f0, has_v ? hi : f0, sh.V[to]);
         }
         if (role == kG) sum_gates(sh.gates[to], g, beta);
       };
@@ -431,7 +503,7 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, int6
           if constexpr (DELTA) {
             if (role == kT) form_T<DK>(sh.K[next], sh.gates[next], sh.T[(j + 1) & 1], sh.T11);
           }
-          if (role == kP) form_P<DELTA, DK>(sh.K[next], sh.Q[next], sh.gates[next], sh.P[(j + 1) & 1]);
+          if (role == kP && out) form_P<DELTA, DK>(sh.K[next], sh.Q[next], sh.gates[next], sh.P[(j + 1) & 1]);
         }
         wait_loads<0>();
         __syncthreads();
@@ -445,16 +517,22 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, int6
     f32x16 S[RT];
     constexpr int SB = DK * DV * 4;
     const int s_at = (8 * ((threadIdx.x & 63) >> 5) * DV + 32 * wave + (threadIdx.x & 31)) * 4;
-    if (A.S0 != nullptr) {
-      const auto sr = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(A.S0 + unit * DK * DV), 0, SB, 0x00027000);
+    {
+      // without a state to start from, the loads are outside their buffer and give zeros
+      const auto sr = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(init), 0, init != nullptr ? SB : 0, 0x00027000);
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           S[r][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sr, s_at, (32 * r + 16 * (i / 8) + i % 8) * DV * 4, 0));
-    } else {
+    }
+    if constexpr (DELTA) {
+      // the identity: the lane's column meets the diagonal in one register of one half
+      const int at = has_v ? -1 : 32 * wave + (threadIdx.x & 31) - 8 * ((threadIdx.x & 63) >> 5);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) S[r] = f32x16{};
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[r][i] = at == 32 * r + 16 * (i / 8) + i % 8 ? 1.f : S[r][i];
     }
     __syncthreads();  // chunk 0's rows and gates
     __syncthreads();  // its T and P
@@ -638,7 +716,7 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, int6
       }
       // ---- the read-outs: a wavefront's 32 columns of a row are 64 bytes, 16 per lane ----------------
       wave_lds_sync();
-      const auto orow = chunk_rows(op, A.o_stride, c0, hi, DV * 2);  // stores behind the last row are dropped
+      const auto orow = chunk_rows(op, A.o_stride, c0, out ? hi : c0, DV * 2);  // stores outside are dropped
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int o_at = (lane / 4 * static_cast<int>(A.o_stride) + 32 * wave + 8 * (lane & 3)) * 2;
@@ -648,7 +726,7 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, int6
       __syncthreads();
     }
 
-    const auto sr = __builtin_amdgcn_make_buffer_rsrc(A.S + unit * DK * DV, 0, SB, 0x00027000);
+    const auto sr = __builtin_amdgcn_make_buffer_rsrc(dest, 0, dest != nullptr ? SB : 0, 0x00027000);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -657,9 +735,79 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, int6
   }
 }
 
+// Between the passes: the states before the segments. B of a sequence's first segment is the state
+// after it; S_seg = A_seg S_(seg - 1) + B_seg takes the place of B_seg, up to the last segment but one.
+// A workgroup has 32 columns of one unit, a wavefront 32 rows of them; fp32 matrix instructions.
+template <int DK, int DV>
+__global__ __launch_bounds__(DK * 2) void k_join_delta(const ScanArgs A, const Split W) {
+  constexpr int LS = 32 + 1;
+  __shared__ float Sh[DK * LS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, half = lane >> 5;
+  const int h = blockIdx.x / (DV / 32) % A.heads, b = blockIdx.x / (DV / 32) / A.heads;
+  const int col = blockIdx.x % (DV / 32) * 32 + l32;
+  int64_t base, lo, hi;
+  const int segs = first_segment(A, W, b, base, lo, hi);
+  for (int seg = 0; seg + 1 < segs && base + seg < W.slots; ++seg) {
+    float* Bs = W.B + ((base + seg) * A.heads + h) * (DK * DV);
+    f32x16 acc;  // register i is row 32 wave + 8 (i / 4) + 4 half + i % 4
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = Bs[static_cast<int64_t>(32 * wave + 8 * (i / 4) + 4 * half + i % 4) * DV + col];
+    if (seg > 0) {
+      const float* As = W.A + ((base + seg) * A.heads + h) * (DK * DK) + (32 * wave + l32) * DK + 4 * half;
+#pragma unroll
+      for (int k = 0; k < DK; k += 8) {  // k slot `half` of step i is row k + 4 half + i
+        const f32x4 a = *reinterpret_cast<const f32x4*>(As + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], Sh[(k + 4 * half + i) * LS + l32], acc, 0, 0, 0);
+      }
+      __syncthreads();  // the old state has been read
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int row = 32 * wave + 8 * (i / 4) + 4 * half + i % 4;
+      Sh[row * LS + l32] = acc[i];
+      if (seg > 0) Bs[static_cast<int64_t>(row) * DV + col] = acc[i];
+    }
+    __syncthreads();
+  }
+}
+
+// The same where A_seg is the product of the segment's gates.
+template <int DK, int DV>
+__global__ __launch_bounds__(256) void k_join_scalar(const ScanArgs A, const Split W) {
+  constexpr int N = DK * DV / 256;
+  __shared__ double part[4];
+  const int h = blockIdx.x % A.heads, b = blockIdx.x / A.heads;
+  int64_t base, lo, hi;
+  const int segs = first_segment(A, W, b, base, lo, hi);
+  float S[N];
+  for (int seg = 0; seg + 1 < segs && base + seg < W.slots; ++seg) {
+    float* Bs = W.B + ((base + seg) * A.heads + h) * (DK * DV);
+    float a = 0.f;
+    if (seg > 0) {
+      const int64_t from = lo + seg * static_cast<int64_t>(W.tokens);  // not the last segment: all its rows exist
+      double c = 0;
+      for (int t = threadIdx.x; t < W.tokens; t += 256) c += static_cast<double>(log2f(A.g[(from + t) * A.heads + h]));
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) c += __shfl_xor(c, d, 64);
+      __syncthreads();
+      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = c;
+      __syncthreads();
+      a = static_cast<float>(exp2((part[0] + part[1]) + (part[2] + part[3])));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = Bs[i * 256 + threadIdx.x];
+      S[i] = seg > 0 ? fmaf(a, S[i], x) : x;
+      if (seg > 0) Bs[i * 256 + threadIdx.x] = S[i];
+    }
+  }
+}
+
 namespace {
 
-using ChunkFn = void (*)(const ScanArgs, int64_t);
+using ChunkFn = void (*)(const ScanArgs, const Split, int64_t);
 
 template <int KIND>
 ChunkFn pick_dims(int dk, int dv) {
@@ -667,12 +815,70 @@ ChunkFn pick_dims(int dk, int dv) {
   return dv == 128 ? k_scan_chunk<KIND, 64, 128> : k_scan_chunk<KIND, 64, 64>;
 }
 
+constexpr int64_t kCUs = 256;
+
+// Few units leave most of the chip idle while each runs its chunks one after the other. Such prompts are
+// cut into segments: the state after a segment is A S + B with S the state before it, so one pass forms
+// A and B of all segments side by side (A: the recurrence from the identity with v = 0; a product of
+// gates for Mamba-2), the states between them follow, and a second pass gives the read-outs.
+// With n segments that is 2 (Mamba-2) or 3 (GDN: A and B are two runs) n-ths of the serial time when
+// slots / units = n - 1 segments fill the chip at once; @@figures@@
+Split plan_split(const seed_shape& sh, int64_t tokens) {
+  Split w{};
+  const bool delta = sh.kind != SEED_MAMBA2;
+  const int64_t units = static_cast<int64_t>(sh.batch) * sh.heads, mean = tokens / sh.batch;
+  const int64_t slots = kCUs * (!delta && sh.d_v == 64 ? 2 : 1);  // workgroups that fit the chip at once
+  const int64_t n = slots / units + 1;
+  if (delta && sh.d_k != sh.d_v) return w;  // A is run as a state of d_k x d_k
+  if (n < (delta ? 4 : 3) || mean < (delta ? 2048 : 1024)) return w;
+  int64_t seg = (mean + n - 1) / n;
+  seg = (seg < 256 ? 256 : seg) + C - 1;
+  w.tokens = static_cast<int32_t>(seg / C * C);
+  w.slots = tokens / w.tokens + sh.batch;
+  return w;
+}
+
+int64_t split_floats(const seed_shape& sh, const Split& w) {  // of A, and of B
+  return w.slots * sh.heads * sh.d_k * sh.d_v;
+}
+
+template <int DK, int DV>
+void join(const seed_shape& sh, const ScanArgs& a, const Split& w, hipStream_t s) {
+  const unsigned units = static_cast<unsigned>(a.batch * a.heads);
+  if (sh.kind == SEED_MAMBA2) k_join_scalar<DK, DV><<<dim3(units), dim3(256), 0, s>>>(a, w);
+  else k_join_delta<DK, DV><<<dim3(units * (DV / 32)), dim3(DK * 2), 0, s>>>(a, w);
+}
+
 }  // namespace
 
+size_t scan_chunk_workspace(const seed_shape& sh, int64_t tokens) {
+  const Split w = plan_split(sh, tokens);
+  return static_cast<size_t>(split_floats(sh, w)) * sizeof(float) * (sh.kind == SEED_MAMBA2 ? 1 : 2);
+}
+
 hipError_t launch_scan_chunk(const seed_shape& sh, const ScanArgs& a, hipStream_t s) {
-  const int64_t units = static_cast<int64_t>(a.batch) * a.heads;
   const ChunkFn fn = sh.kind == SEED_GDN ? pick_dims<SEED_GDN>(sh.d_k, sh.d_v) : pick_dims<SEED_MAMBA2>(sh.d_k, sh.d_v);
-  hipLaunchKernelGGL(fn, dim3(loop_blocks(units)), dim3(sh.d_v * 4), 0, s, a, units);
+  const dim3 threads(sh.d_v * 4);
+  Split w = plan_split(sh, a.tokens);
+  if (w.slots == 0) {
+    const int64_t units = static_cast<int64_t>(a.batch) * a.heads;
+    hipLaunchKernelGGL(fn, dim3(loop_blocks(units)), threads, 0, s, a, w, units);
+    return hipGetLastError();
+  }
+  const bool delta = sh.kind != SEED_MAMBA2;
+  w.B = static_cast<float*>(a.ws);
+  w.A = w.B + split_floats(sh, w);  // GDN only
+  const int64_t items = w.slots * a.heads;
+  w.pass = 1;
+  hipLaunchKernelGGL(fn, dim3(loop_blocks(items * (delta ? 2 : 1))), threads, 0, s, a, w, items * (delta ? 2 : 1));
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (sh.d_k == 128) sh.d_v == 128 ? join<128, 128>(sh, a, w, s) : join<128, 64>(sh, a, w, s);
+  else sh.d_v == 128 ? join<64, 128>(sh, a, w, s) : join<64, 64>(sh, a, w, s);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  w.pass = 2;
+  hipLaunchKernelGGL(fn, dim3(loop_blocks(items)), threads, 0, s, a, w, items);
   return hipGetLastError();
 }
 

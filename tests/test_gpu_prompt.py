@@ -316,6 +316,62 @@ def test_scan_neighbours(kind, dtype):
     assert not torch.isfinite(S[1]).all()
 
 
+@pytest.mark.parametrize("kind", [ref.GDN, ref.MAMBA2])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (128, 64), (64, 128)])
+@pytest.mark.parametrize("carry", [False, True])
+def test_scan_of_few_long_prompts(kind, dk, dv, carry):
+    """Prompts long and few enough to be cut into segments (equal and ragged ones, with empty and
+    short sequences between), the states in place."""
+    rrs, torch = _rrs()
+    for lens in ([2600], [5000, 0, 1], [2100, 6000, 40, 2500]):
+        heads = 2
+        g = _gen(torch, dk + dv + len(lens))
+        t = _scan_inputs(torch, g, kind, sum(lens), heads, 1, dk, dv, "bf16")
+        S0 = torch.randn(len(lens), heads, dk, dv, device="cuda", generator=g) if carry else None
+        want = ref.scan(kind, lens, *map(_np, t), _np(S0))
+        o, S = _run_scan(rrs, torch, kind, lens, t, S0, (heads, dk, dv), "bf16", S=S0)
+        _check_scan(_np(o), _np(S), want, "bf16")
+
+
+@pytest.mark.parametrize("kind", [ref.GDN, ref.MAMBA2])
+@pytest.mark.parametrize("where", [5, 40, 1500, 2999])
+def test_scan_is_causal_for_values_that_are_not_finite(kind, where):
+    """What is not finite at a token leaves the read-outs before it as they were, in the token's own
+    chunk and segment too: v and k, beta and the gate in turn."""
+    rrs, torch = _rrs()
+    heads, dk, dv, n = 1, 128, 64, 3000
+    t = _scan_inputs(torch, _gen(torch, 47), kind, n, heads, 1, dk, dv, "bf16")
+    want, _, mag = ref.scan(kind, [n], *map(_np, t), None)
+    for which, value in ((2, float("inf")), (1, float("nan")), (3, float("inf")), (4, float("nan")), (2, float("nan"))):
+        bad = [x.clone() for x in t]
+        bad[which][where] = value
+        o, S = _run_scan(rrs, torch, kind, [n], tuple(bad), None, (heads, dk, dv), "bf16")
+        got = _np(o[:where])
+        _close(got, want[:where], HALF["bf16"] * np.abs(want[:where]) + 3e-5 * mag[:where, :, None])
+        assert not torch.isfinite(S).all()
+
+
+def test_scan_workspaces():
+    """A given workspace, one of torch's allocator, and one that is too small or misaligned."""
+    rrs, torch = _rrs()
+    heads, dk, dv, n = 1, 64, 64, 2600
+    t = _scan_inputs(torch, _gen(torch, 53), ref.GDN, n, heads, 1, dk, dv, "bf16")
+    shape = rrs.make_shape(rrs.SEED_GDN, 1, heads, dk, dv, 8, 8, rrs.SEED_BF16)
+    need = rrs.seed_prefill_workspace_bytes(shape, rrs.seed_prompt(n, None, 1, dk, dk, dv, dv))
+    assert need > 0
+    assert rrs.seed_prefill_workspace_bytes(shape, rrs.seed_prompt(64, None, 1, dk, dk, dv, dv)) == 0
+    o0, S0 = _run_scan(rrs, torch, ref.GDN, [n], t, None, (heads, dk, dv), "bf16")
+    ws = torch.full((need + 16,), 255, dtype=torch.uint8, device="cuda")
+    o1, S1 = _run_scan(rrs, torch, ref.GDN, [n], t, None, (heads, dk, dv), "bf16", ws=ws[:need])
+    assert torch.equal(o0, o1) and torch.equal(S0, S1) and (ws[need:] == 255).all()
+    with pytest.raises(rrs.SeedError) as e:
+        _run_scan(rrs, torch, ref.GDN, [n], t, None, (heads, dk, dv), "bf16", ws=ws[:need - 1])
+    assert e.value.status == rrs.SEED_ERR_WORKSPACE
+    with pytest.raises(rrs.SeedError) as e:
+        _run_scan(rrs, torch, ref.GDN, [n], t, None, (heads, dk, dv), "bf16", ws=ws[1:need + 1])
+    assert e.value.status == rrs.SEED_ERR_ARG
+
+
 def test_scan_wrong_offsets_stay_inside():
     """Offsets that decrease or leave the buffer give clamped sequences and touch nothing else."""
     rrs, torch = _rrs()
