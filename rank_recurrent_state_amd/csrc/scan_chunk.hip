@@ -45,7 +45,7 @@ struct Split {
   int32_t pass;    // 0: whole sequences; 1: every segment's A and B; 2: the read-outs
   int32_t tokens;  // of a segment, a multiple of C
   int64_t slots;   // segments at most
-  float* A;        // [slots][heads][d_k][d_k]
+  float* A;        // [slots][heads][d_k][d_k]; Mamba-2: [slots][heads], the product of the segment's gates
   float* B;        // [slots][heads][d_k][d_v]
 };
 
@@ -210,7 +210,8 @@ __device__ __forceinline__ void fetch_tile(const uint16_t* base, int64_t stride,
   }
 }
 
-// The gates of the chunk at f0: log2 g summed over the chunk, and the weights that follow.
+// The gates of the chunk at f0: log2 g summed over the chunk, and the weights that follow. sum_gates
+// returns the chunk's whole sum.
 __device__ __forceinline__ void load_gates(const ScanArgs& A, int h, int64_t f0, int64_t hi, float& g, float& beta) {
   const int64_t f1 = f0 + (threadIdx.x & 31);
   const int64_t at = (f1 < hi ? f1 : hi - 1) * A.heads + h;
@@ -219,7 +220,7 @@ __device__ __forceinline__ void load_gates(const ScanArgs& A, int h, int64_t f0,
   beta = f1 < hi ? b1 : 0.f;
 }
 template <class Gates>
-__device__ __forceinline__ void sum_gates(Gates& G, float g, float beta) {
+__device__ __forceinline__ double sum_gates(Gates& G, float g, float beta) {
   const int l = fresh(threadIdx.x & 63), l32 = l & 31;
   // g = 0 counts as 2^-200: across it every weight underflows to 0, as it should
   const float lg = log2f(g);
@@ -230,7 +231,7 @@ __device__ __forceinline__ void sum_gates(Gates& G, float g, float beta) {
     if (l32 >= d) c += up;
   }
   const float ch = static_cast<float>(c), cl = static_cast<float>(c - static_cast<double>(ch));
-  const double rest = __shfl(c, C - 1, C) - c;
+  const double all = __shfl(c, C - 1, C), rest = all - c;
   const float rh = static_cast<float>(rest), rl = static_cast<float>(rest - static_cast<double>(rh));
   const float eh = exp2f(ch), et = exp2f(rh);
   if (l < C) {
@@ -241,6 +242,7 @@ __device__ __forceinline__ void sum_gates(Gates& G, float g, float beta) {
     G.beta[l] = beta;
     G.g[l] = g;
   }
+  return all;
 }
 
 // 2^(c_t - c_s) for t = l32 and the 16 s of the lane's accumulator registers.
@@ -483,6 +485,7 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, cons
       // ---- helpers ------------------------------------------------------------------------------------
       // chunk j's rows go to buffer `to`; its gates are loaded at once and summed when `sum` is called
       float g = 1.f, beta = 0.f;
+      double decay = 0;  // log2 of the product of all gates
       auto fetch = [&](int j, int to) {
         const int64_t f0 = lo + static_cast<int64_t>(j) * C;
         if (role == kG) load_gates(A, h, f0, hi, g, beta);
@@ -491,7 +494,7 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, cons
           if (out) fetch_tile<DK>(qp, A.q_stride, f0, hi, sh.Q[to]);
           fetch_tile<DV>(vp, A.v_stride, f0, has_v ? hi : f0, sh.V[to]);
         }
-        if (role == kG) sum_gates(sh.gates[to], g, beta);
+        if (role == kG) decay += sum_gates(sh.gates[to], g, beta);
       };
       if (n > 0) fetch(0, 0);
       wait_loads<0>();
@@ -510,6 +513,8 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, cons
         next = far;
         far = far == 2 ? 0 : far + 1;
       }
+      if (!DELTA && W.pass == 1 && role == kG && (threadIdx.x & 63) == 0)
+        W.A[item] = static_cast<float>(exp2(decay));
       continue;
     }
 
@@ -773,35 +778,24 @@ __global__ __launch_bounds__(DK * 2) void k_join_delta(const ScanArgs A, const S
   }
 }
 
-// The same where A_seg is the product of the segment's gates.
+// The same where A_seg is the product of the segment's gates: a thread follows 4 elements of a state.
 template <int DK, int DV>
 __global__ __launch_bounds__(256) void k_join_scalar(const ScanArgs A, const Split W) {
-  constexpr int N = DK * DV / 256;
-  __shared__ double part[4];
-  const int h = blockIdx.x % A.heads, b = blockIdx.x / A.heads;
+  constexpr int PARTS = DK * DV / 1024;
+  const int unit = blockIdx.x / PARTS, h = unit % A.heads, b = unit / A.heads;
+  const int at = blockIdx.x % PARTS * 1024 + 4 * threadIdx.x;
   int64_t base, lo, hi;
   const int segs = first_segment(A, W, b, base, lo, hi);
-  float S[N];
+  f32x4 S = {};
+#pragma unroll 4
   for (int seg = 0; seg + 1 < segs && base + seg < W.slots; ++seg) {
-    float* Bs = W.B + ((base + seg) * A.heads + h) * (DK * DV);
-    float a = 0.f;
-    if (seg > 0) {
-      const int64_t from = lo + seg * static_cast<int64_t>(W.tokens);  // not the last segment: all its rows exist
-      double c = 0;
-      for (int t = threadIdx.x; t < W.tokens; t += 256) c += static_cast<double>(log2f(A.g[(from + t) * A.heads + h]));
+    const int64_t slot = (base + seg) * A.heads + h;
+    f32x4* Bs = reinterpret_cast<f32x4*>(W.B + slot * (DK * DV) + at);
+    const f32x4 x = *Bs;
+    const float a = W.A[slot];
 #pragma unroll
-      for (int d = 32; d > 0; d >>= 1) c += __shfl_xor(c, d, 64);
-      __syncthreads();
-      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = c;
-      __syncthreads();
-      a = static_cast<float>(exp2((part[0] + part[1]) + (part[2] + part[3])));
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float x = Bs[i * 256 + threadIdx.x];
-      S[i] = seg > 0 ? fmaf(a, S[i], x) : x;
-      if (seg > 0) Bs[i * 256 + threadIdx.x] = S[i];
-    }
+    for (int e = 0; e < 4; ++e) S[e] = seg > 0 ? fmaf(a, S[e], x[e]) : x[e];
+    if (seg > 0) *Bs = S;
   }
 }
 
@@ -838,14 +832,15 @@ Split plan_split(const seed_shape& sh, int64_t tokens) {
   return w;
 }
 
-int64_t split_floats(const seed_shape& sh, const Split& w) {  // of A, and of B
-  return w.slots * sh.heads * sh.d_k * sh.d_v;
+int64_t floats_of_B(const seed_shape& sh, const Split& w) { return w.slots * sh.heads * sh.d_k * sh.d_v; }
+int64_t floats_of_A(const seed_shape& sh, const Split& w) {
+  return w.slots * sh.heads * (sh.kind == SEED_MAMBA2 ? 1 : sh.d_k * sh.d_k);
 }
 
 template <int DK, int DV>
 void join(const seed_shape& sh, const ScanArgs& a, const Split& w, hipStream_t s) {
   const unsigned units = static_cast<unsigned>(a.batch * a.heads);
-  if (sh.kind == SEED_MAMBA2) k_join_scalar<DK, DV><<<dim3(units), dim3(256), 0, s>>>(a, w);
+  if (sh.kind == SEED_MAMBA2) k_join_scalar<DK, DV><<<dim3(units * (DK * DV / 1024)), dim3(256), 0, s>>>(a, w);
   else k_join_delta<DK, DV><<<dim3(units * (DV / 32)), dim3(DK * 2), 0, s>>>(a, w);
 }
 
@@ -853,7 +848,7 @@ void join(const seed_shape& sh, const ScanArgs& a, const Split& w, hipStream_t s
 
 size_t scan_chunk_workspace(const seed_shape& sh, int64_t tokens) {
   const Split w = plan_split(sh, tokens);
-  return static_cast<size_t>(split_floats(sh, w)) * sizeof(float) * (sh.kind == SEED_MAMBA2 ? 1 : 2);
+  return static_cast<size_t>(floats_of_B(sh, w) + floats_of_A(sh, w)) * sizeof(float);
 }
 
 hipError_t launch_scan_chunk(const seed_shape& sh, const ScanArgs& a, hipStream_t s) {
@@ -867,7 +862,7 @@ hipError_t launch_scan_chunk(const seed_shape& sh, const ScanArgs& a, hipStream_
   }
   const bool delta = sh.kind != SEED_MAMBA2;
   w.B = static_cast<float*>(a.ws);
-  w.A = w.B + split_floats(sh, w);  // GDN only
+  w.A = w.B + floats_of_B(sh, w);
   const int64_t items = w.slots * a.heads;
   w.pass = 1;
   hipLaunchKernelGGL(fn, dim3(loop_blocks(items * (delta ? 2 : 1))), threads, 0, s, a, w, items * (delta ? 2 : 1));
