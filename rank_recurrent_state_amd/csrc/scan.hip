@@ -4,36 +4,47 @@
 // Foundation" and "Exact Update (Lemma 2)").
 //
 // Every column of S follows its own recurrence given q, k, g and beta, so the d_v columns split
-// freely. A wavefront holds 16 columns of one unit's state in registers: lane l has columns
-// 4 (l / 16) .. + 3 and rows (d_k / 16) (l % 16) .. of them, and the two column sums S^T k and S^T q of
-// a token are reduced over 16 lanes with DPP adds. The next kAhead tokens' rows are in flight while
-// one block of them runs. The state is read and written once, whatever the prompt's length.
+// freely. A wavefront holds its columns of one unit's state in registers: kLanes lanes share a column's
+// rows and hold kCols columns each, and the two column sums S^T k and S^T q of a token are reduced over
+// the kLanes lanes with DPP adds. The next kAhead tokens' rows are in flight while one block of them
+// runs. The state is read and written once, whatever the prompt's length.
+//
+// What bounds it: with many units the vector unit (4 instructions per state element and token) and for
+// prompts of a few tokens the states' bytes; with few units the latency of a token's chain. Three
+// layouts, chosen by how many wavefronts 16 columns each would make (1024 fill the chip once).
+// Times for 128 x 128 KDA states, 256 tokens (first row: 32 units, then 256, then 2048):
+//     2 columns, 16 lanes    4 columns, 16 lanes    4 columns, 8 lanes
+//            102 us                 142 us                215 us
+//            269 us                 218 us                218 us
+//           2025 us                1545 us               1246 us
+// and 2048 one-token prompts take 99, 57 and 50 us (5.4 TB/s). With prompts shorter than 16 tokens
+// the narrow layout gains nothing and is not used.
 #include "common.hpp"
 #include "prompt.hpp"
 
 namespace seed {
 
-namespace {
+// Wavefronts of a workgroup: up to 4, of one unit.
+constexpr int scan_waves(int dv, int cols, int lanes) {
+  const int n = dv * lanes / (64 * cols);
+  return n < 4 ? n : 4;
+}
 
-constexpr int kThreads = 256;      // 4 wavefronts: 64 columns of one unit
-constexpr int kAhead = 4;          // tokens loaded ahead
-constexpr int kCols = 4;           // columns per lane
-
-}  // namespace
-
-template <int KIND, int DK, int DV, int IDT>
-__global__ __launch_bounds__(kThreads) void k_scan_tokens(const ScanArgs A, int64_t units) {
+template <int KIND, int DK, int DV, int IDT, int kCols, int kLanes, int kAhead>
+__global__ __launch_bounds__(64 * scan_waves(DV, kCols, kLanes)) void k_scan_tokens(const ScanArgs A, int64_t units) {
   using IT = stor_t<IDT>;
-  constexpr int R = DK / 16;       // rows per lane
-  constexpr int SPLIT = DV / 64;   // workgroups per unit
+  constexpr int R = DK / kLanes;   // rows per lane
+  constexpr int WC = 64 / kLanes * kCols;  // columns per wavefront
+  constexpr int NW = scan_waves(DV, kCols, kLanes);
+  constexpr int SPLIT = DV / (NW * WC);    // workgroups per unit
   constexpr bool DELTA = KIND != SEED_MAMBA2;
   constexpr bool DIAG = KIND == SEED_KDA;
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row0 = (lane & 15) * R;
+  const int row0 = (lane % kLanes) * R;
   for (int64_t item = blockIdx.x; item < units * SPLIT; item += gridDim.x) {
     const int64_t unit = item / SPLIT;
-    const int col0 = static_cast<int>(item % SPLIT) * 64 + wave * 16 + (lane >> 4) * kCols;
+    const int col0 = static_cast<int>(item % SPLIT) * (NW * WC) + wave * WC + lane / kLanes * kCols;
     const int b = static_cast<int>(unit / A.heads), h = static_cast<int>(unit % A.heads);
     const int kh = h / (A.heads / A.key_heads);
     int64_t lo, hi;
@@ -98,13 +109,13 @@ __global__ __launch_bounds__(kThreads) void k_scan_tokens(const ScanArgs A, int6
             sq[c] = fmaf(t.q[i], S[i][c], sq[c]);
           }
         }
-        kq = group_sum<16>(kq);
+        kq = group_sum<kLanes>(kq);
         float w[kCols], o[kCols];
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
-          sq[c] = group_sum<16>(sq[c]);
+          sq[c] = group_sum<kLanes>(sq[c]);
           w[c] = t.v[c];
-          if constexpr (DELTA) w[c] -= group_sum<16>(sk[c]);
+          if constexpr (DELTA) w[c] -= group_sum<kLanes>(sk[c]);
           w[c] *= t.beta;
           o[c] = fmaf(kq, w[c], sq[c]);
         }
@@ -112,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void k_scan_tokens(const ScanArgs A, int6
         for (int i = 0; i < R; ++i)
 #pragma unroll
           for (int c = 0; c < kCols; ++c) S[i][c] = fmaf(t.k[i], w[c], S[i][c]);
-        if ((lane & 15) == 0) store_f32<IDT, kCols>(op + (r0 + a) * A.o_stride, o);
+        if (lane % kLanes == 0) store_f32<IDT, kCols>(op + (r0 + a) * A.o_stride, o);
       }
     }
 
@@ -125,22 +136,40 @@ namespace {
 
 using ScanFn = void (*)(const ScanArgs, int64_t);
 
+struct Layout {
+  int cols, lanes;
+};
+
+Layout pick_layout(const seed_shape& sh, int64_t tokens) {
+  const int64_t waves = static_cast<int64_t>(sh.batch) * sh.heads * (sh.d_v / 16);
+  if (waves <= 512 && tokens >= 16 * static_cast<int64_t>(sh.batch)) return {2, 16};
+  if (waves <= 4096) return {4, 16};
+  return {4, 8};
+}
+
+template <int KIND, int DK, int DV, int IDT>
+ScanFn pick_layout_fn(Layout l) {
+  if (l.cols == 2) return k_scan_tokens<KIND, DK, DV, IDT, 2, 16, 4>;
+  if (l.lanes == 16) return k_scan_tokens<KIND, DK, DV, IDT, 4, 16, 4>;
+  return k_scan_tokens<KIND, DK, DV, IDT, 4, 8, 1>;
+}
+
 template <int KIND, int DK, int DV>
-ScanFn pick_io(int io) {
-  return io == SEED_BF16 ? k_scan_tokens<KIND, DK, DV, 1> : k_scan_tokens<KIND, DK, DV, 0>;
+ScanFn pick_io(int io, Layout l) {
+  return io == SEED_BF16 ? pick_layout_fn<KIND, DK, DV, 1>(l) : pick_layout_fn<KIND, DK, DV, 0>(l);
 }
 
 template <int KIND>
-ScanFn pick_dims(int dk, int dv, int io) {
-  if (dk == 128) return dv == 128 ? pick_io<KIND, 128, 128>(io) : pick_io<KIND, 128, 64>(io);
-  return dv == 128 ? pick_io<KIND, 64, 128>(io) : pick_io<KIND, 64, 64>(io);
+ScanFn pick_dims(int dk, int dv, int io, Layout l) {
+  if (dk == 128) return dv == 128 ? pick_io<KIND, 128, 128>(io, l) : pick_io<KIND, 128, 64>(io, l);
+  return dv == 128 ? pick_io<KIND, 64, 128>(io, l) : pick_io<KIND, 64, 64>(io, l);
 }
 
-ScanFn pick_scan(const seed_shape& sh) {
+ScanFn pick_scan(const seed_shape& sh, Layout l) {
   switch (sh.kind) {
-    case SEED_GDN: return pick_dims<SEED_GDN>(sh.d_k, sh.d_v, sh.io_dtype);
-    case SEED_KDA: return pick_dims<SEED_KDA>(sh.d_k, sh.d_v, sh.io_dtype);
-    default: return pick_dims<SEED_MAMBA2>(sh.d_k, sh.d_v, sh.io_dtype);
+    case SEED_GDN: return pick_dims<SEED_GDN>(sh.d_k, sh.d_v, sh.io_dtype, l);
+    case SEED_KDA: return pick_dims<SEED_KDA>(sh.d_k, sh.d_v, sh.io_dtype, l);
+    default: return pick_dims<SEED_MAMBA2>(sh.d_k, sh.d_v, sh.io_dtype, l);
   }
 }
 
@@ -167,7 +196,9 @@ size_t prefill_scan_workspace(const seed_shape& sh, const seed_prompt& p) {
 hipError_t launch_prefill_scan(const seed_shape& sh, const ScanArgs& a, hipStream_t s) {
   if (takes_chunks(sh, a.tokens, longest(a.q_stride, a.k_stride, a.v_stride, a.o_stride))) return launch_scan_chunk(sh, a, s);
   const int64_t units = static_cast<int64_t>(a.batch) * a.heads;
-  hipLaunchKernelGGL(pick_scan(sh), dim3(loop_blocks(units * (sh.d_v / 64))), dim3(kThreads), 0, s, a, units);
+  const Layout l = pick_layout(sh, a.tokens);
+  const int waves = scan_waves(sh.d_v, l.cols, l.lanes), split = sh.d_v * l.lanes / (64 * l.cols * waves);
+  hipLaunchKernelGGL(pick_scan(sh, l), dim3(loop_blocks(units * split)), dim3(64 * waves), 0, s, a, units);
   return hipGetLastError();
 }
 

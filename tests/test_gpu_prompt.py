@@ -230,6 +230,22 @@ def test_scan(kind, dtype, dk, dv, lens):
 
 @pytest.mark.parametrize("kind", [ref.GDN, ref.KDA, ref.MAMBA2])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("batch,heads,most", [(90, 4, 5), (130, 8, 3), (70, 16, 40)])
+def test_scan_of_many_units(kind, dtype, dk, dv, batch, heads, most):
+    """Many requests, of a few tokens each and of more."""
+    rrs, torch = _rrs()
+    r = np.random.default_rng(batch + most)
+    lens = r.integers(0, most + 1, batch).tolist()
+    g = _gen(torch, batch)
+    t = _scan_inputs(torch, g, kind, sum(lens), heads, heads, dk, dv, dtype)
+    S0 = torch.randn(batch, heads, dk, dv, device="cuda", generator=g)
+    o, S = _run_scan(rrs, torch, kind, lens, t, S0, (heads, dk, dv), dtype)
+    _check_scan(_np(o), _np(S), ref.scan(kind, lens, *map(_np, t), _np(S0)), dtype)
+
+
+@pytest.mark.parametrize("kind", [ref.GDN, ref.KDA, ref.MAMBA2])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_scan_gates_of_every_size(kind, dtype):
     """Gates of 1, of 0, so small that their product underflows, and strong ones token after token,
     next to beta of 0 and 1 and the same key again and again."""
