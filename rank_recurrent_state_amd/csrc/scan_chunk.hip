@@ -436,7 +436,10 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, cons
   }
 
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int h = static_cast<int>(item % A.heads);
+    // Consecutive workgroups go to the 8 XCDs in turn. Heads of one key head are kept key_heads apart, on
+    // the same XCD where key_heads is a multiple of 8, so that they share the rows of q and k in its L2.
+    const int place = static_cast<int>(item % A.heads), share = A.heads / A.key_heads;
+    const int kh = place % A.key_heads, h = kh * share + place / A.key_heads;
     int b;                       // sequence
     int64_t lo, hi;              // its rows to run over
     const float* init = nullptr; // the state to start from (nullptr: zeros, or the identity when v counts as zero)
@@ -471,7 +474,6 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, cons
         dest = last ? A.S + at : nullptr;
       }
     }
-    const int kh = h / (A.heads / A.key_heads);
     lo = __builtin_amdgcn_readfirstlane(static_cast<int>(lo));  // rows are below 2^31
     hi = __builtin_amdgcn_readfirstlane(static_cast<int>(hi));
     const int n = static_cast<int>((hi - lo + C - 1) / C);  // chunks
@@ -514,7 +516,7 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, cons
         far = far == 2 ? 0 : far + 1;
       }
       if (!DELTA && W.pass == 1 && role == kG && (threadIdx.x & 63) == 0)
-        W.A[item] = static_cast<float>(exp2(decay));
+        W.A[item / A.heads * A.heads + h] = static_cast<float>(exp2(decay));
       continue;
     }
 
