@@ -754,27 +754,42 @@ __global__ __launch_bounds__(DK * 2) void k_join_delta(const ScanArgs A, const S
   const int col = blockIdx.x % (DV / 32) * 32 + l32;
   int64_t base, lo, hi;
   const int segs = first_segment(A, W, b, base, lo, hi);
-  for (int seg = 0; seg + 1 < segs && base + seg < W.slots; ++seg) {
-    float* Bs = W.B + ((base + seg) * A.heads + h) * (DK * DV);
-    f32x16 acc;  // register i is row 32 wave + 8 (i / 4) + 4 half + i % 4
+  // the next segment's matrices are on their way while one product runs
+  f32x4 a[DK / 8], na[DK / 8];
+  f32x16 acc, nb;  // register i is row 32 wave + 8 (i / 4) + 4 half + i % 4
+  auto load = [&](int seg) {
+    const int64_t slot = (base + seg) * A.heads + h;
+    const float* Bs = W.B + slot * (DK * DV);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = Bs[static_cast<int64_t>(32 * wave + 8 * (i / 4) + 4 * half + i % 4) * DV + col];
+    for (int i = 0; i < 16; ++i) nb[i] = Bs[(32 * wave + 8 * (i / 4) + 4 * half + i % 4) * DV + col];
+    const float* As = W.A + slot * (DK * DK) + (32 * wave + l32) * DK + 4 * half;
+    if (seg > 0) {  // the first segment has no A
+#pragma unroll
+      for (int k = 0; k < DK / 8; ++k) na[k] = *reinterpret_cast<const f32x4*>(As + 8 * k);
+    }
+  };
+  const int64_t room = W.slots - base;
+  const int n = static_cast<int>(segs - 1 < room ? segs - 1 : room);
+  if (n > 0) load(0);
+  for (int seg = 0; seg < n; ++seg) {
+    acc = nb;
+#pragma unroll
+    for (int k = 0; k < DK / 8; ++k) a[k] = na[k];
+    if (seg + 1 < n) load(seg + 1);
     if (seg > 0) {
-      const float* As = W.A + ((base + seg) * A.heads + h) * (DK * DK) + (32 * wave + l32) * DK + 4 * half;
 #pragma unroll
-      for (int k = 0; k < DK; k += 8) {  // k slot `half` of step i is row k + 4 half + i
-        const f32x4 a = *reinterpret_cast<const f32x4*>(As + k);
+      for (int k = 0; k < DK / 8; ++k)  // k slot `half` of step i is row 8 k + 4 half + i
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], Sh[(k + 4 * half + i) * LS + l32], acc, 0, 0, 0);
-      }
+          acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[k][i], Sh[(8 * k + 4 * half + i) * LS + l32], acc, 0, 0, 0);
       __syncthreads();  // the old state has been read
     }
+    float* Bs = W.B + ((base + seg) * A.heads + h) * (DK * DV);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int row = 32 * wave + 8 * (i / 4) + 4 * half + i % 4;
       Sh[row * LS + l32] = acc[i];
-      if (seg > 0) Bs[static_cast<int64_t>(row) * DV + col] = acc[i];
+      if (seg > 0) Bs[row * DV + col] = acc[i];
     }
     __syncthreads();
   }
