@@ -440,7 +440,7 @@ typedef struct seed_prompt {
 } seed_prompt;
 
 /* Workspace bytes of seed_prefill_scan for these prompts (0: none needed, or invalid arguments).
- * Depends on the sizes only. Host-only, pure. */
+ * Depends on the sizes and strides only. Host-only, pure. */
 size_t seed_prefill_workspace_bytes(const seed_shape *shape, const seed_prompt *prompt);
 
 /*

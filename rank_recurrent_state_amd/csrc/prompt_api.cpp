@@ -3,6 +3,8 @@
 // enqueued, never synchronises and allocates nothing.
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "../../include/seed.h"
 #include "prompt.hpp"
 
@@ -35,6 +37,18 @@ bool overlap(const Rows& a, const Rows& b) {
   const uintptr_t d = b.lo() >= a.lo() ? (b.lo() - a.lo()) % st : (st - (a.lo() - b.lo()) % st) % st;
   // row i of b starts d behind some row position of a and ends before the next one
   return !(d >= static_cast<uintptr_t>(a.width) && d + static_cast<uintptr_t>(b.width) <= st);
+}
+// A buffer of `bytes` bytes.
+Rows flat(const void* p, int64_t bytes) { return Rows{p, 1, bytes, bytes}; }
+// Whether one of `outs` shares a byte with one of `ins` or with another of `outs`.
+bool any_overlap(std::initializer_list<Rows> outs, std::initializer_list<Rows> ins) {
+  for (const Rows* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Rows& i : ins)
+      if (overlap(*o, i)) return true;
+    for (const Rows* p = o + 1; p != outs.end(); ++p)
+      if (overlap(*o, *p)) return true;
+  }
+  return false;
 }
 // The same rows exactly: reading and writing them in place.
 bool same(const Rows& a, const Rows& b) { return a.p == b.p && (a.stride == b.stride || a.rows <= 1); }
@@ -89,7 +103,9 @@ int seed_prefill_conv(const seed_conv* conv, int64_t tokens, const int32_t* offs
   // rows before a tile and the old window are read by other workgroups than those that write
   const Rows rx{x, tokens, x_stride * e, ch * e}, ry{y, tokens, y_stride * e, ch * e};
   const Rows wi{window_in, conv->batch, wrow, wrow}, wo{window_out, conv->batch, wrow, wrow};
-  if (overlap(rx, ry) || overlap(wi, wo) || overlap(wo, rx) || overlap(wo, ry) || overlap(wi, ry)) return SEED_ERR_ARG;
+  if (any_overlap({ry, wo}, {rx, wi, flat(weight, ch * conv->width * 4), flat(bias, ch * 4),
+                             flat(offsets, (static_cast<int64_t>(conv->batch) + 1) * 4)}))
+    return SEED_ERR_ARG;
   seed::ConvArgs a{};
   a.tokens = tokens;
   a.batch = conv->batch;
@@ -122,8 +138,9 @@ int seed_decode_conv(const seed_conv* conv, const uint8_t* active, const void* x
   const int64_t wrow = ch * (conv->width - 1) * e;
   const Rows rx{x, conv->batch, x_stride * e, ch * e}, ry{y, conv->batch, y_stride * e, ch * e};
   const Rows wi{window_in, conv->batch, wrow, wrow}, wo{window_out, conv->batch, wrow, wrow};
-  if ((overlap(rx, ry) && !same(rx, ry)) || (overlap(wi, wo) && !same(wi, wo)) || overlap(wo, rx) || overlap(wo, ry) ||
-      overlap(wi, ry))
+  const Rows fw = flat(weight, ch * conv->width * 4), fb = flat(bias, ch * 4), fa = flat(active, conv->batch);
+  if (any_overlap({ry, wo}, {fw, fb, fa}) || overlap(wo, rx) || overlap(wi, ry) || (overlap(rx, ry) && !same(rx, ry)) ||
+      (overlap(wi, wo) && !same(wi, wo)))
     return SEED_ERR_ARG;
   seed::ConvArgs a{};
   a.batch = conv->batch;
@@ -162,17 +179,15 @@ int seed_prefill_scan(const seed_shape* sh, const seed_prompt* prompt, const voi
   const Rows rv{v, n, prompt->v_stride * e, vw}, ro{o, n, prompt->o_stride * e, vw};
   const int64_t sw = static_cast<int64_t>(sh->d_k) * sh->d_v * 4, units = static_cast<int64_t>(sh->batch) * sh->heads;
   const Rows s0{S0, units, sw, sw}, s1{S, units, sw, sw};
-  if (overlap(ro, rq) || overlap(ro, rk) || overlap(ro, rv) || overlap(ro, s0) || overlap(ro, s1) || overlap(s1, rq) ||
-      overlap(s1, rk) || overlap(s1, rv) || (overlap(s0, s1) && !same(s0, s1)))
+  const Rows fb = flat(beta, n * sh->heads * 4), fo = flat(prompt->offsets, (static_cast<int64_t>(sh->batch) + 1) * 4);
+  const Rows fg = flat(g, n * sh->heads * 4 * (sh->kind == SEED_KDA ? sh->d_k : 1));
+  if (any_overlap({ro, s1}, {rq, rk, rv, fb, fg, fo}) || overlap(ro, s0) || (overlap(s0, s1) && !same(s0, s1)))
     return SEED_ERR_ARG;
   const size_t need = seed_prefill_workspace_bytes(sh, prompt);
-  if (need > 0 && (!ws || ws_bytes < need)) return SEED_ERR_WORKSPACE;
   if (need > 0) {
+    if (!ws || ws_bytes < need) return SEED_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return SEED_ERR_ARG;
-    const int64_t nb = static_cast<int64_t>(need), gw = static_cast<int64_t>(sh->heads) * 4 * (sh->kind == SEED_KDA ? sh->d_k : 1);
-    const Rows rw{ws, 1, nb, nb}, rb{beta, 1, n * sh->heads * 4, n * sh->heads * 4}, rg{g, 1, n * gw, n * gw};
-    for (const Rows& r : {rq, rk, rv, ro, s0, s1, rb, rg})
-      if (overlap(rw, r)) return SEED_ERR_ARG;
+    if (any_overlap({flat(ws, static_cast<int64_t>(need))}, {rq, rk, rv, ro, s0, s1, fb, fg, fo})) return SEED_ERR_ARG;
   }
   seed::ScanArgs a{};
   a.tokens = n;
@@ -222,7 +237,7 @@ int seed_norm_rows(const seed_rows* rows, const void* x, const seed_head_norm* n
   for (const Rows& in : {rx, rg, rs})
     for (const Rows& out : {ry, rt})
       if (overlap(in, out) && !same(in, out)) return SEED_ERR_ARG;
-  if (overlap(ry, rt)) return SEED_ERR_ARG;
+  if (any_overlap({ry, rt}, {flat(norm->weight, w * 4), flat(scale, static_cast<int64_t>(rows->heads) * 4)})) return SEED_ERR_ARG;
   if (rows->rows == 0) return SEED_OK;
   seed::NormArgs a{};
   a.rows = rows->rows;

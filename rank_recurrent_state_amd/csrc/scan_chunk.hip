@@ -21,8 +21,16 @@
 // permuted so that a lane's 8 consecutive accumulator registers are 8 consecutive rows: the
 // accumulators of one product are then the right operand of the next, and S, W and O never leave
 // the registers. K, Q, T and P are left operands in LDS; K^T and V come out of row-major tiles
-// with the transposing LDS read. One wavefront forms T while another forms P and the rest already
-// multiply K and Q with the state.
+// with the transposing LDS read. As many wavefronts again prepare: rows go from memory straight to LDS two
+// chunks ahead, T and P are formed a chunk ahead, so that a chunk costs one barrier and the state's
+// wavefronts wait for nothing else.
+//
+// What bounds it: the vector unit. A state wavefront spends 800 to 900 vector instructions on a GDN chunk (half
+// of them on the pieces of S) next to 82 matrix ones; over 32768 tokens x 32 GDN heads the vector unit is busy
+// 52 % of the time and the matrix unit 28 %, and bank conflicts take 10 % of the LDS cycles. A chunk
+// takes 3.8 us on a compute unit of its own, 32768 GDN tokens x 32 heads 534 us (2.1 TB/s of rows and
+// states), the same tokens x 64 Mamba-2 heads 455 us. 64-token chunks would split S half as often but
+// need 64 accumulators more than the 256 registers; two workgroups per compute unit do not fit LDS.
 #include "common.hpp"
 #include "prompt.hpp"
 
@@ -40,6 +48,10 @@ using s16x4 = __attribute__((ext_vector_type(4))) short;
 using lds_s16x4 = __attribute__((address_space(3))) s16x4;
 
 constexpr int C = 32;       // tokens per chunk
+constexpr int LT = C + 8;   // row length of the T and P pieces
+constexpr int LF = 16 + 4;  // row length of the fp32 block of T
+constexpr int kRanked = 128;  // sequences that are put in order of length
+
 // Long prompts of few units, cut into segments (plan_split).
 struct Split {
   int32_t pass;    // 0: whole sequences; 1: every segment's A and B; 2: the read-outs
@@ -48,10 +60,6 @@ struct Split {
   float* A;        // [slots][heads][d_k][d_k]; Mamba-2: [slots][heads], the product of the segment's gates
   float* B;        // [slots][heads][d_k][d_v]
 };
-
-constexpr int kRanked = 512;  // sequences that are put in order of length
-constexpr int LT = C + 8;   // row length of the T and P pieces
-constexpr int LF = 16 + 4;  // row length of the fp32 block of T
 
 // Row m of a 32-row operand tile holds token or channel perm(m), which puts 8 consecutive ones into
 // a lane's accumulator registers 0..7 and 8..15: register i of lane half h is 16 (i / 8) + 8 h + i % 8.
@@ -128,35 +136,95 @@ __device__ __forceinline__ void wait_loads() {
 // By value: a conditional between two elements of an array would put the array in memory.
 __device__ __forceinline__ float pick(bool c, float a, float b) { return c ? a : b; }
 
-// a += (b of lane N of the lane's 16) c, in one instruction.
-template <int N>
-__device__ __forceinline__ void fmac_bcast16(float& a, float b, float c) {
-  asm("v_fmac_f32_dpp %0, %1, %2 row_newbcast:%3 row_mask:0xf bank_mask:0xf" : "+v"(a) : "v"(b), "v"(c), "n"(N));
-}
-
 // x = (I - L)^-1 e_j for a 16 x 16 strictly lower L: lane i of 16 holds row i of L and gets column i of
-// the inverse. Step S takes x[S], final by then, out of the rows below.
-template <int S, int R>
-__device__ __forceinline__ void solve_row(const float (&L)[16], float (&x)[16]) {
-  if constexpr (R < 16) {
-    fmac_bcast16<R>(x[R], L[S], x[S]);
-    solve_row<S, R + 1>(L, x);
-  }
+// the inverse. Step S takes x[S], final by then, out of the rows below: x[R] += L[R][S] x[S], where L[R][S] is
+// lane R's L[S], a row broadcast inside the instruction. Outputs are numbered from x[15] down, so the
+// text of a step is the first 15 - S lines. A broadcast may read a register two instructions after its
+// write at the earliest, which each step's s_nop sees to.
+#define SEED_FMAC(out, row) \
+  "v_fmac_f32_dpp %" #out ", %[l], %[y] row_newbcast:" #row " row_mask:0xf bank_mask:0xf\n\t"
+#define SEED_STEP1 SEED_FMAC(0, 15)
+#define SEED_STEP2 SEED_STEP1 SEED_FMAC(1, 14)
+#define SEED_STEP3 SEED_STEP2 SEED_FMAC(2, 13)
+#define SEED_STEP4 SEED_STEP3 SEED_FMAC(3, 12)
+#define SEED_STEP5 SEED_STEP4 SEED_FMAC(4, 11)
+#define SEED_STEP6 SEED_STEP5 SEED_FMAC(5, 10)
+#define SEED_STEP7 SEED_STEP6 SEED_FMAC(6, 9)
+#define SEED_STEP8 SEED_STEP7 SEED_FMAC(7, 8)
+#define SEED_STEP9 SEED_STEP8 SEED_FMAC(8, 7)
+#define SEED_STEP10 SEED_STEP9 SEED_FMAC(9, 6)
+#define SEED_STEP11 SEED_STEP10 SEED_FMAC(10, 5)
+#define SEED_STEP12 SEED_STEP11 SEED_FMAC(11, 4)
+#define SEED_STEP13 SEED_STEP12 SEED_FMAC(12, 3)
+#define SEED_STEP14 SEED_STEP13 SEED_FMAC(13, 2)
+#define SEED_STEP15 SEED_STEP14 SEED_FMAC(14, 1)
+#define SEED_X(r) "+v"(x[r])
+#define SEED_OUT1 SEED_X(15)
+#define SEED_OUT2 SEED_OUT1, SEED_X(14)
+#define SEED_OUT3 SEED_OUT2, SEED_X(13)
+#define SEED_OUT4 SEED_OUT3, SEED_X(12)
+#define SEED_OUT5 SEED_OUT4, SEED_X(11)
+#define SEED_OUT6 SEED_OUT5, SEED_X(10)
+#define SEED_OUT7 SEED_OUT6, SEED_X(9)
+#define SEED_OUT8 SEED_OUT7, SEED_X(8)
+#define SEED_OUT9 SEED_OUT8, SEED_X(7)
+#define SEED_OUT10 SEED_OUT9, SEED_X(6)
+#define SEED_OUT11 SEED_OUT10, SEED_X(5)
+#define SEED_OUT12 SEED_OUT11, SEED_X(4)
+#define SEED_OUT13 SEED_OUT12, SEED_X(3)
+#define SEED_OUT14 SEED_OUT13, SEED_X(2)
+#define SEED_OUT15 SEED_OUT14, SEED_X(1)
+#define SEED_SOLVE(S, n) asm("s_nop 1\n\t" SEED_STEP##n : SEED_OUT##n : [l] "v"(L[S]), [y] "v"(x[S]))
+__device__ __forceinline__ void solve16(const float (&L)[16], float (&x)[16]) {
+  SEED_SOLVE(0, 15);
+  SEED_SOLVE(1, 14);
+  SEED_SOLVE(2, 13);
+  SEED_SOLVE(3, 12);
+  SEED_SOLVE(4, 11);
+  SEED_SOLVE(5, 10);
+  SEED_SOLVE(6, 9);
+  SEED_SOLVE(7, 8);
+  SEED_SOLVE(8, 7);
+  SEED_SOLVE(9, 6);
+  SEED_SOLVE(10, 5);
+  SEED_SOLVE(11, 4);
+  SEED_SOLVE(12, 3);
+  SEED_SOLVE(13, 2);
+  SEED_SOLVE(14, 1);
 }
-template <int S>
-__device__ __forceinline__ void solve_from(const float (&L)[16], float (&x)[16]) {
-  if constexpr (S < 15) {
-    solve_row<S, S + 1>(L, x);
-    solve_from<S + 1>(L, x);
-  }
-}
-__device__ __forceinline__ void solve16(float (&L)[16], float (&x)[16]) {
-  // a lane broadcast may read a register two instructions after its write at the earliest
-  asm("s_nop 1"
-      : "+v"(L[0]), "+v"(L[1]), "+v"(L[2]), "+v"(L[3]), "+v"(L[4]), "+v"(L[5]), "+v"(L[6]), "+v"(L[7]), "+v"(L[8]),
-        "+v"(L[9]), "+v"(L[10]), "+v"(L[11]), "+v"(L[12]), "+v"(L[13]), "+v"(L[14]));
-  solve_from<0>(L, x);
-}
+#undef SEED_SOLVE
+#undef SEED_OUT1
+#undef SEED_STEP1
+#undef SEED_OUT2
+#undef SEED_STEP2
+#undef SEED_OUT3
+#undef SEED_STEP3
+#undef SEED_OUT4
+#undef SEED_STEP4
+#undef SEED_OUT5
+#undef SEED_STEP5
+#undef SEED_OUT6
+#undef SEED_STEP6
+#undef SEED_OUT7
+#undef SEED_STEP7
+#undef SEED_OUT8
+#undef SEED_STEP8
+#undef SEED_OUT9
+#undef SEED_STEP9
+#undef SEED_OUT10
+#undef SEED_STEP10
+#undef SEED_OUT11
+#undef SEED_STEP11
+#undef SEED_OUT12
+#undef SEED_STEP12
+#undef SEED_OUT13
+#undef SEED_STEP13
+#undef SEED_OUT14
+#undef SEED_STEP14
+#undef SEED_OUT15
+#undef SEED_STEP15
+#undef SEED_X
+#undef SEED_FMAC
 
 // A copy of x that the compiler takes for a new value.
 __device__ __forceinline__ int fresh(int x) {
@@ -416,9 +484,11 @@ __device__ __forceinline__ int first_segment(const ScanArgs& A, const Split& W, 
 }
 
 // Wavefronts 0 .. NW - 1 hold 32 columns of the state each and run a chunk while the NH others prepare:
-// T and P of the next chunk, and rows and gates of the one after it.
+// T and P of the next chunk, and rows and gates of the one after it. Preparing in the state's own
+// wavefronts instead, with two workgroups per compute unit, took 704 us where this takes 673 (32768 GDN
+// tokens) and 1436 where this takes 936 (one 8192-token prompt, uncut).
 template <int KIND, int DK, int DV>
-__global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, const Split W, int64_t items) {
+__global__ __launch_bounds__(DV * 4, KIND != SEED_MAMBA2 && DK == 128 && DV == 64 ? 1 : 2) void k_scan_chunk(const ScanArgs A, const Split W, int64_t items) {
   using TL = Tiles<KIND, DK, DV>;
   constexpr bool DELTA = TL::DELTA;
   constexpr int NW = DV / 32, NH = NW, NT = (NW + NH) * 64;
@@ -485,7 +555,7 @@ __global__ __launch_bounds__(DV * 4, 2) void k_scan_chunk(const ScanArgs A, cons
 
     if (role >= 0) {
       // ---- helpers ------------------------------------------------------------------------------------
-      // chunk j's rows go to buffer `to`; its gates are loaded at once and summed when `sum` is called
+      // chunk j's rows go to buffer `to`, its gates are loaded and summed
       float g = 1.f, beta = 0.f;
       double decay = 0;  // log2 of the product of all gates
       auto fetch = [&](int j, int to) {
@@ -832,8 +902,17 @@ constexpr int64_t kCUs = 256;
 // cut into segments: the state after a segment is A S + B with S the state before it, so one pass forms
 // A and B of all segments side by side (A: the recurrence from the identity with v = 0; a product of
 // gates for Mamba-2), the states between them follow, and a second pass gives the read-outs.
-// With n segments that is 2 (Mamba-2) or 3 (GDN: A and B are two runs) n-ths of the serial time when
-// slots / units = n - 1 segments fill the chip at once; @@figures@@
+// n = slots / units + 1 segments fill the chip once with the read-outs, and once (Mamba-2) or twice (GDN, whose
+// A and B are two runs) with the first pass: 2 / n or 3 / n of the serial time, and about 50 us.
+// Measured, cut and whole, us:           1024 tokens   2048        8192
+//   GDN 128 x 128,    16 units               89, 121   107, 229   278, 891
+//                     64                    136, 123   198, 229   655, 896
+//                     85                    148, 124   234, 230   779, 895
+//                    128                    165, 124   281, 232   961, 894
+//   Mamba-2 128 x 64, 16                     56, 82     59, 156    91, 600
+//                    128                     80, 85    116, 157   399, 611
+//                    256                    101, 88    172, 161   597, 609
+// and 512 tokens are always faster whole (GDN 77, 66; Mamba-2 54, 45).
 Split plan_split(const seed_shape& sh, int64_t tokens) {
   Split w{};
   const bool delta = sh.kind != SEED_MAMBA2;
@@ -841,7 +920,7 @@ Split plan_split(const seed_shape& sh, int64_t tokens) {
   const int64_t slots = kCUs * (!delta && sh.d_v == 64 ? 2 : 1);  // workgroups that fit the chip at once
   const int64_t n = slots / units + 1;
   if (delta && sh.d_k != sh.d_v) return w;  // A is run as a state of d_k x d_k
-  if (n < (delta ? 4 : 3) || mean < (delta ? 2048 : 1024)) return w;
+  if (n < (delta ? 4 : 3) || mean < (delta && n < 9 ? 2048 : 1024)) return w;
   int64_t seg = (mean + n - 1) / n;
   seg = (seg < 256 ? 256 : seg) + C - 1;
   w.tokens = static_cast<int32_t>(seg / C * C);

@@ -367,6 +367,49 @@ def test_scan_is_causal_for_values_that_are_not_finite(kind, where):
         assert not torch.isfinite(S).all()
 
 
+@pytest.mark.parametrize("log_stride", [23, 24])
+def test_scan_rows_far_apart(log_stride):
+    """Rows whose byte offsets pass 2^32, at a stride that chunks still take and at one they do not."""
+    rrs, torch = _rrs()
+    heads, dk, dv, n, stride = 1, 64, 64, 200, 1 << log_stride
+    t = _scan_inputs(torch, _gen(torch, 59), ref.GDN, n, heads, 1, dk, dv, "bf16")
+    buf = torch.empty((n - 1) * stride + 4 * 64, dtype=torch.bfloat16, device="cuda")
+    far = [buf.as_strided((n, 1, 64), (stride, 64, 1), 64 * i) for i in range(4)]
+    for dst, src in zip(far, t[:3]):
+        dst.copy_(src)
+    shape = rrs.make_shape(rrs.SEED_GDN, 2, heads, dk, dv, 8, 8, rrs.SEED_BF16)
+    S = torch.empty(2, heads, dk, dv, device="cuda")
+    rrs.seed_prefill_scan(shape, _offsets(torch, [77, 123]), *far[:3], t[3], t[4], S, far[3])
+    _check_scan(_np(far[3]), _np(S), ref.scan(ref.GDN, [77, 123], *map(_np, t), None), "bf16")
+
+
+def test_long_scan_captured_and_replayed():
+    """A prompt cut into segments, in a graph whose workspace comes from torch's allocator."""
+    rrs, torch = _rrs()
+    heads, d, n = 1, 64, 2700
+    t = _scan_inputs(torch, _gen(torch, 61), ref.GDN, n, heads, 1, d, d, "bf16")
+    shape = rrs.make_shape(rrs.SEED_GDN, 1, heads, d, d, 8, 8, rrs.SEED_BF16)
+    off = _offsets(torch, [n])
+
+    def run(o, S):
+        rrs.seed_prefill_scan(shape, off, *t, S, o)
+
+    eager, graphed = ([torch.empty(n, heads, d, dtype=torch.bfloat16, device="cuda"), torch.empty(1, heads, d, d, device="cuda")]
+                      for _ in range(2))
+    run(*graphed)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(*graphed)
+    for i in range(4):
+        t[2].copy_(torch.randn(n, heads, d, device="cuda", generator=_gen(torch, i)))
+        graph.replay()
+        torch.cuda.synchronize()
+        run(*eager)
+        torch.cuda.synchronize()
+        assert torch.equal(eager[0], graphed[0]) and torch.equal(eager[1], graphed[1])
+
+
 def test_scan_workspaces():
     """A given workspace, one of torch's allocator, and one that is too small or misaligned."""
     rrs, torch = _rrs()
