@@ -410,6 +410,30 @@ def test_long_scan_captured_and_replayed():
         assert torch.equal(eager[0], graphed[0]) and torch.equal(eager[1], graphed[1])
 
 
+def test_long_scan_with_wrong_offsets_and_on_given_streams():
+    """Cut prompts whose offsets decrease or leave the buffer stay inside it and leave the rows around
+    alone; the call's own workspace follows the stream it is given."""
+    rrs, torch = _rrs()
+    heads, d, n = 2, 64, 5000
+    t = _scan_inputs(torch, _gen(torch, 67), ref.GDN, n, heads, 1, d, d, "bf16")
+    guard = torch.full((n + 64, heads, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    shape = rrs.make_shape(rrs.SEED_GDN, 4, heads, d, d, 8, 8, rrs.SEED_BF16)
+    room = torch.full((6, heads, d, d), 3.0, device="cuda")
+    off = torch.tensor([0, n, -7, n, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    assert rrs.seed_prefill_workspace_bytes(shape, rrs.seed_prompt(4 * n, None, 1, d, d, 2 * d, 2 * d)) > 0
+    rrs.seed_prefill_scan(rrs.make_shape(rrs.SEED_GDN, 4, heads, d, d, 8, 8, rrs.SEED_BF16), off, *t, room[1:5], guard[32:32 + n])
+    torch.cuda.synchronize()
+    assert (guard[:32] == 7.0).all() and (guard[32 + n:] == 7.0).all()
+    assert (room[0] == 3.0).all() and (room[5] == 3.0).all()
+    o0, S0 = _run_scan(rrs, torch, ref.GDN, [n], t, None, (heads, d, d), "bf16")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0):
+        o1, S1 = _run_scan(rrs, torch, ref.GDN, [n], t, None, (heads, d, d), "bf16", stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(S0, S1) and torch.equal(o0, o1)
+
+
 def test_scan_workspaces():
     """A given workspace, one of torch's allocator, and one that is too small or misaligned."""
     rrs, torch = _rrs()
