@@ -9,12 +9,11 @@
 // T = (I + L)^-1 is formed explicitly, by forward substitution in 16 x 16 blocks (products of powers
 // of L would cancel badly when keys repeat), and multiplies the right-hand side.
 //
-// Precision. q, k and v are bf16 and enter the matrix instructions exactly. fp32 operands enter
-// as sums of bf16 pieces, each the rounding of what the ones before left: three pieces hold all 24
-// bits (the state where it meets k, T and its right-hand side, W where it enters the state), two hold
-// 16 (the state where it meets q, P and W in P W), enough for a read-out that is rounded to 8 bits
-// and does not feed back. Sums are fp32. The running c is summed in fp64 and kept as two floats,
-// so that differences of large sums keep their bits.
+// Precision. q, k and v are bf16 and enter the matrix instructions exactly. fp32 operands (the state, T
+// and its right-hand side, P, W) enter as sums of three bf16 pieces, each the rounding of what the
+// ones before left, which hold all 24 bits; products of two such sums leave out the terms below
+// 2^-24. Sums are fp32. The running c is summed in fp64 and kept as two floats, so that differences
+// of large sums keep their bits.
 //
 // Layout. A workgroup has one unit and one wavefront per 32 columns of d_v; a wavefront holds its
 // columns of the state, d_k x 32 fp32, in accumulator layout. Rows of the operand tiles are
@@ -258,7 +257,7 @@ struct Tiles {
     float beta[C], g[C];
   } gates[3];
   // by the chunk's number modulo 2
-  uint16_t P[2][2][C * LT];
+  uint16_t P[2][3][C * LT];
   uint16_t T[DELTA ? 2 : 1][DELTA ? 3 : 1][DELTA ? C * LT : 8];
   float T11[DELTA ? 16 * LF : 4]; // column-major: the lower diagonal block of T
   int32_t len[kRanked], found;    // of ranked_sequence
@@ -324,9 +323,9 @@ __device__ __forceinline__ void weights(const Gates& G, int l32, int half, float
   }
 }
 
-// P (Mamba-2: times diag(beta)) in two pieces, by one wavefront.
+// P (Mamba-2: times diag(beta)) in three pieces, by one wavefront.
 template <bool DELTA, int DK, class Gates>
-__device__ __forceinline__ void form_P(Tile<DK>& K, Tile<DK>& Q, const Gates& G, uint16_t (&P)[2][C * LT]) {
+__device__ __forceinline__ void form_P(Tile<DK>& K, Tile<DK>& Q, const Gates& G, uint16_t (&P)[3][C * LT]) {
   const int lane = fresh(threadIdx.x & 63), l32 = lane & 31, half = lane >> 5, prow = perm(l32);
   f32x16 acc = {};
 #pragma unroll
@@ -344,10 +343,10 @@ __device__ __forceinline__ void form_P(Tile<DK>& K, Tile<DK>& Q, const Gates& G,
       if constexpr (!DELTA) w *= G.beta[s];
       x[j] = s <= l32 ? w : 0.f;
     }
-    bf16x8 pc[2];
-    split<2>(x, pc);
+    bf16x8 pc[3];
+    split<3>(x, pc);
 #pragma unroll
-    for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(P[n] + l32 * LT + 16 * s8 + 8 * half) = pc[n];
+    for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(P[n] + l32 * LT + 16 * s8 + 8 * half) = pc[n];
   }
 }
 
@@ -639,20 +638,13 @@ __global__ __launch_bounds__(DV * 4, KIND != SEED_MAMBA2 && DK == 128 && DV == 6
           for (int j = 0; j < 8; ++j) x[j] = S[r][8 * s + j];
           const int col = 32 * r + 16 * s + 8 * half;
           const bf16x8 aq = frag(Q.at(prow, col));
-          if constexpr (DELTA) {
-            bf16x8 pc[3];
-            split<3>(x, pc);
-            const bf16x8 ak = frag(K.at(prow, col));
-            ks = mma(ak, pc[2], ks);
-            qs = mma(aq, pc[1], qs);
-            ks = mma(ak, pc[1], ks);
-            qs = mma(aq, pc[0], qs);
-            ks = mma(ak, pc[0], ks);
-          } else {
-            bf16x8 pc[2];
-            split<2>(x, pc);
-            qs = mma(aq, pc[1], qs);
-            qs = mma(aq, pc[0], qs);
+          bf16x8 pc[3], ak;
+          split<3>(x, pc);
+          if constexpr (DELTA) ak = frag(K.at(prow, col));
+#pragma unroll
+          for (int n = 2; n >= 0; --n) {
+            if constexpr (DELTA) ks = mma(ak, pc[n], ks);
+            qs = mma(aq, pc[n], qs);
           }
         }
       // v in accumulator layout, and as the bf16 right operand it already is
@@ -745,19 +737,24 @@ __global__ __launch_bounds__(DV * 4, KIND != SEED_MAMBA2 && DK == 128 && DV == 6
         for (int i = 0; i < 16; ++i) o[i] = hd[i] * qs[i];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const bf16x8 p0 = frag(P[0] + prow * LT + 16 * s + 8 * half), p1 = frag(P[1] + prow * LT + 16 * s + 8 * half);
+          bf16x8 pp[3];
+#pragma unroll
+          for (int n = 0; n < 3; ++n) pp[n] = frag(P[n] + prow * LT + 16 * s + 8 * half);
           if constexpr (DELTA) {
             float x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = w[8 * s + j];
-            bf16x8 wp[2];
-            split<2>(x, wp);
-            o = mma(p1, wp[0], o);
-            o = mma(p0, wp[1], o);
-            o = mma(p0, wp[0], o);
+            bf16x8 wp[3];
+            split<3>(x, wp);
+            o = mma(pp[2], wp[0], o);
+            o = mma(pp[1], wp[1], o);
+            o = mma(pp[0], wp[2], o);
+            o = mma(pp[1], wp[0], o);
+            o = mma(pp[0], wp[1], o);
+            o = mma(pp[0], wp[0], o);
           } else {
-            o = mma(p1, vb[s], o);
-            o = mma(p0, vb[s], o);
+#pragma unroll
+            for (int n = 2; n >= 0; --n) o = mma(pp[n], vb[s], o);
           }
         }
         // ---- S = 2^(c_end) S + K^T diag(tail) W ----------------------------------------------------------
