@@ -452,7 +452,7 @@ size_t seed_prefill_workspace_bytes(const seed_shape *shape, const seed_prompt *
  *   q, k    [tokens][key_heads][d_k] rows (io_dtype): head h uses key head h / (heads / key_heads).
  *   v, o    [tokens][heads][d_v] rows (io_dtype); o is written.
  *   beta    float [tokens][heads]; g float [tokens][heads] (GDN, Mamba-2) or [tokens][heads][d_k]
- *           (KDA), 0 <= g.
+ *           (KDA), 0 <= g (any size; bf16 prompts are fastest where no gate passes 1).
  *   S0      float [batch][heads][d_k][d_v]: the states the sequences start from, or NULL for zeros.
  *   S       written, same layout: the states after each sequence's last token (S0's, or zeros, for
  *           an empty one). May be S0 itself.

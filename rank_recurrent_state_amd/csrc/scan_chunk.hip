@@ -251,10 +251,11 @@ struct Tiles {
   // by the chunk's number modulo 3: one in use, one that T and P are formed of, one arriving
   Tile<DK> K[3], Q[3];
   Tile<DV> V[3];                  // v, then o
-  struct Gates {
+  struct alignas(16) Gates {
     float ch[C], cl[C];           // c as a sum of two floats
     float head[C], tail[C];       // 2^c_t, 2^(c_end - c_t)
     float beta[C], g[C];
+    float wild;                   // NaN when a gate is outside 0 .. 1, else 0
   } gates[3];
   // by the chunk's number modulo 2
   uint16_t P[2][3][C * LT];
@@ -278,7 +279,8 @@ __device__ __forceinline__ void fetch_tile(const uint16_t* base, int64_t stride,
 }
 
 // The gates of the chunk at f0: log2 g summed over the chunk, and the weights that follow. sum_gates
-// returns the chunk's whole sum.
+// returns the chunk's whole sum, minus infinity where a gate is 0. The weights are for gates of at most
+// 1, whose products only fall; other chunks are marked and run token after token.
 __device__ __forceinline__ void load_gates(const ScanArgs& A, int h, int64_t f0, int64_t hi, float& g, float& beta) {
   const int64_t f1 = f0 + (threadIdx.x & 31);
   const int64_t at = (f1 < hi ? f1 : hi - 1) * A.heads + h;
@@ -289,7 +291,7 @@ __device__ __forceinline__ void load_gates(const ScanArgs& A, int h, int64_t f0,
 template <class Gates>
 __device__ __forceinline__ double sum_gates(Gates& G, float g, float beta) {
   const int l = fresh(threadIdx.x & 63), l32 = l & 31;
-  // g = 0 counts as 2^-200: across it every weight underflows to 0, as it should
+  // g = 0 counts as 2^-200: with no gate above 1, every weight across it underflows to 0, as it should
   const float lg = log2f(g);
   double c = lg < -200.f ? -200.0 : static_cast<double>(lg);
 #pragma unroll
@@ -309,7 +311,9 @@ __device__ __forceinline__ double sum_gates(Gates& G, float g, float beta) {
     G.beta[l] = beta;
     G.g[l] = g;
   }
-  return all;
+  const bool wild = __any(!(g >= 0.f && g <= 1.f)), none = __any(g == 0.f);
+  if (l == 0) G.wild = wild ? __builtin_nanf("") : 0.f;
+  return none ? -__builtin_inf() : all;
 }
 
 // 2^(c_t - c_s) for t = l32 and the 16 s of the lane's accumulator registers.
@@ -686,8 +690,8 @@ __global__ __launch_bounds__(DV * 4, KIND != SEED_MAMBA2 && DK == 128 && DV == 6
       }
 
       // A value that is not finite would reach the tokens before its own through the zeros of T and P:
-      // such a chunk runs token after token instead.
-      float fin = 0.f;
+      // such a chunk runs token after token instead, as does one with a gate outside 0 .. 1.
+      float fin = G.wild;
 #pragma unroll
       for (int i = 0; i < 16; ++i) fin = fmaf(w[i], 0.f, fin);
       if (__builtin_expect(__any(!(fin == 0.f)), 0)) {
