@@ -691,7 +691,9 @@ __global__ __launch_bounds__(DV * 4, KIND != SEED_MAMBA2 && DK == 128 && DV == 6
 
       // A value that is not finite would reach the tokens before its own through the zeros of T and P:
       // such a chunk runs token after token instead, as does one with a gate outside 0 .. 1.
+      // W has met the state in GDN; in Mamba-2 any row of Q S shows a state that is not finite.
       float fin = G.wild;
+      if constexpr (!DELTA) fin = out ? fmaf(qs[0], 0.f, fin) : fin;
 #pragma unroll
       for (int i = 0; i < 16; ++i) fin = fmaf(w[i], 0.f, fin);
       if (__builtin_expect(__any(!(fin == 0.f)), 0)) {
