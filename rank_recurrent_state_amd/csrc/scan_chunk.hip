@@ -58,7 +58,9 @@ struct Split {
   int64_t slots;   // segments at most
   float* A;        // [slots][heads][d_k][d_k]; Mamba-2: [slots][heads], the product of the segment's gates
   float* B;        // [slots][heads][d_k][d_v]
+  int32_t* bad;    // [batch][heads][kParts]: whether a join's wavefront met a value that is not finite
 };
+constexpr int kParts = 64;  // wavefronts of the joins of a unit, at most
 
 // Row m of a 32-row operand tile holds token or channel perm(m), which puts 8 consecutive ones into
 // a lane's accumulator registers 0..7 and 8..15: register i of lane half h is 16 (i / 8) + 8 h + i % 8.
@@ -545,6 +547,17 @@ __global__ __launch_bounds__(DV * 4, KIND != SEED_MAMBA2 && DK == 128 && DV == 6
         if (seg == 0) continue;
         init = W.B + in_ws - static_cast<int64_t>(A.heads) * (DK * DV);
         dest = last ? A.S + at : nullptr;
+        // A S + B is not the state where either is infinite or NaN (0 times infinity, a segment's A that
+        // overflows next to a state of zeros): then one workgroup runs all that follows the first segment.
+        constexpr int kJoins = DELTA ? (DV / 32) * (DK / 32) : DK * DV / 256;
+        const int32_t* bad = W.bad + (static_cast<int64_t>(b) * A.heads + h) * kParts;
+        const int lane = threadIdx.x & 63;
+        if (__any(lane < kJoins && bad[lane] != 0)) {
+          if (seg != 1) continue;
+          int64_t first;
+          sequence_rows(A.offsets, b, A.tokens, first, hi);
+          dest = A.S + at;
+        }
       }
     }
     lo = __builtin_amdgcn_readfirstlane(static_cast<int>(lo));  // rows are below 2^31
@@ -844,6 +857,7 @@ __global__ __launch_bounds__(DK * 2) void k_join_delta(const ScanArgs A, const S
   const int64_t room = W.slots - base;
   const int n = static_cast<int>(segs - 1 < room ? segs - 1 : room);
   if (n > 0) load(0);
+  float fin = 0.f;  // NaN once a state is not finite
   for (int seg = 0; seg < n; ++seg) {
     acc = nb;
 #pragma unroll
@@ -863,9 +877,12 @@ __global__ __launch_bounds__(DK * 2) void k_join_delta(const ScanArgs A, const S
       const int row = 32 * wave + 8 * (i / 4) + 4 * half + i % 4;
       Sh[row * LS + l32] = acc[i];
       if (seg > 0) Bs[row * DV + col] = acc[i];
+      fin = fmaf(acc[i], 0.f, fin);
     }
     __syncthreads();
   }
+  const bool bad = __any(!(fin == 0.f));
+  if (lane == 0) W.bad[(static_cast<int64_t>(b) * A.heads + h) * kParts + blockIdx.x % (DV / 32) * (DK / 32) + wave] = bad;
 }
 
 // The same where A_seg is the product of the segment's gates: a thread follows 4 elements of a state.
@@ -877,6 +894,7 @@ __global__ __launch_bounds__(256) void k_join_scalar(const ScanArgs A, const Spl
   int64_t base, lo, hi;
   const int segs = first_segment(A, W, b, base, lo, hi);
   f32x4 S = {};
+  float fin = 0.f;  // NaN once a state is not finite
 #pragma unroll 4
   for (int seg = 0; seg + 1 < segs && base + seg < W.slots; ++seg) {
     const int64_t slot = (base + seg) * A.heads + h;
@@ -884,9 +902,14 @@ __global__ __launch_bounds__(256) void k_join_scalar(const ScanArgs A, const Spl
     const f32x4 x = *Bs;
     const float a = W.A[slot];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) S[e] = seg > 0 ? fmaf(a, S[e], x[e]) : x[e];
+    for (int e = 0; e < 4; ++e) {
+      S[e] = seg > 0 ? fmaf(a, S[e], x[e]) : x[e];
+      fin = fmaf(S[e], 0.f, fin);
+    }
     if (seg > 0) *Bs = S;
   }
+  const bool bad = __any(!(fin == 0.f));
+  if ((threadIdx.x & 63) == 0) W.bad[static_cast<int64_t>(unit) * kParts + blockIdx.x % PARTS * 4 + (threadIdx.x >> 6)] = bad;
 }
 
 namespace {
@@ -947,7 +970,9 @@ void join(const seed_shape& sh, const ScanArgs& a, const Split& w, hipStream_t s
 
 size_t scan_chunk_workspace(const seed_shape& sh, int64_t tokens) {
   const Split w = plan_split(sh, tokens);
-  return static_cast<size_t>(floats_of_B(sh, w) + floats_of_A(sh, w)) * sizeof(float);
+  if (w.slots == 0) return 0;
+  return static_cast<size_t>(floats_of_B(sh, w) + floats_of_A(sh, w)) * sizeof(float) +
+         static_cast<size_t>(sh.batch) * sh.heads * kParts * sizeof(int32_t);
 }
 
 hipError_t launch_scan_chunk(const seed_shape& sh, const ScanArgs& a, hipStream_t s) {
@@ -962,6 +987,7 @@ hipError_t launch_scan_chunk(const seed_shape& sh, const ScanArgs& a, hipStream_
   const bool delta = sh.kind != SEED_MAMBA2;
   w.B = static_cast<float*>(a.ws);
   w.A = w.B + floats_of_B(sh, w);
+  w.bad = reinterpret_cast<int32_t*>(w.A + floats_of_A(sh, w));
   const int64_t items = w.slots * a.heads;
   w.pass = 1;
   hipLaunchKernelGGL(fn, dim3(loop_blocks(items * (delta ? 2 : 1))), threads, 0, s, a, w, items * (delta ? 2 : 1));

@@ -53,3 +53,39 @@ def test_mamba2_from_infinite_states(dk, dv, small):
     S0[0, 0, 5, 7], S0[1, 1, 60, 33], S0[1, 1, 2, 0] = float("inf"), float("-inf"), float("nan")
     o, S = _check(rrs, torch, ref.MAMBA2, lens, t, S0, (heads, dk, dv))
     assert np.isposinf(o[:70, 0, 7]).all() and np.isneginf(S[1, 1, 60, 33]) and np.isfinite(o[:70, 1]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("strong", [False, True])
+def test_cut_mamba2_prompts_with_infinite_values(d, strong):
+    """An infinite value's column stays infinite through the segments behind it, whatever their gates' product."""
+    rrs, torch = _rrs()
+    lens, heads = [2600, 1500], 2
+    g = _gen(torch, d)
+    t = _positive(torch, g, ref.MAMBA2, 4100, heads, d, d)
+    if strong:
+        t[4][300:] *= 0.5
+    t[2][400, 0, 3], t[2][1000, 1, 40], t[2][2600 + 700, 1, 11] = float("inf"), float("-inf"), float("nan")
+    S0 = torch.randn(2, heads, d, d, device="cuda", generator=g)
+    S0[1, 0, 9, 9] = float("inf")
+    o, S = _check(rrs, torch, ref.MAMBA2, lens, t, S0, (heads, d, d))
+    assert np.isposinf(o[400:2600, 0, 3]).all() and np.isneginf(S[0, 1, :, 40]).all() and np.isposinf(S[1, 0, 9, 9])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_cut_gdn_prompts_whose_transitions_overflow(d):
+    """Keys longer than the delta rule holds, under values of zero: the state is zero until the first
+    value, whatever the product of the transitions before it."""
+    rrs, torch = _rrs()
+    lens, heads = [2600], 2
+    g = _gen(torch, 5 * d)
+    q, k, v, beta, gate = _scan_inputs(torch, g, ref.GDN, 2600, heads, 1, d, d, "bf16")
+    v[:1400] = 0
+    k[200:1300] *= 8
+    t = (q, k, v, beta, gate)
+    o, S = _check(rrs, torch, ref.GDN, lens, t, None, (heads, d, d))
+    assert (o[:1400] == 0).all() and np.isfinite(S).all()
+    # the states of a second sequence beside it are its own
+    more = tuple(torch.cat([x, x[1400:], x[1400:]]) for x in t)
+    o, S = _check(rrs, torch, ref.GDN, [2600, 2400], more, None, (heads, d, d))
+    assert np.isfinite(S).all()
