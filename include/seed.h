@@ -387,10 +387,10 @@ int seed_dense_decode_step(const seed_shape *shape, float *S, const void *q, con
  * host: entries are clamped into 0 .. tokens and a decreasing pair reads as an empty sequence, so
  * wrong ones give wrong results but no access outside the buffers.
  *
- * Rows. Row buffers take a row stride, in elements, of at least the row's width; inside a row,
+ * Rows. Row buffers take a row stride, in elements, of at least the row's width and at most 2^40; inside a row,
  * heads and values are contiguous, so that q, k and v can be column ranges of one buffer. io_dtype
- * is SEED_F32 or SEED_BF16. tokens or rows may be 0, and are at most 2^31 - 1 (else
- * SEED_ERR_UNSUPPORTED). Outputs must not overlap each other or the inputs except where an entry says
+ * is SEED_F32 or SEED_BF16. tokens or rows may be 0, and are at most 2^31 - 1, and a buffer's rows span
+ * at most 2^56 bytes (else SEED_ERR_UNSUPPORTED). Outputs must not overlap each other or the inputs except where an entry says
  * so; an overlap is SEED_ERR_ARG (two buffers of different strides whose ranges meet count as
  * overlapping). Arithmetic is fp32, rounded once to io_dtype.
  */

@@ -11,7 +11,8 @@
 namespace {
 
 constexpr int64_t kMostRows = (int64_t{1} << 31) - 1;  // offsets are int32
-constexpr int64_t kMostStride = int64_t{1} << 40;      // rows times stride stays far inside 64 bits
+constexpr int64_t kMostStride = int64_t{1} << 40;      // a row's bytes stay far inside 64 bits
+constexpr int64_t kMostBytes = int64_t{1} << 56;       // of a buffer, so that its offsets and end stay inside 64 bits
 
 bool io_ok(int32_t d) { return d == SEED_F32 || d == SEED_BF16 || d == SEED_F16; }
 int64_t io_bytes(int32_t d) { return d == SEED_F32 ? 4 : 2; }
@@ -23,6 +24,8 @@ bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride
 struct Rows {
   const void* p;
   int64_t rows, stride, width;
+  // within the address range that the kernels' and these checks' arithmetic holds
+  bool fits() const { return p == nullptr || rows <= 0 || stride <= 0 || (rows <= kMostBytes / stride && lo() <= UINTPTR_MAX - kMostBytes); }
   uintptr_t lo() const { return reinterpret_cast<uintptr_t>(p); }
   uintptr_t hi() const { return lo() + static_cast<uintptr_t>((rows - 1) * stride + width); }
 };
@@ -38,8 +41,13 @@ bool overlap(const Rows& a, const Rows& b) {
   // row i of b starts d behind some row position of a and ends before the next one
   return !(d >= static_cast<uintptr_t>(a.width) && d + static_cast<uintptr_t>(b.width) <= st);
 }
-// A buffer of `bytes` bytes.
-Rows flat(const void* p, int64_t bytes) { return Rows{p, 1, bytes, bytes}; }
+// A buffer of `count` times `bytes` bytes.
+Rows flat(const void* p, int64_t count, int64_t bytes) { return Rows{p, count, bytes, bytes}; }
+bool all_fit(std::initializer_list<Rows> all) {
+  for (const Rows& r : all)
+    if (!r.fits()) return false;
+  return true;
+}
 // Whether one of `outs` shares a byte with one of `ins` or with another of `outs`.
 bool any_overlap(std::initializer_list<Rows> outs, std::initializer_list<Rows> ins) {
   for (const Rows* o = outs.begin(); o != outs.end(); ++o) {
@@ -103,9 +111,10 @@ int seed_prefill_conv(const seed_conv* conv, int64_t tokens, const int32_t* offs
   // rows before a tile and the old window are read by other workgroups than those that write
   const Rows rx{x, tokens, x_stride * e, ch * e}, ry{y, tokens, y_stride * e, ch * e};
   const Rows wi{window_in, conv->batch, wrow, wrow}, wo{window_out, conv->batch, wrow, wrow};
-  if (any_overlap({ry, wo}, {rx, wi, flat(weight, ch * conv->width * 4), flat(bias, ch * 4),
-                             flat(offsets, (static_cast<int64_t>(conv->batch) + 1) * 4)}))
-    return SEED_ERR_ARG;
+  const Rows fw = flat(weight, conv->width, ch * 4), fb = flat(bias, ch, 4);
+  const Rows fo = flat(offsets, static_cast<int64_t>(conv->batch) + 1, 4);
+  if (!all_fit({rx, ry, wi, wo, fw, fb, fo})) return SEED_ERR_UNSUPPORTED;
+  if (any_overlap({ry, wo}, {rx, wi, fw, fb, fo})) return SEED_ERR_ARG;
   seed::ConvArgs a{};
   a.tokens = tokens;
   a.batch = conv->batch;
@@ -138,7 +147,8 @@ int seed_decode_conv(const seed_conv* conv, const uint8_t* active, const void* x
   const int64_t wrow = ch * (conv->width - 1) * e;
   const Rows rx{x, conv->batch, x_stride * e, ch * e}, ry{y, conv->batch, y_stride * e, ch * e};
   const Rows wi{window_in, conv->batch, wrow, wrow}, wo{window_out, conv->batch, wrow, wrow};
-  const Rows fw = flat(weight, ch * conv->width * 4), fb = flat(bias, ch * 4), fa = flat(active, conv->batch);
+  const Rows fw = flat(weight, conv->width, ch * 4), fb = flat(bias, ch, 4), fa = flat(active, conv->batch, 1);
+  if (!all_fit({rx, ry, wi, wo, fw, fb, fa})) return SEED_ERR_UNSUPPORTED;
   if (any_overlap({ry, wo}, {fw, fb, fa}) || overlap(wo, rx) || overlap(wi, ry) || (overlap(rx, ry) && !same(rx, ry)) ||
       (overlap(wi, wo) && !same(wi, wo)))
     return SEED_ERR_ARG;
@@ -179,15 +189,16 @@ int seed_prefill_scan(const seed_shape* sh, const seed_prompt* prompt, const voi
   const Rows rv{v, n, prompt->v_stride * e, vw}, ro{o, n, prompt->o_stride * e, vw};
   const int64_t sw = static_cast<int64_t>(sh->d_k) * sh->d_v * 4, units = static_cast<int64_t>(sh->batch) * sh->heads;
   const Rows s0{S0, units, sw, sw}, s1{S, units, sw, sw};
-  const Rows fb = flat(beta, n * sh->heads * 4), fo = flat(prompt->offsets, (static_cast<int64_t>(sh->batch) + 1) * 4);
-  const Rows fg = flat(g, n * sh->heads * 4 * (sh->kind == SEED_KDA ? sh->d_k : 1));
+  const Rows fb = flat(beta, n, static_cast<int64_t>(sh->heads) * 4), fo = flat(prompt->offsets, static_cast<int64_t>(sh->batch) + 1, 4);
+  const Rows fg = flat(g, n, static_cast<int64_t>(sh->heads) * 4 * (sh->kind == SEED_KDA ? sh->d_k : 1));
+  if (!all_fit({rq, rk, rv, ro, s0, s1, fb, fg, fo})) return SEED_ERR_UNSUPPORTED;
   if (any_overlap({ro, s1}, {rq, rk, rv, fb, fg, fo}) || overlap(ro, s0) || (overlap(s0, s1) && !same(s0, s1)))
     return SEED_ERR_ARG;
   const size_t need = seed_prefill_workspace_bytes(sh, prompt);
   if (need > 0) {
     if (!ws || ws_bytes < need) return SEED_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return SEED_ERR_ARG;
-    if (any_overlap({flat(ws, static_cast<int64_t>(need))}, {rq, rk, rv, ro, s0, s1, fb, fg, fo})) return SEED_ERR_ARG;
+    if (any_overlap({flat(ws, static_cast<int64_t>(need), 1)}, {rq, rk, rv, ro, s0, s1, fb, fg, fo})) return SEED_ERR_ARG;
   }
   seed::ScanArgs a{};
   a.tokens = n;
@@ -232,12 +243,16 @@ int seed_norm_rows(const seed_rows* rows, const void* x, const seed_head_norm* n
   if (rows->io_dtype == SEED_F16) return SEED_ERR_UNSUPPORTED;
   if (rows->rows > kMostRows) return SEED_ERR_UNSUPPORTED;
   const Rows rx{x, rows->rows, rows->x_stride * e, w * e}, ry{y, rows->rows, rows->y_stride * e, w * e};
-  const Rows rg{norm->gate, rows->rows, rows->gate_stride * e, w * e}, rs{skip, rows->rows, rows->skip_stride * e, w * e};
-  const Rows rt{total, rows->rows, rows->total_stride * e, w * e};
+  const Rows none{};  // the strides of absent buffers are not looked at
+  const Rows rg = norm->gate ? Rows{norm->gate, rows->rows, rows->gate_stride * e, w * e} : none;
+  const Rows rs = skip ? Rows{skip, rows->rows, rows->skip_stride * e, w * e} : none;
+  const Rows rt = total ? Rows{total, rows->rows, rows->total_stride * e, w * e} : none;
+  const Rows fw = flat(norm->weight, w, 4), fs = flat(scale, rows->heads, 4);
+  if (!all_fit({rx, ry, rg, rs, rt, fw, fs})) return SEED_ERR_UNSUPPORTED;
   for (const Rows& in : {rx, rg, rs})
     for (const Rows& out : {ry, rt})
       if (overlap(in, out) && !same(in, out)) return SEED_ERR_ARG;
-  if (any_overlap({ry, rt}, {flat(norm->weight, w * 4), flat(scale, static_cast<int64_t>(rows->heads) * 4)})) return SEED_ERR_ARG;
+  if (any_overlap({ry, rt}, {fw, fs})) return SEED_ERR_ARG;
   if (rows->rows == 0) return SEED_OK;
   seed::NormArgs a{};
   a.rows = rows->rows;
