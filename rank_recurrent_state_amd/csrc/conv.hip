@@ -11,7 +11,7 @@
 // chip alike; a tile inside one sequence takes a loop without boundary checks whose loads are all
 // issued first. Channel counts, strides or addresses that do not allow 16-byte accesses take
 // the same kernels with one channel per thread. Sums are fp32 and rounded once.
-// Measured: 32768 rows of 16 prompts x 8192 bf16 channels, windows carried, 193 us (5.6 TB/s); 512 tokens x
+// Measured: 32768 rows of 16 prompts x 8192 bf16 channels, windows carried, 194 us (5.5 TB/s); 512 tokens x
 // 12288 bf16 channels 22 us (4.6 TB/s); one channel per thread, 3001 rows x 1037 fp32 channels, 11.7 us
 // (2.1 TB/s, the call included).
 #include "common.hpp"
@@ -23,14 +23,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = 16;  // rows of a prompt tile
-
-// y / (1 + e^-y). 16-bit outputs take the hardware exponential and reciprocal (relative error
-// below 2^-20, far under the output's rounding); fp32 ones the library's.
-template <int DT>
-__device__ __forceinline__ float silu(float y) {
-  if constexpr (DT == 0) return y / (1.f + expf(-y));
-  else return y * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * y));
-}
 
 template <int DT, int VEC>
 __device__ __forceinline__ void load_row(const void* base, int64_t at, float (&out)[VEC]) {
@@ -63,8 +55,9 @@ struct Taps {
       float s = b[e];
 #pragma unroll
       for (int j = 0; j < W; ++j) s = fmaf(w[j][e], x[j][e], s);
-      y[e] = act ? silu<DT>(s) : s;
+      y[e] = s;
     }
+    if (act) silu<DT>(y);
   }
 };
 

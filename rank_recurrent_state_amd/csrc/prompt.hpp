@@ -89,6 +89,34 @@ __device__ __forceinline__ void sequence_rows(const int32_t* __restrict__ offset
   lo = l;
   hi = h;
 }
+
+// y / (1 + e^-y) in the place of every y. 16-bit outputs take the hardware exponential and reciprocal,
+// fp32 ones the library's. The rounding of the exponential's argument grows with |y|: the relative
+// error is below 2^-20 for |y| <= 8 and 2^-17 for y >= -80, where a 16-bit output is rounded by 2^-9. Below
+// -80 the sum is e^-y and would overflow, and its reciprocal underflow, while y e^y is a normal
+// number down to -91: there y e^(y/2) e^(y/2), good to 2^-16. One branch for all N: with one for each,
+// 32768 rows x 8192 bf16 channels of the convolution take 199 us instead of 194.
+template <int DT, int N>
+__device__ __forceinline__ void silu(float (&y)[N]) {
+  float low = y[0];
+#pragma unroll
+  for (int e = 1; e < N; ++e) low = fminf(low, y[e]);
+  float r[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if constexpr (DT == 0) r[e] = y[e] / (1.f + expf(-y[e]));
+    else r[e] = y[e] * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * y[e]));
+  }
+  if (__builtin_expect(low < -80.f, 0)) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float h = DT == 0 ? expf(0.5f * y[e]) : __builtin_amdgcn_exp2f(0.7213475204444817f * y[e]);
+      if (y[e] < -80.f) r[e] = y[e] * h * h;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) y[e] = r[e];
+}
 #endif
 
 }  // namespace seed
