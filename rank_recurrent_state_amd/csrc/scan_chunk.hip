@@ -929,24 +929,31 @@ constexpr int64_t kCUs = 256;
 // A and B of all segments side by side (A: the recurrence from the identity with v = 0; a product of
 // gates for Mamba-2), the states between them follow, and a second pass gives the read-outs.
 // n = slots / units + 1 segments fill the chip once with the read-outs, and once (Mamba-2) or twice (GDN, whose
-// A and B are two runs) with the first pass: 2 / n or 3 / n of the serial time, and about 50 us.
-// Measured, cut and whole, us:           1024 tokens   2048        8192
-//   GDN 128 x 128,    16 units               89, 121   107, 229   278, 891
-//                     64                    136, 123   198, 229   655, 896
-//                     85                    148, 124   234, 230   779, 895
-//                    128                    165, 124   281, 232   961, 894
-//   Mamba-2 128 x 64, 16                     56, 82     59, 156    91, 600
-//                    128                     80, 85    116, 157   399, 611
-//                    256                    101, 88    172, 161   597, 609
-// and 512 tokens are always faster whole (GDN 77, 66; Mamba-2 54, 45).
+// A and B are two runs) with the first pass: 2 / n or 3 / n of the serial time, and about 50 us. Three
+// segments of Mamba-2 with d_v = 64 gain less, since the two workgroups of a compute unit slow each other.
+// Measured, cut and whole, us:           1024 tokens   2048        4096        8192
+//   GDN 128 x 128,    16 units               90, 129   107, 247   173, 484   262, 958
+//                     64                    133, 130   193, 250   339, 487   632, 968
+//                     85 (n = 4)            145, 130   232, 251   413, 487   770, 965
+//                    128 (n = 3)            166, 131   287, 251   525, 490  1004, 968
+//   Mamba-2 128 x 64, 16                     58, 89     62, 171    67, 337    95, 668
+//                    128                     85, 92    123, 175   222, 344   419, 680
+//                    170 (n = 4)             89, 92    147, 176   268, 344   510, 680
+//                    176 (n = 3)            108, 95    183, 177   344, 345   662, 679
+//                    256                    107, 93    188, 178   348, 347   670, 682
+//           128 x 128, 128 (n = 3)           88, 95    145, 180   265, 351   520, 692
+// and 512 tokens are always faster whole (GDN 80, 69; Mamba-2 56, 48).
 Split plan_split(const seed_shape& sh, int64_t tokens) {
   Split w{};
   const bool delta = sh.kind != SEED_MAMBA2;
   const int64_t units = static_cast<int64_t>(sh.batch) * sh.heads, mean = tokens / sh.batch;
-  const int64_t slots = kCUs * (!delta && sh.d_v == 64 ? 2 : 1);  // workgroups that fit the chip at once
+  // Workgroups that fit the chip at once. Two of GDN with 64 x 64 would fit a compute unit too; its rule was
+  // measured with one.
+  const int64_t slots = kCUs * (!delta && sh.d_v == 64 ? 2 : 1);
   const int64_t n = slots / units + 1;
   if (delta && sh.d_k != sh.d_v) return w;  // A is run as a state of d_k x d_k
-  if (n < (delta ? 4 : 3) || mean < (delta && n < 9 ? 2048 : 1024)) return w;
+  const int64_t least = delta ? (n < 9 ? 2048 : 1024) : (n == 3 && sh.d_v == 64 ? 4096 : 1024);
+  if (n < (delta ? 4 : 3) || mean < least) return w;
   int64_t seg = (mean + n - 1) / n;
   seg = (seg < 256 ? 256 : seg) + C - 1;
   w.tokens = static_cast<int32_t>(seg / C * C);
