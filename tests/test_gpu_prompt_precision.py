@@ -77,3 +77,24 @@ def test_readouts_that_cancel_over_two_tokens(kind, dk, dv):
     f, b = _np(first)[:, :, None], _np(beta)[1::2][:, :, None]
     tol[1::2] += 2.0 ** -20 * size * (f + b if kind == ref.MAMBA2 else f + b + b * f)
     _close(_np(o), want, tol)
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_keys_that_cancel_over_the_state(dk, dv):
+    """The delta rule's own read: every key reads two rows of the state, one the other's negative up to
+    2^-13, and puts what it read back. Sums of three pieces for each of two rows and three additions to the
+    state, 10 half-steps of 2^-24 of a row's value: 2^-20 is 16; a row cut to 16 bits is off by up to 64."""
+    rrs, torch = _rrs()
+    heads, n = 3, dk // 2
+    g = _gen(torch, 5 * dk + dv)
+    S0 = torch.randn(1, heads, dk, dv, device="cuda", generator=g)
+    S0[:, :, 1::2] = S0[:, :, 0::2] * (2.0 ** -13 * torch.randn(1, heads, n, dv, device="cuda", generator=g) - 1)
+    k = torch.zeros(n, 1, dk, device="cuda")
+    k[torch.arange(n), 0, 2 * torch.arange(n)] = 1
+    k[torch.arange(n), 0, 2 * torch.arange(n) + 1] = 1
+    v = torch.zeros(n, heads, dv, device="cuda")
+    ones = torch.ones(n, heads, device="cuda")
+    t = (k.bfloat16(), k.bfloat16(), v.bfloat16(), ones, ones)
+    _, S = _run_scan(rrs, torch, ref.GDN, [n], t, S0, (heads, dk, dv), "bf16")
+    _, want, _ = ref.scan(ref.GDN, [n], *map(_np, t), _np(S0))
+    _close(_np(S), want, 2.0 ** -20 * np.abs(_np(S0)))
