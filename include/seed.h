@@ -450,6 +450,8 @@ size_t seed_prefill_workspace_bytes(const seed_shape *shape, const seed_prompt *
  * with the read-out o_t = S_t^T q_t.
  *   shape   kind, batch (sequences), heads, d_k, d_v and io_dtype; the other fields are ignored.
  *   q, k    [tokens][key_heads][d_k] rows (io_dtype): head h uses key head h / (heads / key_heads).
+ *           Taken as they are: GDN and KDA need keys of unit length (beta |k|^2 below 2, or the states
+ *           grow without bound), which seed_norm_rows gives with weight 1 / sqrt(d_k).
  *   v, o    [tokens][heads][d_v] rows (io_dtype); o is written.
  *   beta    float [tokens][heads]; g float [tokens][heads] (GDN, Mamba-2) or [tokens][heads][d_k]
  *           (KDA), 0 <= g (any size; bf16 prompts are fastest where no gate passes 1).
@@ -458,6 +460,10 @@ size_t seed_prefill_workspace_bytes(const seed_shape *shape, const seed_prompt *
  *           an empty one). May be S0 itself.
  *   ws      workspace of seed_prefill_workspace_bytes bytes, 16-byte aligned (NULL when that is 0);
  *           it must not be shared by calls that may run at the same time.
+ * How a call runs goes by its sizes, not by the offsets: bf16 GDN and Mamba-2 prompts of 16 tokens or more on
+ * average take 32 tokens at a time, and few prompts of 1024 or more on average are cut into segments that run
+ * side by side; all else goes token after token. One long prompt among many short ones is faster in a
+ * call of its own.
  * q, k, v, o, S0, S (and KDA's g) must be 16-byte aligned and the row strides multiples of 16 bytes,
  * else SEED_ERR_ARG. States are fp32 and every product with a state or a value takes fp32 operands;
  * sums are fp32.
