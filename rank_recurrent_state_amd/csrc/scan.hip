@@ -178,8 +178,12 @@ ScanFn pick_scan(const seed_shape& sh, Layout l) {
 namespace {
 // Whether the chunked kernel takes the call: bf16 rows and a gate per head, rows near enough for 32 of
 // them to lie within a 31-bit offset, and prompts of 16 tokens or more on average. Chunked and token
-// after token, 1024 GDN units of 128 x 128: 57 and 40 us at 8 tokens, 57 and 57 at 16, 58 and 90 at 32;
-// 256 units: 15 and 17, 16 and 23, 16 and 35.
+// after token, from zeros, us:        8 tokens     12          16          24          32
+//   GDN 128 x 128,   1024 units       49, 33       49, 42      48, 49      48, 65      48, 81
+//                     256             17, 14       17, 17      17, 20      17, 26      17, 33
+//                      32             13, 10       14, 11      13, 11      14, 14      14, 17
+//   Mamba-2 128 x 64, 1024            22, 22       22, 26      22, 31      22, 40      22, 49
+// The lengths themselves are on the device: one long prompt among many short ones goes by the average too.
 bool takes_chunks(const seed_shape& sh, int64_t tokens, int64_t longest_stride) {
   return sh.io_dtype == SEED_BF16 && sh.kind != SEED_KDA && tokens >= 16 * static_cast<int64_t>(sh.batch) &&
          longest_stride < (int64_t{1} << 24);

@@ -24,12 +24,14 @@
 // chunks ahead, T and P are formed a chunk ahead, so that a chunk costs one barrier and the state's
 // wavefronts wait for nothing else.
 //
-// What bounds it: the vector unit. A state wavefront spends 800 to 900 vector instructions on a GDN chunk (half
-// of them on the pieces of S) next to 82 matrix ones; over 32768 tokens x 32 GDN heads the vector unit is busy
-// 52 % of the time and the matrix unit 28 %, and bank conflicts take 10 % of the LDS cycles. A chunk
-// takes 3.8 us on a compute unit of its own, 32768 GDN tokens x 32 heads 534 us (2.1 TB/s of rows and
-// states), the same tokens x 64 Mamba-2 heads 455 us. 64-token chunks would split S half as often but
-// need 64 accumulators more than the 256 registers; two workgroups per compute unit do not fit LDS.
+// What bounds it: waits inside a chunk. A state wavefront spends about 940 vector instructions on a GDN chunk
+// (half of them on the pieces of S) next to 96 matrix ones, in a chain K S, W, O, S; with one state and one
+// preparing wavefront per SIMD to cover its waits, neither unit is full: over 32768 tokens x 32 GDN heads
+// the vector unit is busy 50 % of the time and the matrix unit 30 % (Mamba-2, 64 heads: 47 % and 19 %), and
+// bank conflicts take 10 % of the LDS cycles. A chunk takes 3.8 us on a compute unit of its own, 32768
+// GDN tokens x 32 heads 589 us (1.95 TB/s of rows and states), the same tokens x 64 Mamba-2 heads
+// 523 us. 64-token chunks would split S half as often but need 64 accumulators more than the 256
+// registers; two GDN workgroups per compute unit fit LDS at 64 x 64 only.
 #include "common.hpp"
 #include "prompt.hpp"
 
@@ -433,8 +435,8 @@ __device__ __forceinline__ void form_T(Tile<DK>& K, const Gates& G, uint16_t (&T
 
 // The sequence that is `rank`-th by length, longest first (the earlier of two equal ones first); with
 // more than kRanked sequences simply sequence `rank`. Workgroups start in block order, and a long
-// sequence started last would be run by a few of them alone: 16 prompts of 0 to 3646 tokens x 64
-// Mamba-2 heads take 528 us in the order given and 460 us longest first. Called by the whole workgroup.
+// sequence started last would be run by a few of them alone: with read-outs in 16 bits, 16 prompts of 0
+// to 3646 tokens x 64 Mamba-2 heads took 528 us in the order given and 460 us longest first. Called by the whole workgroup.
 template <int NT>
 __device__ __forceinline__ int ranked_sequence(const ScanArgs& A, int rank, int32_t (&len)[kRanked], int32_t& found) {
   if (A.batch > kRanked) return rank;
@@ -490,10 +492,15 @@ __device__ __forceinline__ int first_segment(const ScanArgs& A, const Split& W, 
 
 // Wavefronts 0 .. NW - 1 hold 32 columns of the state each and run a chunk while the NH others prepare:
 // T and P of the next chunk, and rows and gates of the one after it. Preparing in the state's own
-// wavefronts instead, with two workgroups per compute unit, took 704 us where this takes 673 (32768 GDN
-// tokens) and 1436 where this takes 936 (one 8192-token prompt, uncut).
+// wavefronts instead, with two workgroups per compute unit, took 704 us where this took 673 (32768 GDN
+// tokens, at the same stage) and 1436 where this took 936 (one 8192-token prompt, uncut).
+//
+// The launch bound is the wavefronts of a SIMD that LDS lets run together, two at most: DV = 128 brings two,
+// DV = 64 one, or two where a second workgroup fits. One leaves 512 registers to a wavefront, two 256.
 template <int KIND, int DK, int DV>
-__global__ __launch_bounds__(DV * 4, KIND != SEED_MAMBA2 && DK == 128 && DV == 64 ? 1 : 2) void k_scan_chunk(const ScanArgs A, const Split W, int64_t items) {
+constexpr int kWavesPerSimd = DV == 64 && 2 * sizeof(Tiles<KIND, DK, DV>) > 160 * 1024 ? 1 : 2;
+template <int KIND, int DK, int DV>
+__global__ __launch_bounds__(DV * 4, (kWavesPerSimd<KIND, DK, DV>)) void k_scan_chunk(const ScanArgs A, const Split W, int64_t items) {
   using TL = Tiles<KIND, DK, DV>;
   constexpr bool DELTA = TL::DELTA;
   constexpr int NW = DV / 32, NH = NW, NT = (NW + NH) * 64;
