@@ -454,7 +454,8 @@ size_t seed_prefill_workspace_bytes(const seed_shape *shape, const seed_prompt *
  *           grow without bound), which seed_norm_rows gives with weight 1 / sqrt(d_k).
  *   v, o    [tokens][heads][d_v] rows (io_dtype); o is written.
  *   beta    float [tokens][heads]; g float [tokens][heads] (GDN, Mamba-2) or [tokens][heads][d_k]
- *           (KDA), 0 <= g (any size; bf16 prompts are fastest where no gate passes 1).
+ *           (KDA), 0 <= g (any size; bf16 prompts are slower where gates above 1 bring a
+ *           product of up to 32 of them above 2^50, or stand next to one below 2^-50).
  *   S0      float [batch][heads][d_k][d_v]: the states the sequences start from, or NULL for zeros.
  *   S       written, same layout: the states after each sequence's last token (S0's, or zeros, for
  *           an empty one). May be S0 itself.

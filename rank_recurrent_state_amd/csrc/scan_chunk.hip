@@ -30,7 +30,7 @@
 // the vector unit is busy 50 % of the time and the matrix unit 30 % (Mamba-2, 64 heads: 47 % and 19 %), and
 // bank conflicts take 10 % of the LDS cycles. A chunk takes 3.8 us on a compute unit of its own, 32768
 // GDN tokens x 32 heads 589 us (1.95 TB/s of rows and states), the same tokens x 64 Mamba-2 heads
-// 523 us. 64-token chunks would split S half as often but need 64 accumulators more than the 256
+// 513 us. 64-token chunks would split S half as often but need 64 accumulators more than the 256
 // registers; two GDN workgroups per compute unit fit LDS at 64 x 64 only.
 #include "common.hpp"
 #include "prompt.hpp"
@@ -259,7 +259,7 @@ struct Tiles {
     float ch[C], cl[C];           // c as a sum of two floats
     float head[C], tail[C];       // 2^c_t, 2^(c_end - c_t)
     float beta[C], g[C];
-    float wild;                   // NaN when a gate is outside 0 .. 1, else 0
+    float wild;                   // NaN when the chunk has to run token after token, else 0
   } gates[3];
   // by the chunk's number modulo 2
   uint16_t P[2][3][C * LT];
@@ -283,8 +283,10 @@ __device__ __forceinline__ void fetch_tile(const uint16_t* base, int64_t stride,
 }
 
 // The gates of the chunk at f0: log2 g summed over the chunk, and the weights that follow. sum_gates
-// returns the chunk's whole sum, minus infinity where a gate is 0. The weights are for gates of at most
-// 1, whose products only fall; other chunks are marked and run token after token.
+// returns the chunk's whole sum, minus infinity where a gate is 0. Products of gates of at most 1 only fall, and
+// those that underflow stay 0. Next to a gate above 1 every product has to be a normal number, below 2^100
+// here: other chunks, and those with gates that are negative or not finite, are marked and run token
+// after token.
 __device__ __forceinline__ void load_gates(const ScanArgs& A, int h, int64_t f0, int64_t hi, float& g, float& beta) {
   const int64_t f1 = f0 + (threadIdx.x & 31);
   const int64_t at = (f1 < hi ? f1 : hi - 1) * A.heads + h;
@@ -315,7 +317,8 @@ __device__ __forceinline__ double sum_gates(Gates& G, float g, float beta) {
     G.beta[l] = beta;
     G.g[l] = g;
   }
-  const bool wild = __any(!(g >= 0.f && g <= 1.f)), none = __any(g == 0.f);
+  const bool wild = __any(!(g >= 0.f && g < __builtin_inff())) || (__any(g > 1.f) && __any(c < -50.0 || c > 50.0));
+  const bool none = __any(g == 0.f);
   if (l == 0) G.wild = wild ? __builtin_nanf("") : 0.f;
   return none ? -__builtin_inf() : all;
 }
@@ -710,7 +713,7 @@ __global__ __launch_bounds__(DV * 4, (kWavesPerSimd<KIND, DK, DV>)) void k_scan_
       }
 
       // A value that is not finite would reach the tokens before its own through the zeros of T and P:
-      // such a chunk runs token after token instead, as does one with a gate outside 0 .. 1.
+      // such a chunk runs token after token instead, as does one whose gates are marked.
       // W has met the state in GDN; in Mamba-2 any row of Q S shows a state that is not finite.
       float fin = G.wild;
       if constexpr (!DELTA) fin = out ? fmaf(qs[0], 0.f, fin) : fin;

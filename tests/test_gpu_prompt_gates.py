@@ -112,3 +112,19 @@ def test_small_gates_in_cut_prompts(kind, d):
     gate[3800], gate[3999] = 0.0, 0.0
     S0 = torch.randn(2, heads, d, d, device="cuda", generator=g)
     _check(rrs, torch, kind, lens, t, S0, (heads, d, d), "bf16")
+
+
+@pytest.mark.parametrize("kind", [ref.GDN, ref.KDA, ref.MAMBA2])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_gates_around_one(kind, dk, dv):
+    """Growth and decay that nearly cancel, and runs of both whose products stay within 2^50 over 32 tokens and pass it."""
+    rrs, torch = _rrs()
+    lens, heads = [300, 200], 2
+    g = _gen(torch, 11 * kind + dk)
+    t = _scan_inputs(torch, g, kind, 500, heads, 1, dk, dv, "bf16")
+    gate = t[4]
+    gate[:] = 2.0 ** (torch.rand(gate.shape, device="cuda", generator=g) - 0.5)
+    gate[64:94], gate[96:126] = 2.0, 0.5
+    gate[300:348], gate[350:398] = 3.0, 1 / 3.0  # 2^50.7 in a chunk and more
+    S0 = torch.randn(2, heads, dk, dv, device="cuda", generator=g)
+    _check(rrs, torch, kind, lens, t, S0, (heads, dk, dv), "bf16")
