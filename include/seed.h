@@ -508,6 +508,169 @@ typedef struct seed_residual {
 int seed_norm_rows(const seed_rows *rows, const void *x, const seed_head_norm *norm,
                    const seed_residual *residual, void *y, void *stream);
 
+/* ---- the attention layers between the recurrent ones, and drafted tokens -------------------------
+ *
+ * A hybrid model keeps a few softmax-attention layers, whose caches grow with the context and are not
+ * compressed. Per token such a layer turns its queries and keys by their positions, stores the keys and
+ * values, and attends over what is stored; behind the last layer, drafted tokens are checked against the
+ * model's probabilities. Row buffers, strides, offsets, overlaps and limits as for the prompt path
+ * above; io_dtype is SEED_F32 or SEED_BF16, arithmetic fp32 unless said otherwise, rounded once.
+ * Source: picx.dev summary, abstract and "Introduction and Theoretical Foundation" (hybrid models interleave
+ * a few softmax-attention layers with many recurrent ones; their caches are left as they are).
+ */
+
+/* Rotary positions. Pair i of a head's first `dim` values, (x_i, x_{i + dim/2}) or, interleaved,
+ * (x_{2i}, x_{2i+1}), is turned by the angle 2 pi turns[i] position:
+ *     (a, b) <- amplitude (a cos - b sin, a sin + b cos);
+ * the values behind the first dim stay as they are. The angle is reduced in fp64, so that far positions
+ * keep theirs. */
+typedef struct seed_rotary {
+  int32_t dim;          /* rotated values of a head: even, at least 2, at most the head's dim    */
+  int32_t interleaved;  /* 0: pairs (i, i + dim / 2); 1: pairs (2 i, 2 i + 1)                    */
+  float amplitude;      /* finite; 1 unless a long-context scaling has one                       */
+  const double *turns;  /* [dim / 2], device memory: turns per position (frequency / 2 pi)       */
+} seed_rotary;
+
+enum { SEED_ROTARY_PLAIN = 0, SEED_ROTARY_LINEAR = 1, SEED_ROTARY_BASE = 2, SEED_ROTARY_PARTS = 3, SEED_ROTARY_INDEX = 4 };
+
+/* Where the turns come from: base^(-2 i / dim) / (2 pi), and for contexts `factor` times the trained one
+ *   SEED_ROTARY_LINEAR  divided by factor;
+ *   SEED_ROTARY_BASE    with base factor^(dim / (dim - 2)) in the place of base (dim > 2);
+ *   SEED_ROTARY_PARTS   times keep + (1 - keep) / factor, keep = clamp((n - low) / (high - low), 0, 1) with
+ *                       n = length turns, the turns over the trained length: fast pairs stay, slow ones stretch;
+ *   SEED_ROTARY_INDEX   the same with keep falling linearly in i from 1 to 0 between the indices where
+ *                       n = high (rounded down, at least 0) and n = low (rounded up, at most dim - 1). */
+typedef struct seed_rotary_scaling {
+  int32_t kind;
+  double base;       /* > 0 (SEED_ROTARY_INDEX: > 1), finite */
+  double factor;     /* > 0, finite (ignored by SEED_ROTARY_PLAIN) */
+  double length;     /* trained length in tokens, > 0 (PARTS and INDEX; ignored by the others) */
+  double low, high;  /* 0 < low < high (PARTS and INDEX; ignored by the others) */
+} seed_rotary_scaling;
+
+/* Fills turns[0 .. dim / 2 - 1] in HOST memory (the caller copies it to the device once). Host-only, pure. */
+int seed_rotary_turns(const seed_rotary_scaling *scaling, int32_t dim, double *turns);
+
+/*
+ * Rotary positions of rows x [rows][heads][dim] into y: row r is turned by positions[r] (int32
+ * [rows], device memory, any value). Of `rows`, rows, heads, dim, io_dtype, x_stride and y_stride are used.
+ * Queries and keys side by side in one buffer are one call over both heads' columns. y may be x (same
+ * address and stride): then the values behind the rotated ones are not touched.
+ */
+int seed_rotate_rows(const seed_rows *rows, const seed_rotary *rotary, const void *x, const int32_t *positions,
+                     void *y, void *stream);
+
+/*
+ * A paged cache of keys and values. Position p of request b lies in page table[b][p / page], slot p % page;
+ * head h of a slot is `dim` contiguous values at k (or v) + page_stride number + token_stride slot + head_stride h.
+ * Pages are [page][key_heads][dim] (token_stride >= key_heads head_stride) or [key_heads][page][dim] (head_stride >=
+ * page token_stride), without overlaps inside a page or between pages (else SEED_ERR_ARG); k and v have the same
+ * strides and may lie side by side in one buffer.
+ * table entries are read on the device where a position needs them, and not checked on the host: one outside
+ * 0 .. pages - 1 is a page that is not there. A page may be listed by several requests (a shared
+ * prefix); only pages that receive new rows must belong to one.
+ */
+typedef struct seed_cache {
+  int32_t batch;      /* requests                                                                */
+  int32_t key_heads;  /* heads of keys and values                                                */
+  int32_t dim;        /* 64, 128 or 256 (others SEED_ERR_UNSUPPORTED)                              */
+  int32_t io_dtype;   /* SEED_F32 or SEED_BF16                                                   */
+  int32_t page;       /* positions of a page: a power of two, 16 .. 2^20 (others SEED_ERR_UNSUPPORTED) */
+  int32_t width;      /* pages of a request at most; page * width at most 2^31 - 1                */
+  int64_t pages;      /* pages of the pool                                                       */
+  int64_t page_stride, token_stride, head_stride;  /* elements, multiples of 16 bytes             */
+  void *k, *v;            /* 16-byte aligned, device memory                                      */
+  const int32_t *table;   /* [batch][width], device memory                                       */
+} seed_cache;
+
+/*
+ * The new tokens of a call: rows offsets[b] .. offsets[b + 1] - 1 of the row buffers are request b's
+ * newest tokens, and lengths[b] (int32 [batch], device memory) counts the tokens of the request, these
+ * included: row i of n has position lengths[b] - n + i. offsets NULL: one token each, tokens = batch.
+ */
+typedef struct seed_tokens {
+  int64_t tokens;          /* rows of the row buffers                                            */
+  const int32_t *offsets;  /* [batch + 1], device memory, or NULL                                */
+  const int32_t *lengths;  /* [batch], device memory                                             */
+  int32_t heads;           /* heads of the queries: a multiple of key_heads                      */
+  int64_t q_stride, k_stride, v_stride, o_stride;  /* elements between rows; of absent buffers ignored */
+} seed_tokens;
+
+/*
+ * Stores new keys and values at their positions of the cache, prompts and single tokens alike.
+ *   rotary  turns k before it is stored and q into q_out (NULL: no rotation).
+ *   k, v    [tokens][key_heads][dim] rows (io_dtype).
+ *   q       [tokens][heads][dim] rows, or NULL for none; q_out written, same shape (o_stride), may be q.
+ * A row whose position is negative or beyond the table, or whose page is not there, is not stored (its q is still
+ * turned, by that position). Rows of no request are not read or written.
+ */
+int seed_cache_append(const seed_cache *cache, const seed_tokens *tokens, const seed_rotary *rotary, const void *q,
+                      const void *k, const void *v, void *q_out, void *stream);
+
+/* Which keys a call's rows see, and the limits that set its launch. */
+typedef struct seed_attend {
+  int32_t max_tokens;  /* most new tokens of a request, 1 .. 32; a request's rows behind are not written */
+  int32_t max_length;  /* most tokens of a request: larger lengths are taken as this one; at most page * width */
+  int32_t window;      /* > 0: a row sees its own position and the window - 1 before it; 0: all */
+  float scale;         /* of the products q . k; finite                                          */
+} seed_attend;
+
+/* Workspace bytes of seed_decode_attend (0: none needed, or invalid arguments). Depends on the sizes
+ * only. Host-only, pure. */
+size_t seed_attend_workspace_bytes(const seed_cache *cache, const seed_tokens *tokens, const seed_attend *attend);
+
+/*
+ * Attention of every request's new tokens over its cache, which holds them already (seed_cache_append):
+ *     o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j),  lse = log sum_j w_j
+ * over the positions j that the row sees: up to its own, inside the window, in pages that are there. Query
+ * head h reads key head h / (heads / key_heads). A row that sees no position, or whose scores are all minus
+ * infinity, gets o = 0 and lse = minus infinity. What a position holds that a row does not see, infinities and
+ * NaN too, does not reach that row.
+ *   q, o   [tokens][heads][dim] rows (io_dtype), 16-byte aligned, strides multiples of 16 bytes; o is written.
+ *   lse    float [tokens][heads], written, or NULL.
+ *   ws     workspace of seed_attend_workspace_bytes bytes, 16-byte aligned (NULL when that is 0); it must
+ *          not be shared by calls that may run at the same time.
+ * Long caches of few requests are split over their length and joined (by the sizes: max_length, not lengths, sets
+ * the cut, so a max_length close to the longest request's is faster than a far one). Weights and sums are fp32;
+ * bf16 weights enter the products in two pieces. The same call gives the same bits.
+ */
+int seed_decode_attend(const seed_cache *cache, const seed_tokens *tokens, const seed_attend *attend, const void *q,
+                       void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Drafted tokens to check. Request b has rows offsets[b] .. offsets[b + 1] - 1: row r holds the model's
+ * probabilities for the token behind it, and drafts[r] the token drafted there, but for the request's last row, which
+ * has none (its entries of drafts, uniforms and draft are not read). One row: no draft, a plain draw. */
+typedef struct seed_drafts {
+  int32_t batch, vocab;
+  int32_t io_dtype;        /* SEED_F32 or SEED_BF16: storage of target and draft                 */
+  int64_t rows;
+  const int32_t *offsets;  /* [batch + 1], device memory                                         */
+  int64_t target_stride, draft_stride;  /* elements between rows (of an absent draft ignored)    */
+} seed_drafts;
+
+/* Workspace bytes of seed_verify_drafts (0 for invalid arguments). Host-only, pure. */
+size_t seed_verify_workspace_bytes(const seed_drafts *drafts);
+
+/*
+ * Verification of drafted tokens from given random numbers. A request's drafts are kept in turn while
+ *     uniforms[r] draft[r][x] < target[r][x],  x = drafts[r]         (draft NULL: draft[r][x] = 1)
+ * and the token at the first row where that fails is drawn from max(target - draft, 0) (draft NULL: target without x);
+ * behind a request whose drafts are all kept it is drawn from target. So every token has the model's
+ * distribution. The draw is the smallest token t with draws[b] W < w_0 + .. + w_t, W the sum of all weights w, or
+ * the last token of positive weight if there is none; where no token has a positive weight it is from
+ * target itself, and -1 where that has none either. Weights that are negative or NaN count as 0, drafts outside
+ * 0 .. vocab - 1 are refused. Comparisons and sums are fp64.
+ *   target    [rows][vocab] rows (io_dtype); draft the same, or NULL for drafts that come without probabilities.
+ *   drafts    int32 [rows]; uniforms float [rows], draws float [batch], in [0, 1).
+ *   out       int32 [rows], written: a request's kept drafts, the drawn token, then -1. May be drafts.
+ *   counts    int32 [batch], written: tokens the request gained, drafts kept + 1 (0 for a request of no rows).
+ *   ws        workspace of seed_verify_workspace_bytes bytes, 16-byte aligned; it must not be shared by
+ *             calls that may run at the same time.
+ */
+int seed_verify_drafts(const seed_drafts *d, const void *target, const void *draft, const int32_t *drafts,
+                       const float *uniforms, const float *draws, int32_t *out, int32_t *counts, void *ws,
+                       size_t ws_bytes, void *stream);
+
 /*
  * Streams restricted to a set of compute units, for schedules that run the HBM-bound decode and
  * the arithmetic-bound compression side by side on disjoint parts of the chip. These are the

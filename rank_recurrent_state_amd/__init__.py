@@ -24,6 +24,10 @@ _NAMES = {
     "seed_decode_step_normed", "seed_decode_step_ragged_normed",
     "make_conv", "seed_conv", "seed_decode_conv", "seed_norm_rows", "seed_prefill_conv", "seed_prefill_scan",
     "seed_prefill_workspace_bytes", "seed_prompt", "seed_residual", "seed_rows",
+    "SEED_ROTARY_BASE", "SEED_ROTARY_INDEX", "SEED_ROTARY_LINEAR", "SEED_ROTARY_PARTS", "SEED_ROTARY_PLAIN",
+    "Cache", "Rotary", "make_rotary", "seed_attend", "seed_attend_workspace_bytes", "seed_cache", "seed_cache_append",
+    "seed_decode_attend", "seed_drafts", "seed_rotary", "seed_rotary_scaling", "seed_rotary_turns", "seed_rotate_rows",
+    "seed_tokens", "seed_verify_drafts", "seed_verify_workspace_bytes",
     "seed_scale_len", "seed_shape", "seed_state", "seed_state_bytes", "seed_state_from_dense",
     "seed_status_string", "seed_version", "seed_workspace_bytes",
 }

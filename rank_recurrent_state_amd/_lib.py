@@ -18,6 +18,7 @@ SEED_GDN, SEED_KDA, SEED_MAMBA2 = 0, 1, 2
 SEED_F32, SEED_BF16, SEED_F16 = 0, 1, 2
 SEED_ROUND_NEAREST, SEED_ROUND_STOCHASTIC = 0, 1
 SEED_OP_COMPRESS, SEED_OP_FROM_DENSE = 0, 1
+SEED_ROTARY_PLAIN, SEED_ROTARY_LINEAR, SEED_ROTARY_BASE, SEED_ROTARY_PARTS, SEED_ROTARY_INDEX = 0, 1, 2, 3, 4
 
 EXPORTS = [
     "seed_state_bytes", "seed_scale_len", "seed_workspace_bytes", "seed_state_from_dense",
@@ -26,7 +27,9 @@ EXPORTS = [
     "seed_chunk_max_tokens", "seed_decode_chunk_ragged", "seed_state_spectrum", "seed_compress_units",
     "seed_stream_create_cu_masked", "seed_stream_destroy", "seed_decode_step_normed",
     "seed_decode_step_ragged_normed", "seed_prefill_conv", "seed_decode_conv", "seed_prefill_scan",
-    "seed_prefill_workspace_bytes", "seed_norm_rows", "seed_status_string", "seed_version",
+    "seed_prefill_workspace_bytes", "seed_norm_rows", "seed_rotary_turns", "seed_rotate_rows", "seed_cache_append",
+    "seed_attend_workspace_bytes", "seed_decode_attend", "seed_verify_workspace_bytes", "seed_verify_drafts",
+    "seed_status_string", "seed_version",
 ]
 
 SEED_SPECTRUM_LEN = 33
@@ -72,6 +75,41 @@ class seed_rows(ctypes.Structure):
 
 class seed_residual(ctypes.Structure):
     _fields_ = [("skip", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("total", ctypes.c_void_p)]
+
+
+class seed_rotary(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("turns", ctypes.c_void_p)]
+
+
+class seed_rotary_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("length", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class seed_cache(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("key_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("page", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("table", ctypes.c_void_p)]
+
+
+class seed_tokens(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("heads", ctypes.c_int32), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64)]
+
+
+class seed_attend(ctypes.Structure):
+    _fields_ = [("max_tokens", ctypes.c_int32), ("max_length", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class seed_drafts(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("vocab", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("target_stride", ctypes.c_int64),
+                ("draft_stride", ctypes.c_int64)]
 
 
 class seed_state(ctypes.Structure):
@@ -150,6 +188,17 @@ def _load():
                                              ctypes.c_size_t, P]),
         "seed_norm_rows": (ctypes.c_int, [ctypes.POINTER(seed_rows), P, ctypes.POINTER(seed_head_norm),
                                           ctypes.POINTER(seed_residual), P, P]),
+        "seed_rotary_turns": (ctypes.c_int, [ctypes.POINTER(seed_rotary_scaling), ctypes.c_int32,
+                                             ctypes.POINTER(ctypes.c_double)]),
+        "seed_rotate_rows": (ctypes.c_int, [ctypes.POINTER(seed_rows), ctypes.POINTER(seed_rotary), P, P, P, P]),
+        "seed_cache_append": (ctypes.c_int, [ctypes.POINTER(seed_cache), ctypes.POINTER(seed_tokens),
+                                             ctypes.POINTER(seed_rotary), P, P, P, P, P]),
+        "seed_attend_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(seed_cache), ctypes.POINTER(seed_tokens),
+                                                          ctypes.POINTER(seed_attend)]),
+        "seed_decode_attend": (ctypes.c_int, [ctypes.POINTER(seed_cache), ctypes.POINTER(seed_tokens),
+                                              ctypes.POINTER(seed_attend), P, P, P, P, ctypes.c_size_t, P]),
+        "seed_verify_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(seed_drafts)]),
+        "seed_verify_drafts": (ctypes.c_int, [ctypes.POINTER(seed_drafts), P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
         "seed_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "seed_version": (ctypes.c_char_p, []),
     }
@@ -589,6 +638,22 @@ class _Args:
             raise ValueError(f"{name}: rows overlap (stride {stride[0]}, width {width})")
         return t.data_ptr(), stride[0]
 
+    def workspace(self, need, ws, stream):
+        """The address and size of the caller's workspace, or of one from torch's allocator where the
+        call needs it; the tensor with them, so that it lives until the launch."""
+        if ws is None and need > 0:
+            # made on the stream that uses it, so that its memory's next use is ordered behind
+            torch = self.torch
+            if stream is None and self.device == torch.cuda.current_device():
+                ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            else:
+                on = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
+                with torch.cuda.device(self.device), torch.cuda.stream(on):
+                    ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        if ws is None:
+            return None, 0, None
+        return self.dense("ws", ws, ws.numel(), ws.dtype), ws.numel() * ws.element_size(), ws
+
     def launch(self, fn_name, stream, *args):
         """Calls the entry point on the tensors' device, with its current stream unless one is given."""
         cuda = self.torch.cuda
@@ -703,3 +768,195 @@ def seed_norm_rows(x, weight, y, gate=None, eps: float = 1e-6, gate_first: bool 
     a.launch("seed_norm_rows", stream, ctypes.byref(seed_rows(rows, heads, dim, SEED_F32 if dt is f32 else SEED_BF16, xs, ys,
                                                               gs, ss, ts)),
              xp, ctypes.byref(norm), res, yp)
+
+
+# ---- attention layers and drafted tokens ------------------------------------------------------------
+
+def seed_rotary_turns(dim: int, base: float = 10000.0, scaling: int = SEED_ROTARY_PLAIN, factor: float = 1.0,
+                      length: float = 0.0, low: float = 1.0, high: float = 32.0) -> list:
+    """Turns per position of a head's dim / 2 rotated pairs (see seed_rotary_scaling)."""
+    turns = (ctypes.c_double * max(dim // 2, 1))()
+    how = seed_rotary_scaling(scaling, base, factor, length, low, high)
+    _check("seed_rotary_turns", LIB.seed_rotary_turns(ctypes.byref(how), dim, turns))
+    return list(turns)
+
+
+class Rotary:
+    """Rotary positions of a layer: the first `dim` values of a head in pairs, turned by turns[i] (a float64
+    device tensor) per position."""
+
+    def __init__(self, turns, interleaved: bool = False, amplitude: float = 1.0):
+        import torch
+        if turns.dtype is not torch.float64 or not turns.is_cuda or not turns.is_contiguous() or turns.dim() != 1:
+            raise ValueError("turns: expected a contiguous float64 device vector")
+        self.turns = turns
+        self.c = seed_rotary(2 * turns.numel(), 1 if interleaved else 0, amplitude, turns.data_ptr())
+
+
+def make_rotary(dim: int, base: float = 10000.0, interleaved: bool = False, scaling: int = SEED_ROTARY_PLAIN,
+                factor: float = 1.0, length: float = 0.0, low: float = 1.0, high: float = 32.0, amplitude: float = 1.0,
+                device="cuda") -> Rotary:
+    """The Rotary of seed_rotary_turns, its table on the device."""
+    import torch
+    turns = torch.tensor(seed_rotary_turns(dim, base, scaling, factor, length, low, high), dtype=torch.float64)
+    return Rotary(turns.to(device), interleaved, amplitude)
+
+
+class Cache:
+    """A paged cache (torch tensors used as memory only): k, v [pages, page, key_heads, dim] of one set of
+    strides (values of a head contiguous; a transposed [pages, key_heads, page, dim] is one too), table int32
+    [batch, width]: the pages of each request."""
+
+    def __init__(self, k, v, table):
+        torch, io = _io()
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError(f"k, v: expected [pages, page, key_heads, dim], got {tuple(k.shape)} and {tuple(v.shape)}")
+        if k.dtype is not v.dtype or k.dtype not in io.values():
+            raise ValueError(f"k, v: expected one dtype of {list(io.values())}, got {k.dtype} and {v.dtype}")
+        if table.dim() != 2 or table.dtype is not torch.int32 or not table.is_contiguous():
+            raise ValueError("table: expected a contiguous int32 [batch, width]")
+        for name, t in (("k", k), ("v", v), ("table", table)):
+            if not t.is_cuda:
+                raise ValueError(f"{name}: expected a device tensor")
+            if t.get_device() != k.get_device():
+                raise ValueError(f"{name}: on device {t.get_device()}, k on device {k.get_device()}")
+        pages, page, heads, dim = k.shape
+        # the stride of a single page or head is never used: any that fits
+        strides = []
+        for t in (k, v):
+            p, s, h, d = t.stride()
+            if d != 1 and dim > 1:
+                raise ValueError("k, v: expected contiguous values inside a head")
+            h = h if heads > 1 else dim
+            strides.append((p if pages > 1 else max((page - 1) * s + (heads - 1) * h + dim, 1), s, h))
+        if strides[0] != strides[1]:
+            raise ValueError(f"k, v: expected the same strides, got {k.stride()} and {v.stride()}")
+        align = 16 // k.element_size()
+        p, s, h = strides[0]
+        if pages == 1:
+            p = -(-p // align) * align
+        self.k, self.v, self.table = k, v, table
+        self.device, self.dtype = k.get_device(), k.dtype
+        code = next(c for c, t in io.items() if t is k.dtype)
+        self.c = seed_cache(table.shape[0], heads, dim, code, page, table.shape[1], pages, p, s, h, k.data_ptr(), v.data_ptr(),
+                            table.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+
+def _attention_rows(x, name, heads, dim):
+    if x.dim() != 3 or x.shape[2] != dim or (heads is not None and x.shape[1] != heads):
+        raise ValueError(f"{name}: expected [tokens, {'heads' if heads is None else heads}, {dim}], got {tuple(x.shape)}")
+    return x.shape
+
+
+def seed_rotate_rows(rotary: Rotary, x, positions, y, stream=None) -> None:
+    """Rotary positions of x [rows, heads, dim] (rows may be strided) into y, which may be x: row r by
+    positions[r] (int32 [rows] on the device)."""
+    torch, _ = _io()
+    shape, dt = x.shape, x.dtype
+    if len(shape) != 3:
+        raise ValueError(f"x: expected [rows, heads, dim], got {tuple(shape)}")
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f"x: expected dtype float32 or bfloat16, got {dt}")
+    rows, heads, dim = shape
+    a, width = _Args(torch), heads * dim
+    xp, xs = a.rows("x", x, shape, width, dt)
+    yp, ys = a.rows("y", y, shape, width, dt)
+    a._on("rotary", rotary.turns)
+    a.launch("seed_rotate_rows", stream,
+             ctypes.byref(seed_rows(rows, heads, dim, SEED_F32 if dt is torch.float32 else SEED_BF16, xs, ys)),
+             ctypes.byref(rotary.c), xp, a.dense("positions", positions, rows, torch.int32), yp)
+
+
+def seed_cache_append(cache: Cache, lengths, k, v, offsets=None, rotary: Rotary | None = None, q=None, q_out=None,
+                      stream=None) -> None:
+    """Stores new keys and values k, v [tokens, key_heads, dim] (rows may be strided) at their positions of the
+    cache: request b's rows offsets[b] .. offsets[b + 1] (None: one row each) are the last of its lengths[b] tokens
+    (int32 on the device). rotary turns k by the positions, and q [tokens, heads, dim] into q_out (which may be q)."""
+    torch, _ = _io()
+    c, i32 = cache.c, torch.int32
+    a, dt, dim, kh = _Args(torch), cache.dtype, c.dim, c.key_heads
+    a._on("cache", cache.k)
+    ks = _attention_rows(k, "k", kh, dim)
+    n = ks[0]
+    kp, k_stride = a.rows("k", k, ks, kh * dim, dt)
+    vp, v_stride = a.rows("v", v, ks, kh * dim, dt)
+    heads, qp, op, q_stride, o_stride = 0, None, None, 0, 0
+    if q is not None:
+        heads = _attention_rows(q, "q", None, dim)[1]
+        qp, q_stride = a.rows("q", q, (n, heads, dim), heads * dim, dt)
+        if q_out is None:
+            raise ValueError("q_out: expected a tensor for the queries")
+        op, o_stride = a.rows("q_out", q_out, (n, heads, dim), heads * dim, dt)
+    elif q_out is not None:
+        raise ValueError("q: expected the queries of q_out")
+    if rotary is not None:
+        a._on("rotary", rotary.turns)
+    new = seed_tokens(n, a.dense("offsets", offsets, c.batch + 1, i32), a.dense("lengths", lengths, c.batch, i32), heads,
+                      q_stride, k_stride, v_stride, o_stride)
+    a.launch("seed_cache_append", stream, cache.ref, ctypes.byref(new), None if rotary is None else ctypes.byref(rotary.c),
+             qp, kp, vp, op)
+
+
+def seed_attend_workspace_bytes(cache: Cache, tokens: int, heads: int, max_tokens: int = 1, max_length: int | None = None,
+                                window: int = 0, ragged: bool = False) -> int:
+    """Workspace bytes of seed_decode_attend for `tokens` new rows of `heads` query heads (ragged: the call
+    gets offsets); 0 also for invalid sizes."""
+    c = cache.c
+    new = seed_tokens(tokens, c.table if ragged else None, c.table, heads, heads * c.dim, 0, 0, heads * c.dim)
+    how = seed_attend(max_tokens, c.page * c.width if max_length is None else max_length, window, 1.0)
+    return int(LIB.seed_attend_workspace_bytes(cache.ref, ctypes.byref(new), ctypes.byref(how)))
+
+
+def seed_decode_attend(cache: Cache, lengths, q, o, offsets=None, max_tokens: int = 1, max_length: int | None = None,
+                       scale: float | None = None, window: int = 0, lse=None, ws=None, stream=None) -> None:
+    """Attention of every request's new tokens, q [tokens, heads, dim] (rows may be strided), over its cache,
+    which holds them already, into o. lengths, offsets: as for seed_cache_append; max_tokens: the most new tokens
+    of a request; max_length: the most tokens of a request (None: what the table holds); scale: None for
+    1 / sqrt(dim); window: positions a row sees, 0 for all; lse: float [tokens, heads] or None. ws: a workspace
+    of seed_attend_workspace_bytes bytes; without one, one is taken from torch's allocator when needed."""
+    torch, _ = _io()
+    c, i32 = cache.c, torch.int32
+    a, dt, dim = _Args(torch), cache.dtype, c.dim
+    a._on("cache", cache.k)
+    shape = _attention_rows(q, "q", None, dim)
+    n, heads = shape[0], shape[1]
+    qp, q_stride = a.rows("q", q, shape, heads * dim, dt)
+    op, o_stride = a.rows("o", o, shape, heads * dim, dt)
+    new = ctypes.byref(seed_tokens(n, a.dense("offsets", offsets, c.batch + 1, i32), a.dense("lengths", lengths, c.batch, i32),
+                                   heads, q_stride, 0, 0, o_stride))
+    how = ctypes.byref(seed_attend(max_tokens, c.page * c.width if max_length is None else max_length, window,
+                                   dim ** -0.5 if scale is None else scale))
+    lp = a.dense("lse", lse, n * heads, torch.float32)
+    need = LIB.seed_attend_workspace_bytes(cache.ref, new, how) if ws is None else 0
+    wp, size, ws = a.workspace(need, ws, stream)
+    a.launch("seed_decode_attend", stream, cache.ref, new, how, qp, op, lp, wp, size)
+
+
+def seed_verify_workspace_bytes(batch: int, vocab: int) -> int:
+    return int(LIB.seed_verify_workspace_bytes(ctypes.byref(seed_drafts(batch, vocab, SEED_F32, 0, None, vocab, vocab))))
+
+
+def seed_verify_drafts(target, drafts, uniforms, draws, out, counts, offsets, draft=None, ws=None, stream=None) -> None:
+    """Drafted tokens checked against the model's probabilities: target, draft [rows, vocab] (rows may be
+    strided; draft None for drafts without probabilities), drafts int32 and uniforms float [rows], draws float
+    [batch], offsets int32 [batch + 1]: request b's rows, of which the last has no draft. out int32 [rows]: the
+    kept drafts, the drawn token, then -1; counts int32 [batch]: tokens gained. ws: a workspace of
+    seed_verify_workspace_bytes bytes, taken from torch's allocator without one."""
+    torch, _ = _io()
+    i32, f32, dt = torch.int32, torch.float32, target.dtype
+    if target.dim() != 2:
+        raise ValueError(f"target: expected [rows, vocab], got {tuple(target.shape)}")
+    if dt is not torch.bfloat16 and dt is not f32:
+        raise ValueError(f"target: expected dtype float32 or bfloat16, got {dt}")
+    a, shape, batch = _Args(torch), target.shape, counts.numel()
+    n, vocab = shape
+    tp, t_stride = a.rows("target", target, shape, vocab, dt)
+    dp, d_stride = a.rows("draft", draft, shape, vocab, dt)
+    d = ctypes.byref(seed_drafts(batch, vocab, SEED_F32 if dt is f32 else SEED_BF16, n, a.dense("offsets", offsets, batch + 1, i32),
+                                 t_stride, d_stride))
+    ptrs = (a.dense("drafts", drafts, n, i32), a.dense("uniforms", uniforms, n, f32), a.dense("draws", draws, batch, f32),
+            a.dense("out", out, n, i32), a.dense("counts", counts, batch, i32))
+    need = LIB.seed_verify_workspace_bytes(d) if ws is None else 0
+    wp, size, ws = a.workspace(need, ws, stream)
+    a.launch("seed_verify_drafts", stream, d, tp, dp, *ptrs, wp, size)
