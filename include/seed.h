@@ -564,8 +564,8 @@ int seed_rotate_rows(const seed_rows *rows, const seed_rotary *rotary, const voi
  * A paged cache of keys and values. Position p of request b lies in page table[b][p / page], slot p % page;
  * head h of a slot is `dim` contiguous values at k (or v) + page_stride number + token_stride slot + head_stride h.
  * Pages are [page][key_heads][dim] (token_stride >= key_heads head_stride) or [key_heads][page][dim] (head_stride >=
- * page token_stride), without overlaps inside a page or between pages (else SEED_ERR_ARG); k and v have the same
- * strides and may lie side by side in one buffer.
+ * page token_stride), without overlaps inside a page or between pages (else SEED_ERR_ARG), token_stride at most 2^24
+ * (else SEED_ERR_UNSUPPORTED); k and v have the same strides and may lie side by side in one buffer.
  * table entries are read on the device where a position needs them, and not checked on the host: one outside
  * 0 .. pages - 1 is a page that is not there. A page may be listed by several requests (a shared
  * prefix); only pages that receive new rows must belong to one.
@@ -576,7 +576,7 @@ typedef struct seed_cache {
   int32_t dim;        /* 64, 128 or 256 (others SEED_ERR_UNSUPPORTED)                              */
   int32_t io_dtype;   /* SEED_F32 or SEED_BF16                                                   */
   int32_t page;       /* positions of a page: a power of two, 16 .. 2^20 (others SEED_ERR_UNSUPPORTED) */
-  int32_t width;      /* pages of a request at most; page * width at most 2^31 - 1                */
+  int32_t width;      /* pages of a request at most; page * width at most 2^30                    */
   int64_t pages;      /* pages of the pool                                                       */
   int64_t page_stride, token_stride, head_stride;  /* elements, multiples of 16 bytes             */
   void *k, *v;            /* 16-byte aligned, device memory                                      */
@@ -612,7 +612,7 @@ typedef struct seed_attend {
   int32_t max_tokens;  /* most new tokens of a request, 1 .. 32; a request's rows behind are not written */
   int32_t max_length;  /* most tokens of a request: larger lengths are taken as this one; at most page * width */
   int32_t window;      /* > 0: a row sees its own position and the window - 1 before it; 0: all */
-  float scale;         /* of the products q . k; finite                                          */
+  float scale;         /* of the products q . k; finite and not 0                                */
 } seed_attend;
 
 /* Workspace bytes of seed_decode_attend (0: none needed, or invalid arguments). Depends on the sizes

@@ -28,8 +28,21 @@ using f32x4 = __attribute__((ext_vector_type(4))) float;
 using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
 using u32x2 = __attribute__((ext_vector_type(2))) uint32_t;
 using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
+using global_char = __attribute__((address_space(1))) char;
+using scalar_int = __attribute__((address_space(4))) int32_t;  // read by scalar loads, which vector loads do not wait for
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Keeps an address that is the same for the whole wavefront in scalar registers.
+__device__ __forceinline__ const global_char* scalar(const char* p) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a)), hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+  return reinterpret_cast<const global_char*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+template <typename T>
+__device__ __forceinline__ T load(const global_char* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const __attribute__((address_space(1))) T*>(p));
+}
 
 // Maximum / sum over the four lanes that share lane % 16.
 __device__ __forceinline__ float max4(float v) {
@@ -49,6 +62,31 @@ __device__ __forceinline__ float sum4(float v) {
   y = v;
   lane_swap32(x, y);
   return x + y;
+}
+
+// The largest magnitudes of two words' values (of both halves side by side for 16-bit values), whether one is
+// an infinity or NaN, and a word with those set to 0.
+template <int DT>
+__device__ __forceinline__ uint32_t largest(uint32_t a, uint32_t b) {
+  using u16x2 = __attribute__((ext_vector_type(2))) uint16_t;
+  if constexpr (DT == 0) return max(a, b & 0x7fffffffu);
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b & 0x7fff7fffu)));
+}
+template <int DT>
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  if constexpr (DT == 0) return (w & 0x7f800000u) == 0x7f800000u;
+  else return (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  if constexpr (DT == 0) return (w & 0x7f800000u) == 0x7f800000u ? 0u : w;
+  else return ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u) | ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu);
+}
+
+// log of sum 2^max.
+__device__ __forceinline__ float natural_log_sum(float max, float sum) {
+  return sum == 0.f ? kNegInf : static_cast<float>((static_cast<double>(max) + log2(static_cast<double>(sum))) * 0.6931471805599453);
 }
 
 // The positions that the rows of a request see between them: keys [k0, k1), row i at first + i.
@@ -84,310 +122,376 @@ struct Tile {
   static constexpr int VC = D / (16 * VE);
   static constexpr int kOut = D / 16;                 // accumulators of 16 rows: value 16 VE c + VE m + j in number VE c + j
   static constexpr int kWords = VE * kBytes / 4;
+  static constexpr int kRow = D * kBytes;             // bytes of a key
+  static constexpr int kLine = kRow / 16;             // lanes that load a row of 16 bytes each,
+  static constexpr int kAtOnce = kWave / kLine;       // and rows of one load
+  static constexpr int kTile = kKeys * kRow;
+  // Where LDS holds 16-byte piece c of key r: the pieces of a row trade places so that 16 rows' pieces of one
+  // number lie in different banks.
+  static __device__ __forceinline__ uint32_t piece(int r, int c) {
+    return r * kRow + ((c ^ (kLine == 8 ? (r >> 1) & 7 : r & 15)) << 4);
+  }
 };
 
 }  // namespace
 
-template <int DT, int D, int MT>
-__global__ __launch_bounds__(kThreads) void k_attend(const AttendArgs A, int row_blocks, int64_t units) {
+// RW wavefronts take 16 rows each of the same keys, kWaves / RW of them other keys.
+template <int DT, int D, int RW>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attend(const AttendArgs A, unsigned row_blocks, unsigned units) {
   using L = Tile<DT, D>;
   using T = stor_t<DT>;
+  constexpr int KW = kWaves / RW;
   constexpr int GT = L::kOut < 8 ? L::kOut : 8;  // accumulators joined at a time
-  __shared__ float stat[kWaves][MT * 16][2];
-  __shared__ f32x4 red[kWaves][GT][kWave];
+  // A wavefront's keys (RW = 1), or all wavefronts' keys and values, twice; at the end the accumulators.
+  constexpr int kJoin = kWaves * GT * kWave * 16, kTiles = RW == 1 ? kWaves * L::kTile : 4 * L::kTile;
+  __shared__ __attribute__((aligned(16))) char smem[kJoin > kTiles ? kJoin : kTiles];
+  __shared__ float weights[kWaves][L::kKeys * 16];
+  __shared__ float stat[kWaves][16][2];
 
-  // row blocks of one unit read the same keys: on the same XCD, one after the other
-  const int64_t id = blockIdx.x;
-  const int64_t group = id / (8 * row_blocks);
-  const int within = static_cast<int>(id - group * 8 * row_blocks);
-  const int rb = within / 8;
-  const int64_t unit = group * 8 + within % 8;
-  if (unit >= units) return;
+  // Workgroups go to the 8 XCDs in turn. The row blocks of a unit read the same keys: they follow one
+  // another on one XCD. Otherwise neighbouring heads, whose keys lie side by side, run on different ones (5 % faster
+  // than on the same).
   const CacheArgs& C = A.c;
+  const unsigned group = blockIdx.x / (8 * row_blocks), within = blockIdx.x % (8 * row_blocks);
+  const int rb = static_cast<int>(within / 8);
+  const unsigned unit = group * 8 + within % 8;
+  if (unit >= units) return;
   const int kh = static_cast<int>(unit % C.key_heads);
-  const int64_t rest = unit / C.key_heads;
+  const unsigned rest = unit / C.key_heads;
   const int b = static_cast<int>(rest % C.batch), split = static_cast<int>(rest / C.batch);
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const Span sp = span_of(A, b);
   const int share = C.heads / C.key_heads;
-  const int rows = sp.n * share, row0 = rb * MT * 16;
-  if (row0 >= rows || split >= max(sp.used, 1)) return;
+  const int rows = sp.n * share, block0 = rb * RW * 16;
+  if (block0 >= rows || split >= max(sp.used, 1)) return;
 
-  // this lane's row of each 16: a query of key head kh
-  int pos[MT];
-  u32x4 Q[MT][L::kQ];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int r = row0 + 16 * t + l16;
-    const int token = r / share;
-    pos[t] = r < rows ? sp.first + token : -1;
+  // this lane's row of the wavefront's 16: a query of key head kh
+  const int row0 = block0 + 16 * (wave % RW);
+  const int r = row0 + l16, token = r / share;
+  const int pos = r < rows ? sp.first + token : -1;
+  u32x4 Q[L::kQ];
+  {
     const T* q = static_cast<const T*>(A.q) + (sp.lo + token) * A.q_stride + static_cast<int64_t>(kh * share + r - token * share) * D;
 #pragma unroll
     for (int c = 0; c < L::kQ; ++c) {
-      Q[t][c] = u32x4{0, 0, 0, 0};
-      if (r < rows) Q[t][c] = *reinterpret_cast<const u32x4*>(q + c * 4 * L::kVec + g * L::kVec);
+      Q[c] = u32x4{0, 0, 0, 0};
+      if (r < rows) Q[c] = *reinterpret_cast<const u32x4*>(q + c * 4 * L::kVec + g * L::kVec);
+      Q[c] ^= A.negate;
     }
   }
 
-  f32x4 O[MT][L::kOut];
-  float m[MT], l[MT];
+  f32x4 O[L::kOut];
+  float m = kNegInf, l = 0.f;
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    m[t] = kNegInf;
-    l[t] = 0.f;
-#pragma unroll
-    for (int j = 0; j < L::kOut; ++j) O[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int j = 0; j < L::kOut; ++j) O[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int from = sp.base + split * A.chunk;
   const int to = static_cast<int>(min(static_cast<int64_t>(from) + A.chunk, static_cast<int64_t>(sp.k1)));
   const int last_pos = sp.first + sp.n - 1;
-  const int32_t* __restrict__ table = C.table + static_cast<int64_t>(b) * C.width;
-  const T* __restrict__ kb = static_cast<const T*>(C.k) + kh * C.head_stride;
-  const T* __restrict__ vb = static_cast<const T*>(C.v) + kh * C.head_stride;
-  const int64_t ts = C.token_stride;
+  const scalar_int* table = reinterpret_cast<const scalar_int*>(reinterpret_cast<uintptr_t>(C.table + static_cast<int64_t>(b) * C.width));
+  // a lane's place within 16 positions, in bytes; the positions' page is the same for the whole wavefront
+  const char* __restrict__ kb = reinterpret_cast<const char*>(static_cast<const T*>(C.k) + kh * C.head_stride);
+  const char* __restrict__ vb = reinterpret_cast<const char*>(static_cast<const T*>(C.v) + kh * C.head_stride);
+  const int64_t ts = C.token_stride * L::kBytes;
+  const uint32_t in_k = static_cast<uint32_t>(l16 * ts) + g * 16, in_v = static_cast<uint32_t>(4 * g * ts) + l16 * L::VE * L::kBytes;
   const int in_page = (1 << C.page_shift) - 1;
 
-  for (int t0 = from + wave * L::kKeys; t0 < to; t0 += kWaves * L::kKeys) {
-    // the 16 positions of a part lie in one page; parts behind the last key read the last one's
-    bool there[L::kSub];
+  // The places of a tile's parts: 16 positions lie in one page; parts behind this workgroup's last read that again.
+  struct Where {
     int64_t at[L::kSub];
+    bool there[L::kSub];
+  };
+  auto find = [&](int t0) {
+    Where w;
 #pragma unroll
     for (int u = 0; u < L::kSub; ++u) {
-      const int p = min(t0 + 16 * u, (sp.k1 - 1) & ~15);
-      const int64_t number = table[p >> C.page_shift];
-      there[u] = number >= 0 && number < C.pages;
-      at[u] = (there[u] ? number : 0) * C.page_stride + (p & in_page) * ts;
+      const int p = min(t0 + 16 * u, (to - 1) & ~15);
+      const int number = table[p >> C.page_shift];
+      w.there[u] = number >= 0 && number < C.pages;
+      w.at[u] = (w.there[u] ? number : 0) * C.page_stride * L::kBytes + (p & in_page) * ts;
     }
-    u32x4 K[L::kSub][L::kQ];
+    return w;
+  };
+  // Whole rows per load, 16 bytes per lane: 6.6 TB/s of keys and values, 5.7 with the 64 bytes of 16 rows that the
+  // products take; and past the caches, which keep nothing of a cache read once a step (5.9 with them).
+  constexpr int kLoads = L::kKeys / L::kAtOnce / RW;
+  const int my_row = lane / L::kLine, my_piece = lane % L::kLine, share_of = RW == 1 ? 0 : wave;
+  const uint32_t in_row = static_cast<uint32_t>(my_row * ts) + my_piece * 16;
+  u32x4 K[kLoads], Vr[kLoads];
+  auto load_rows = [&](const char* pool, const Where& w, u32x4 (&x)[kLoads]) {
 #pragma unroll
-    for (int u = 0; u < L::kSub; ++u)
+    for (int i = 0; i < kLoads; ++i) {
+      const int first = (i * RW) * L::kAtOnce;  // the first wavefront's first row
+      const int row = first + share_of * L::kAtOnce;
+      int64_t at = w.at[0];
+      if constexpr (L::kSub == 2) at = row < 16 ? w.at[0] : w.at[1];
+      x[i] = load<u32x4>(scalar(pool + at + row % 16 * ts) + in_row);
+    }
+  };
+  uint32_t V[4 * L::kSub][L::VC][L::kWords];
+  // RW = 1: values straight to where the products take them
+  auto load_v = [&](const Where& w) {
 #pragma unroll
-      for (int c = 0; c < L::kQ; ++c)
-        K[u][c] = *reinterpret_cast<const u32x4*>(kb + at[u] + l16 * ts + c * 4 * L::kVec + g * L::kVec);
-    uint32_t V[4 * L::kSub][L::VC][L::kWords];
-    auto load_v = [&]() {
+    for (int i = 0; i < 4 * L::kSub; ++i) {
+      const global_char* base = scalar(vb + w.at[i / 4] + i % 4 * ts);
+#pragma unroll
+      for (int c = 0; c < L::VC; ++c) {
+        const global_char* p = base + in_v + c * 16 * L::VE * L::kBytes;
+        if constexpr (L::kWords == 4) {
+          const u32x4 x = load<u32x4>(p);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) V[i][c][e] = x[e];
+        } else {
+          const u32x2 x = load<u32x2>(p);
+          V[i][c][0] = x[0];
+          V[i][c][1] = x[1];
+        }
+      }
+    }
+  };
+
+  // Keys are loaded a tile ahead, as soon as the last ones are in LDS, values while the scores are formed (RW > 1:
+  // a tile ahead too): something is always on its way.
+  constexpr int kTurn = KW * L::kKeys;
+  Where here{};
+  const int start = from + (RW == 1 ? wave * L::kKeys : 0);
+  if (from < to) {
+    here = find(start);
+    load_rows(kb, here, K);
+    if constexpr (RW > 1) load_rows(vb, here, Vr);
+  }
+  int turn = 0;
+  for (int t0 = start; t0 < to; t0 += kTurn) {
+    char* keys = smem + (RW == 1 ? wave * L::kTile : turn * 2 * L::kTile);
+    turn ^= 1;
+    if constexpr (RW == 1) load_v(here);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = (i * RW + share_of) * L::kAtOnce + my_row;
+      *reinterpret_cast<u32x4*>(keys + L::piece(row, my_piece)) = K[i];
+      if constexpr (RW > 1) *reinterpret_cast<u32x4*>(keys + L::kTile + row * L::kRow + my_piece * 16) = Vr[i];
+    }
+    const Where next = find(t0 + kTurn);
+    load_rows(kb, next, K);  // behind the last tile one that is there: the loads on their way are then the same in number
+    if constexpr (RW > 1) {
+      load_rows(vb, next, Vr);
+      // the tile is whole; the other one is free once every wavefront is past this point in the next turn
+      __syncthreads();
+    } else {
+      wave_lds_sync();
+    }
+
+    f32x4 S[L::kSub];
+#pragma unroll
+    for (int u = 0; u < L::kSub; ++u) {
+      S[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < L::kQ; ++c) {
+        const u32x4 k = *reinterpret_cast<const u32x4*>(keys + L::piece(16 * u + l16, 4 * c + g));
+        if constexpr (DT == 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            S[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[e]), __uint_as_float(Q[c][e]), S[u], 0, 0, 0);
+        } else {
+          S[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k), __builtin_bit_cast(bf16x8, Q[c]), S[u], 0, 0, 0);
+        }
+      }
+    }
+    if constexpr (RW > 1) {
 #pragma unroll
       for (int i = 0; i < 4 * L::kSub; ++i)
 #pragma unroll
         for (int c = 0; c < L::VC; ++c) {
-          const T* p = vb + at[i / 4] + (4 * g + i % 4) * ts + c * 16 * L::VE + l16 * L::VE;
-          if constexpr (L::kWords == 4) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+          const char* p = keys + L::kTile + (16 * (i / 4) + 4 * g + i % 4) * L::kRow + (c * 16 + l16) * L::VE * L::kBytes;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) V[i][c][e] = w[e];
-          } else {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-            V[i][c][0] = w[0];
-            V[i][c][1] = w[1];
-          }
+          for (int e = 0; e < L::kWords; ++e) V[i][c][e] = reinterpret_cast<const uint32_t*>(p)[e];
         }
-    };
-    load_v();
-
-    f32x4 S[MT][L::kSub];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int u = 0; u < L::kSub; ++u) {
-        S[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < L::kQ; ++c) {
-          if constexpr (DT == 0) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              S[t][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(K[u][c][e]), __uint_as_float(Q[t][c][e]), S[t][u], 0, 0, 0);
-          } else {
-            S[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, K[u][c]), __builtin_bit_cast(bf16x8, Q[t][c]),
-                                                              S[t][u], 0, 0, 0);
-          }
-        }
-      }
+    } else {
+      wave_lds_sync();  // the next tile's keys go to the same place
+    }
 
     // some row does not see some position of the tile
     bool edge = t0 < sp.k0 || t0 + L::kKeys > sp.first + 1 || (A.window > 0 && t0 <= last_pos - A.window);
 #pragma unroll
-    for (int u = 0; u < L::kSub; ++u) edge = edge || !there[u];
-    auto sees = [&](int p, int i) {  // position p, key i of this lane
-      const int key = t0 + 16 * (i / 4) + 4 * g + i % 4;
-      return there[i / 4] && key <= p && (A.window <= 0 || key > p - A.window);
-    };
-
-    float P[MT][4 * L::kSub];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      float top = kNegInf;
-#pragma unroll
-      for (int i = 0; i < 4 * L::kSub; ++i) {
-        float x = S[t][i / 4][i % 4] * A.scale2;
-        if (edge && !sees(pos[t], i)) x = kNegInf;
-        top = fmaxf(top, x);
-      }
-      if (__any(top > m[t] + 8.f)) {
-        const float now = fmaxf(m[t], max4(top));
-        // nothing summed so far, or all of it of weight 0: 2^(-inf)
-        const float f = now == kNegInf ? 1.f : exp2_(m[t] - now);
-        m[t] = now;
-        l[t] *= f;
-#pragma unroll
-        for (int j = 0; j < L::kOut; ++j) O[t][j] *= f;
-      }
-      const float sub = m[t] == kNegInf ? 0.f : m[t];
-#pragma unroll
-      for (int i = 0; i < 4 * L::kSub; ++i) {
-        float p = exp2_(fmaf(S[t][i / 4][i % 4], A.scale2, -sub));
-        if (edge && !sees(pos[t], i)) p = 0.f;
-        P[t][i] = p;
-        l[t] += p;
-      }
-    }
-
-    auto values = [&](int t, f32x4 (&acc)[L::kOut], int only) {  // only >= 0: of this row alone
-      if constexpr (DT == 0) {
-#pragma unroll
-        for (int c = 0; c < L::VC; ++c)
-#pragma unroll
-          for (int j = 0; j < L::VE; ++j) {
-            f32x4 z = acc[c * L::VE + j];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(V[i][c][j]), P[t][i], z, 0, 0, 0);
-            if (only < 0 || l16 == only) acc[c * L::VE + j] = z;
-          }
-      } else {
-        u32x4 hi, lo;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          hi[i] = pack2<1>(P[t][2 * i], P[t][2 * i + 1]);
-          lo[i] = pack2<1>(P[t][2 * i] - lo16<1>(hi[i]), P[t][2 * i + 1] - hi16<1>(hi[i]));
-        }
-#pragma unroll
-        for (int c = 0; c < L::VC; ++c)
-#pragma unroll
-          for (int j = 0; j < L::VE; ++j) {
-            u32x4 a;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              a[i] = __builtin_amdgcn_perm(V[2 * i + 1][c][j / 2], V[2 * i][c][j / 2], j % 2 == 0 ? 0x05040100u : 0x07060302u);
-            f32x4 z = acc[c * L::VE + j];
-            z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, hi), z, 0, 0, 0);
-            z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, lo), z, 0, 0, 0);
-            if (only < 0 || l16 == only) acc[c * L::VE + j] = z;
-          }
-      }
-    };
-    auto clear_v = [&](int i) {
-#pragma unroll
-      for (int c = 0; c < L::VC; ++c)
-#pragma unroll
-        for (int e = 0; e < L::kWords; ++e) V[i][c][e] = 0;
-    };
-
-    bool apart = false;
+    for (int u = 0; u < L::kSub; ++u) edge = edge || !here.there[u];
     if (edge) {
-      // A weight of 0 does not keep an infinity or NaN out of a product. Values that no row sees become 0; where
-      // those that some rows see are not all finite, the rows are taken one at a time.
-      uint32_t bad = 0;
 #pragma unroll
       for (int i = 0; i < 4 * L::kSub; ++i) {
         const int key = t0 + 16 * (i / 4) + 4 * g + i % 4;
-        if (!there[i / 4] || key < sp.k0 || key >= sp.k1) clear_v(i);
+        const bool seen = here.there[i / 4] && key <= pos && (A.window <= 0 || key > pos - A.window);
+        S[i / 4][i % 4] = seen ? S[i / 4][i % 4] : kNegInf;
+      }
+    }
+    float top = kNegInf;
+#pragma unroll
+    for (int i = 0; i < 4 * L::kSub; ++i) top = fmaxf(top, S[i / 4][i % 4]);
+    top *= A.scale2;
+    if (__any(top > m + 8.f)) {
+      const float now = fmaxf(m, max4(top));
+      // nothing summed so far, or all of it of weight 0: 2^(-inf)
+      const float f = now == kNegInf ? 1.f : exp2_(m - now);
+      m = now;
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < L::kOut; ++j) O[j] *= f;
+    }
+    const float sub = m == kNegInf ? 0.f : m;
+    float P[4 * L::kSub];
+#pragma unroll
+    for (int i = 0; i < 4 * L::kSub; ++i) {
+      P[i] = exp2_(fmaf(S[i / 4][i % 4], A.scale2, -sub));
+      l += P[i];
+    }
+    u32x4 hi, lo;
+    if constexpr (DT != 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        hi[i] = pack2<1>(P[2 * i], P[2 * i + 1]);
+        lo[i] = pack2<1>(P[2 * i] - lo16<1>(hi[i]), P[2 * i + 1] - hi16<1>(hi[i]));
+      }
+    }
+    auto product = [&](int c, int j, f32x4 z) {
+      if constexpr (DT == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(V[i][c][j]), P[i], z, 0, 0, 0);
+      } else {
+        u32x4 a;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          a[i] = __builtin_amdgcn_perm(V[2 * i + 1][c][j / 2], V[2 * i][c][j / 2], j % 2 == 0 ? 0x05040100u : 0x07060302u);
+        z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, hi), z, 0, 0, 0);
+        z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, lo), z, 0, 0, 0);
+      }
+      return z;
+    };
+    // Values that no row sees become 0: a weight of 0 does not keep an infinity or NaN out of a product.
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < 4 * L::kSub; ++i) {
+        const int key = t0 + 16 * (i / 4) + 4 * g + i % 4;
+        const bool seen = here.there[i / 4] && key >= sp.k0 && key < sp.k1;
 #pragma unroll
         for (int c = 0; c < L::VC; ++c)
 #pragma unroll
-          for (int e = 0; e < L::kWords; ++e) {
-            const uint32_t w = V[i][c][e];
-            if constexpr (DT == 0) bad |= (w & 0x7f800000u) == 0x7f800000u;
-            else bad |= (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
+          for (int e = 0; e < L::kWords; ++e) V[i][c][e] = seen ? V[i][c][e] : 0u;
+      }
+    }
+    // Neither does a second piece of 0, or the weight of a row that does not see them, keep out those that
+    // are left: they are added one by one, and the products get 0 in their place.
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * L::kSub; ++i)
+#pragma unroll
+      for (int c = 0; c < L::VC; ++c)
+#pragma unroll
+        for (int e = 0; e < L::kWords; ++e) most = largest<DT>(most, V[i][c][e]);
+    if (__builtin_expect(__any(not_finite<DT>(most)), 0)) {
+      float* mine = weights[wave];  // [key][row]
+#pragma unroll
+      for (int i = 0; i < 4 * L::kSub; ++i) {
+        mine[(16 * (i / 4) + 4 * g + i % 4) * 16 + l16] = P[i];
+#pragma unroll
+        for (int c = 0; c < L::VC; ++c)
+#pragma unroll
+          for (int e = 0; e < L::kWords; ++e) V[i][c][e] = finite_only<DT>(V[i][c][e]);
+      }
+      wave_lds_sync();
+#pragma unroll 1
+      for (int k = 0; k < L::kKeys; ++k) {
+        const int key = t0 + k;
+        const bool seen = here.there[k / 16] && key <= pos && (A.window <= 0 || key > pos - A.window);
+        if (!seen) continue;
+        const float p = mine[k * 16 + l16];
+        const char* base = vb + here.at[k / 16] + k % 16 * ts;
+#pragma unroll
+        for (int c = 0; c < L::VC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // this lane's values of the row: 4 runs of VE
+            const T* v = reinterpret_cast<const T*>(base) + c * 16 * L::VE + (4 * g + e) * L::VE;
+#pragma unroll
+            for (int j = 0; j < L::VE; ++j) {
+              const float x = to_f32<DT>(v[j]);
+              if (!(fabsf(x) < __builtin_inff())) O[c * L::VE + j][e] += p * x;
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
       }
-      apart = __any(bad != 0);
     }
-    if (!apart) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) values(t, O[t], -1);
-    } else {
+    for (int c = 0; c < L::VC; ++c)
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-        for (int r = 0; r < 16; ++r) {
-          load_v();
-          const int row = row0 + 16 * t + r;
-          const int p = row < rows ? sp.first + row / share : -1;
-#pragma unroll
-          for (int i = 0; i < 4 * L::kSub; ++i)
-            if (!sees(p, i)) clear_v(i);
-          values(t, O[t], r);
-        }
-    }
+      for (int j = 0; j < L::VE; ++j) O[c * L::VE + j] = product(c, j, O[c * L::VE + j]);
+    here = next;
   }
 
-  // join the wavefronts: the largest maximum, sums and accumulators brought to it
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    l[t] = sum4(l[t]);
-    if (g == 0) {
-      stat[wave][16 * t + l16][0] = m[t];
-      stat[wave][16 * t + l16][1] = l[t];
-    }
+  f32x4(*red)[GT][kWave] = reinterpret_cast<f32x4(*)[GT][kWave]>(smem);
+  // join the wavefronts of the same rows: the largest maximum, sums and accumulators brought to it
+  l = sum4(l);
+  if (g == 0) {
+    stat[wave][l16][0] = m;
+    stat[wave][l16][1] = l;
   }
   __syncthreads();
-  const bool whole = sp.used <= 1;
-  const int orow = threadIdx.x & 15, om = threadIdx.x >> 4;  // the row and 16th of its values that this thread writes
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
+  float f = 0.f;
+  {
     float top = kNegInf;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stat[w][16 * t + l16][0]);
-    const float f = m[t] == kNegInf ? 0.f : exp2_(m[t] - top);
-    // the same for the row this thread writes
-    float wtop = kNegInf, sum = 0.f;
+    for (int k = 0; k < KW; ++k) top = fmaxf(top, stat[k * RW + wave % RW][l16][0]);
+    if (m != kNegInf) f = exp2_(m - top);
+  }
+  const bool whole = sp.used <= 1;
+  const int orow = threadIdx.x & 15, om = threadIdx.x >> 4;  // the row of each 16 and the 16th of its values that this thread writes
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) wtop = fmaxf(wtop, stat[w][16 * t + orow][0]);
+  for (int j0 = 0; j0 < L::kOut; j0 += GT) {
+    if (j0 > 0) __syncthreads();  // what was joined before has been read
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float mw = stat[w][16 * t + orow][0], lw = stat[w][16 * t + orow][1];
-      sum += mw == kNegInf ? lw : lw * exp2_(mw - wtop);  // lw: 0, or NaN
-    }
-    const int r = row0 + 16 * t + orow;
-    const int token = r / share, head = kh * share + r - token * share;
-    const int64_t line = (sp.lo + token) * C.heads + head;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (r < rows && om == 0) {
-      if (!whole) {
-        float* st = A.stat + (line * A.splits + split) * 2;
-        st[0] = wtop;
-        st[1] = sum;
-      } else if (A.lse != nullptr) {
-        A.lse[line] = sum == 0.f ? kNegInf : static_cast<float>((static_cast<double>(wtop) + log2(static_cast<double>(sum))) * 0.6931471805599453);
+    for (int j = 0; j < GT; ++j) red[wave][j][lane] = O[j0 + j] * f;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < RW; ++w) {
+      const int out = block0 + 16 * w + orow;
+      if (out >= rows) continue;
+      float top = kNegInf, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < KW; ++k) top = fmaxf(top, stat[k * RW + w][orow][0]);
+#pragma unroll
+      for (int k = 0; k < KW; ++k) {
+        const float mw = stat[k * RW + w][orow][0], lw = stat[k * RW + w][orow][1];
+        sum += mw == kNegInf ? lw : lw * exp2_(mw - top);  // lw: 0, or NaN
       }
-    }
-#pragma unroll
-    for (int j0 = 0; j0 < L::kOut; j0 += GT) {
-      __syncthreads();  // what was joined before has been read
-#pragma unroll
-      for (int j = 0; j < GT; ++j) red[wave][j][lane] = O[t][j0 + j] * f;
-      __syncthreads();
+      const int ot = out / share, head = kh * share + out - ot * share;
+      const int64_t line = (sp.lo + ot) * C.heads + head;
+      if (om == 0 && j0 == 0) {
+        if (!whole) {
+          float* st = A.stat + (line * A.splits + split) * 2;
+          st[0] = top;
+          st[1] = sum;
+        } else if (A.lse != nullptr) {
+          A.lse[line] = natural_log_sum(top, sum);
+        }
+      }
       constexpr int kRun = L::VE;  // neighbouring values of a thread
 #pragma unroll
       for (int c = 0; c < GT / kRun; ++c) {
         float y[kRun];
 #pragma unroll
         for (int j = 0; j < kRun; ++j) {
-          const int src = (om >> 2) * 16 + orow;
           y[j] = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) y[j] += reinterpret_cast<const float*>(&red[w][c * kRun + j][src])[om & 3];
+          for (int k = 0; k < KW; ++k)
+            y[j] += reinterpret_cast<const float*>(&red[k * RW + w][c * kRun + j][(om >> 2) * 16 + orow])[om & 3];
         }
         const int v = (j0 / kRun + c) * 16 * kRun + om * kRun;
-        if (r < rows) {
-          if (!whole) {
-            store_f32<0, kRun>(A.part + (line * A.splits + split) * D + v, y);
-          } else {
+        if (!whole) {
+          store_f32<0, kRun>(A.part + (line * A.splits + split) * D + v, y);
+        } else {
+          const float inv = 1.f / sum;
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) y[j] = sum == 0.f ? 0.f : y[j] * inv;
-            store_f32<DT, kRun>(static_cast<T*>(A.o) + (sp.lo + token) * A.o_stride + static_cast<int64_t>(head) * D + v, y);
-          }
+          for (int j = 0; j < kRun; ++j) y[j] = sum == 0.f ? 0.f : y[j] * inv;
+          store_f32<DT, kRun>(static_cast<T*>(A.o) + (sp.lo + ot) * A.o_stride + static_cast<int64_t>(head) * D + v, y);
         }
       }
     }
@@ -440,61 +544,57 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs A) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) out[e] = sum == 0.f ? 0.f : y[e] / sum;
   store_f32<DT, 4>(static_cast<T*>(A.o) + (sp.lo + token) * A.o_stride + static_cast<int64_t>(head) * D + 4 * v, out);
-  if (v == 0 && A.lse != nullptr)
-    A.lse[line] = sum == 0.f ? kNegInf : static_cast<float>((static_cast<double>(top) + log2(static_cast<double>(sum))) * 0.6931471805599453);
+  if (v == 0 && A.lse != nullptr) A.lse[line] = natural_log_sum(top, sum);
 }
 
 namespace {
 
-// 16-row tiles of a wavefront: as many as the rows need and the registers hold (accumulators and
-// queries grow with both the tiles and the head).
-int tiles_of(int32_t max_tokens, int32_t share, int dim) {
-  const int64_t rows = static_cast<int64_t>(max_tokens) * share;
-  const int most = 256 / dim;
-  int t = 1;
-  while (t < most && 16 * t < rows) t *= 2;
-  return t;
+// Wavefronts of a workgroup that take rows of their own.
+int row_waves(const AttendArgs& a) {
+  const int64_t rows = static_cast<int64_t>(a.max_tokens) * (a.c.heads / a.c.key_heads);
+  return rows <= 16 ? 1 : kWaves;
+}
+int64_t row_blocks(const AttendArgs& a) {
+  const int64_t rows = static_cast<int64_t>(a.max_tokens) * (a.c.heads / a.c.key_heads), of = 16 * row_waves(a);
+  return (rows + of - 1) / of;
 }
 
-template <int DT, int D, int MT>
+template <int DT, int D, int RW>
 hipError_t attend(const AttendArgs& a, hipStream_t s) {
-  const int64_t rows = static_cast<int64_t>(a.max_tokens) * (a.c.heads / a.c.key_heads);
-  const int64_t row_blocks = (rows + 16 * MT - 1) / (16 * MT);
-  const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * a.splits;
-  const int64_t blocks = (units + 7) / 8 * 8 * row_blocks;
-  k_attend<DT, D, MT><<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s>>>(a, static_cast<int>(row_blocks), units);
+  const int64_t blocks = row_blocks(a), units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * a.splits;
+  k_attend<DT, D, RW><<<dim3(static_cast<unsigned>((units + 7) / 8 * 8 * blocks)), dim3(kThreads), 0, s>>>(
+      a, static_cast<unsigned>(blocks), static_cast<unsigned>(units));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   k_attend_join<DT, D><<<dim3(static_cast<unsigned>(static_cast<int64_t>(a.c.batch) * a.max_tokens * a.c.heads)), dim3(kThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
+template <int DT, int D>
+hipError_t by_rows(const AttendArgs& a, hipStream_t s) {
+  return row_waves(a) == 1 ? attend<DT, D, 1>(a, s) : attend<DT, D, kWaves>(a, s);
+}
+
 template <int DT>
 hipError_t pick(const AttendArgs& a, hipStream_t s) {
-  const int t = tiles_of(a.max_tokens, a.c.heads / a.c.key_heads, a.c.dim);
-  if (a.c.dim == 64) return t == 1 ? attend<DT, 64, 1>(a, s) : t == 2 ? attend<DT, 64, 2>(a, s) : attend<DT, 64, 4>(a, s);
-  if (a.c.dim == 128) return t == 1 ? attend<DT, 128, 1>(a, s) : attend<DT, 128, 2>(a, s);
-  return attend<DT, 256, 1>(a, s);
+  return a.c.dim == 64 ? by_rows<DT, 64>(a, s) : a.c.dim == 128 ? by_rows<DT, 128>(a, s) : by_rows<DT, 256>(a, s);
 }
 
 }  // namespace
 
 void plan_attend(int32_t io_dtype, AttendArgs& a) {
-  constexpr int kStep = 128;  // keys of one turn of a workgroup
+  const int64_t kStep = (io_dtype == SEED_BF16 ? 32 : 16) * kWaves / row_waves(a);  // keys of one turn of a workgroup
   constexpr int64_t kGroups = 2048;
-  const int share = a.c.heads / a.c.key_heads;
-  const int64_t rows = static_cast<int64_t>(a.max_tokens) * share, mt = tiles_of(a.max_tokens, share, a.c.dim);
-  const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * ((rows + 16 * mt - 1) / (16 * mt));
+  const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * row_blocks(a);
   int64_t span = a.capacity;
   if (a.window > 0) {
     const int64_t near = static_cast<int64_t>(a.window) + a.max_tokens - 1 + 31;
     span = near < span ? near : span;
   }
   int64_t splits = (kGroups + units - 1) / units;
-  const int64_t most = (span + kStep - 1) / kStep;
+  const int64_t most = (span + 127) / 128;
   splits = splits < most ? splits : most;
-  const int64_t chunk = ((span + splits - 1) / splits + kStep - 1) / kStep * kStep;
-  a.chunk = static_cast<int32_t>(chunk < (int64_t{1} << 31) - kStep ? chunk : (int64_t{1} << 31) - kStep);
+  a.chunk = static_cast<int32_t>(((span + splits - 1) / splits + kStep - 1) / kStep * kStep);
   a.splits = static_cast<int32_t>((span + a.chunk - 1) / a.chunk);
 }
 

@@ -49,7 +49,8 @@ struct AppendArgs {
 struct AttendArgs {
   CacheArgs c;
   int32_t max_tokens, capacity, window;
-  float scale2;             // scale log2(e)
+  float scale2;             // |scale| log2(e)
+  uint32_t negate;          // the sign bits of a word of q, where scale is negative
   int32_t chunk, splits;    // keys of a workgroup, and workgroups along the longest cache
   int64_t q_stride, o_stride;
   const void* q;

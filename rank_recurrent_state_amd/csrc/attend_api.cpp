@@ -13,6 +13,7 @@ namespace {
 using namespace seed;
 
 constexpr int64_t kMostBlocks = (int64_t{1} << 24) - 1;  // of 256 threads: a launch has fewer than 2^32
+constexpr int64_t kMostTokenStride = int64_t{1} << 24;   // 16 positions' bytes are 32-bit offsets
 constexpr int64_t kMostPositions = int64_t{1} << 30;     // positions and their tiles' ends are int32
 
 int check_rotary(const seed_rotary* r, int32_t dim) {
@@ -35,6 +36,7 @@ int check_cache(const seed_cache* c) {
     if (st <= 0 || st > kMostStride || st % align != 0) return SEED_ERR_ARG;
   // the spans below stay inside 64 bits
   if (c->key_heads > kMostBytes / 4 / c->head_stride || c->page > kMostBytes / 4 / c->token_stride) return SEED_ERR_UNSUPPORTED;
+  if (c->token_stride > kMostTokenStride) return SEED_ERR_UNSUPPORTED;
   // [page][key_heads][dim] or [key_heads][page][dim], nothing overlapping; the stride of a single head or page is not looked at
   const int64_t d = c->dim, heads = c->key_heads, page = c->page;
   const bool by_token = (heads == 1 || c->head_stride >= d) && c->token_stride >= (heads - 1) * c->head_stride + d &&
@@ -123,13 +125,14 @@ int check_attend(const seed_cache* c, const seed_tokens* t, const seed_attend* w
   if (!w || w->max_tokens < 1 || w->max_length < 1 || w->window < 0 || !isfinite(w->scale)) return SEED_ERR_ARG;
   if (static_cast<int64_t>(w->max_length) > static_cast<int64_t>(c->page) * c->width) return SEED_ERR_ARG;
   if (w->max_tokens > 32) return SEED_ERR_UNSUPPORTED;
-  const double scale2 = static_cast<double>(w->scale) * 1.4426950408889634;
-  if (!isfinite(static_cast<float>(scale2))) return SEED_ERR_ARG;
+  const double scale2 = fabs(static_cast<double>(w->scale)) * 1.4426950408889634;
+  if (!isfinite(static_cast<float>(scale2)) || static_cast<float>(scale2) == 0.f) return SEED_ERR_ARG;
   a.c = cache_args(c, t);
   a.max_tokens = w->max_tokens;
   a.capacity = w->max_length;
   a.window = w->window >= w->max_length ? 0 : w->window;  // a window that holds every position
   a.scale2 = static_cast<float>(scale2);
+  a.negate = w->scale < 0.f ? (c->io_dtype == SEED_F32 ? 0x80000000u : 0x80008000u) : 0u;
   // a row block of 16 at least: the launch has to hold a workgroup for each, and one per row to join them
   const int64_t rows = static_cast<int64_t>(w->max_tokens) * t->heads;
   if (rows > kMostBlocks / c->batch || (static_cast<int64_t>(c->batch) * c->key_heads + 8) * (rows / c->key_heads / 16 + 1) > kMostBlocks)

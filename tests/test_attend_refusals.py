@@ -179,7 +179,7 @@ def test_attend():
                 dict(qs=516), dict(os=516)):
         assert _attend(r, tokens=_tokens(r, **bad)) == arg, bad
     for bad in (dict(most=0), dict(most=-1), dict(length=0), dict(length=129), dict(window=-1), dict(scale=INF), dict(scale=NAN),
-                dict(scale=3e38), dict(q=None), dict(o=None), dict(q=BASE + 8), dict(o=FAR + 2), dict(lse=FAR + (1 << 20) + 2),
+                dict(scale=3e38), dict(scale=0.0), dict(q=None), dict(o=None), dict(q=BASE + 8), dict(o=FAR + 2), dict(lse=FAR + (1 << 20) + 2),
                 # overlaps
                 dict(o=BASE), dict(o=BASE + 1024), dict(lse=FAR + 64), dict(o=16 * FAR), dict(lse=32 * FAR + 64), dict(o=8 * FAR),
                 dict(o=2 * FAR), dict(lse=3 * FAR), dict(lse=BASE + 8)):
