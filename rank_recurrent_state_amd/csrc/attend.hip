@@ -14,6 +14,8 @@
 // piece the weights' rounding, 2^-9 each, is as large as o's. The products are far from the matrix unit's rate.
 // m is only moved when a score passes it by 8 (weights up to 2^8): most tiles then need no exchange between
 // lanes and no rescaling, and every weight keeps its relative precision.
+#include <algorithm>
+
 #include "attend.hpp"
 #include "common.hpp"
 
@@ -21,7 +23,8 @@ namespace seed {
 
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / kWave;
+constexpr int kWaves = 4;  // of a workgroup; short caches take kMany
+constexpr int kMany = 8;
 constexpr float kNegInf = -__builtin_inff();
 
 using f32x4 = __attribute__((ext_vector_type(4))) float;
@@ -86,8 +89,12 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
 
 // log of sum 2^max.
 __device__ __forceinline__ float natural_log_sum(float max, float sum) {
-  return sum == 0.f ? kNegInf : static_cast<float>((static_cast<double>(max) + log2(static_cast<double>(sum))) * 0.6931471805599453);
+  constexpr float kLn2 = 0.693147181f;
+  return sum == 0.f ? kNegInf : fmaf(max, kLn2, __builtin_amdgcn_logf(sum) * kLn2);
 }
+
+// The token of row r: r / share, exact for the shares that the host admits (up to 2^14, r below 32 share).
+__device__ __forceinline__ int token_of(const AttendArgs& A, int r) { return static_cast<int>((static_cast<float>(r) + 0.5f) * A.per_share); }
 
 // The positions that the rows of a request see between them: keys [k0, k1), row i at first + i.
 struct Span {
@@ -135,27 +142,31 @@ struct Tile {
 
 }  // namespace
 
-// RW wavefronts take 16 rows each of the same keys, kWaves / RW of them other keys.
-template <int DT, int D, int RW>
-__global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attend(const AttendArgs A, unsigned row_blocks, unsigned units) {
+// NW wavefronts: RW = 1: of the same 16 rows and keys of their own each; RW = NW: of 16 rows each and the same keys.
+template <int DT, int D, int RW, int NW>
+__global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_attend(const AttendArgs A, unsigned row_blocks, unsigned units) {
   using L = Tile<DT, D>;
   using T = stor_t<DT>;
-  constexpr int KW = kWaves / RW;
+  static_assert(RW == 1 || RW == NW, "rows or keys of their own");
+  constexpr int KW = NW / RW;
   constexpr int GT = L::kOut < 8 ? L::kOut : 8;  // accumulators joined at a time
   // A wavefront's keys (RW = 1), or all wavefronts' keys and values, twice; at the end the accumulators.
-  constexpr int kJoin = kWaves * GT * kWave * 16, kTiles = RW == 1 ? kWaves * L::kTile : 4 * L::kTile;
+  constexpr int kJoin = NW * GT * kWave * 16, kTiles = RW == 1 ? NW * L::kTile : 4 * L::kTile;
   __shared__ __attribute__((aligned(16))) char smem[kJoin > kTiles ? kJoin : kTiles];
-  __shared__ float weights[kWaves][L::kKeys * 16];
-  __shared__ float stat[kWaves][16][2];
+  __shared__ float weights[NW][L::kKeys * 16];
+  __shared__ float stat[NW][16][2];
 
-  // Workgroups go to the 8 XCDs in turn. The row blocks of a unit read the same keys: they follow one
-  // another on one XCD. Otherwise neighbouring heads, whose keys lie side by side, run on different ones (5 % faster
-  // than on the same).
   const CacheArgs& C = A.c;
-  const unsigned group = blockIdx.x / (8 * row_blocks), within = blockIdx.x % (8 * row_blocks);
-  const int rb = static_cast<int>(within / 8);
-  const unsigned unit = group * 8 + within % 8;
-  if (unit >= units) return;
+  unsigned unit = blockIdx.x;
+  int rb = 0;
+  if constexpr (RW > 1) {
+    // Workgroups go to the 8 XCDs in turn: the row blocks of a unit, which read the same keys, follow one another
+    // on one XCD. Neighbouring heads, whose keys lie side by side, run on different ones (5 % faster than on the same).
+    const unsigned group = blockIdx.x / (8 * row_blocks), within = blockIdx.x % (8 * row_blocks);
+    rb = static_cast<int>(within / 8);
+    unit = group * 8 + within % 8;
+    if (unit >= units) return;
+  }
   const int kh = static_cast<int>(unit % C.key_heads);
   const unsigned rest = unit / C.key_heads;
   const int b = static_cast<int>(rest % C.batch), split = static_cast<int>(rest / C.batch);
@@ -163,24 +174,24 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attend(const Att
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const Span sp = span_of(A, b);
-  const int share = C.heads / C.key_heads;
+  const int share = A.share;
   const int rows = sp.n * share, block0 = rb * RW * 16;
   if (block0 >= rows || split >= max(sp.used, 1)) return;
 
   // this lane's row of the wavefront's 16: a query of key head kh
-  const int row0 = block0 + 16 * (wave % RW);
-  const int r = row0 + l16, token = r / share;
+  const int row0 = block0 + (RW > 1 ? 16 * wave : 0);
+  const int r = row0 + l16, token = token_of(A, r);
   const int pos = r < rows ? sp.first + token : -1;
   u32x4 Q[L::kQ];
-  {
+#pragma unroll
+  for (int c = 0; c < L::kQ; ++c) Q[c] = u32x4{0, 0, 0, 0};
+  if (r < rows) {
     const T* q = static_cast<const T*>(A.q) + (sp.lo + token) * A.q_stride + static_cast<int64_t>(kh * share + r - token * share) * D;
 #pragma unroll
-    for (int c = 0; c < L::kQ; ++c) {
-      Q[c] = u32x4{0, 0, 0, 0};
-      if (r < rows) Q[c] = *reinterpret_cast<const u32x4*>(q + c * 4 * L::kVec + g * L::kVec);
-      Q[c] ^= A.negate;
-    }
+    for (int c = 0; c < L::kQ; ++c) Q[c] = *reinterpret_cast<const u32x4*>(q + c * 4 * L::kVec + g * L::kVec);
   }
+#pragma unroll
+  for (int c = 0; c < L::kQ; ++c) Q[c] ^= A.negate;
 
   f32x4 O[L::kOut];
   float m = kNegInf, l = 0.f;
@@ -401,11 +412,13 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attend(const Att
       wave_lds_sync();
 #pragma unroll 1
       for (int k = 0; k < L::kKeys; ++k) {
-        const int key = t0 + k;
-        const bool seen = here.there[k / 16] && key <= pos && (A.window <= 0 || key > pos - A.window);
+        const int key = t0 + k, last = L::kSub - 1;  // no run-time index into here: it would leave the registers
+        const bool page = k < 16 ? here.there[0] : here.there[last];
+        const int64_t at = k < 16 ? here.at[0] : here.at[last];
+        const bool seen = page && key <= pos && (A.window <= 0 || key > pos - A.window);
         if (!seen) continue;
         const float p = mine[k * 16 + l16];
-        const char* base = vb + here.at[k / 16] + k % 16 * ts;
+        const char* base = vb + at + k % 16 * ts;
 #pragma unroll
         for (int c = 0; c < L::VC; ++c)
 #pragma unroll
@@ -427,44 +440,40 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attend(const Att
     here = next;
   }
 
+  constexpr bool kOwn = RW == 1 && L::kTile == GT * kWave * 16;  // a wavefront's accumulators take the place of its own tile
+  // Join the wavefronts of the same rows: sums and accumulators brought to the largest maximum. The tiles' place
+  // takes the accumulators, a few at a time.
   f32x4(*red)[GT][kWave] = reinterpret_cast<f32x4(*)[GT][kWave]>(smem);
-  // join the wavefronts of the same rows: the largest maximum, sums and accumulators brought to it
   l = sum4(l);
   if (g == 0) {
     stat[wave][l16][0] = m;
     stat[wave][l16][1] = l;
   }
-  __syncthreads();
-  float f = 0.f;
-  {
-    float top = kNegInf;
-#pragma unroll
-    for (int k = 0; k < KW; ++k) top = fmaxf(top, stat[k * RW + wave % RW][l16][0]);
-    if (m != kNegInf) f = exp2_(m - top);
-  }
   const bool whole = sp.used <= 1;
-  const int orow = threadIdx.x & 15, om = threadIdx.x >> 4;  // the row of each 16 and the 16th of its values that this thread writes
+  const int tid = threadIdx.x & 255, orow = tid & 15, om = tid >> 4;  // the row of each 16 and the 16th of its values that this thread writes
+  const int half = threadIdx.x >> 8;                                  // NW = 8: which of the accumulators
 #pragma unroll
   for (int j0 = 0; j0 < L::kOut; j0 += GT) {
-    if (j0 > 0) __syncthreads();  // what was joined before has been read
+    if (!kOwn || j0 > 0) __syncthreads();  // the last tile, or what was joined before, has been read
 #pragma unroll
-    for (int j = 0; j < GT; ++j) red[wave][j][lane] = O[j0 + j] * f;
+    for (int j = 0; j < GT; ++j) red[wave][j][lane] = O[j0 + j];
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < RW; ++w) {
       const int out = block0 + 16 * w + orow;
       if (out >= rows) continue;
-      float top = kNegInf, sum = 0.f;
+      float top = kNegInf, sum = 0.f, f[KW];
 #pragma unroll
-      for (int k = 0; k < KW; ++k) top = fmaxf(top, stat[k * RW + w][orow][0]);
+      for (int k = 0; k < KW; ++k) top = fmaxf(top, stat[RW > 1 ? w : k][orow][0]);
 #pragma unroll
       for (int k = 0; k < KW; ++k) {
-        const float mw = stat[k * RW + w][orow][0], lw = stat[k * RW + w][orow][1];
-        sum += mw == kNegInf ? lw : lw * exp2_(mw - top);  // lw: 0, or NaN
+        const float mw = stat[RW > 1 ? w : k][orow][0];
+        f[k] = mw == kNegInf ? 1.f : exp2_(mw - top);  // without a weight: zeros, or NaN
+        sum += stat[RW > 1 ? w : k][orow][1] * f[k];
       }
-      const int ot = out / share, head = kh * share + out - ot * share;
+      const int ot = token_of(A, out), head = kh * share + out - ot * share;
       const int64_t line = (sp.lo + ot) * C.heads + head;
-      if (om == 0 && j0 == 0) {
+      if (om == 0 && half == 0 && j0 == 0) {
         if (!whole) {
           float* st = A.stat + (line * A.splits + split) * 2;
           st[0] = top;
@@ -473,16 +482,18 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attend(const Att
           A.lse[line] = natural_log_sum(top, sum);
         }
       }
-      constexpr int kRun = L::VE;  // neighbouring values of a thread
+      constexpr int kRun = L::VE, kRuns = GT / kRun;  // neighbouring values of a thread
 #pragma unroll
-      for (int c = 0; c < GT / kRun; ++c) {
+      for (int c = 0; c < kRuns; ++c) {
+        if (NW > kWaves && c % 2 != half && kRuns > 1) continue;
+        if (NW > kWaves && kRuns == 1 && half != 0) continue;
         float y[kRun];
 #pragma unroll
         for (int j = 0; j < kRun; ++j) {
           y[j] = 0.f;
 #pragma unroll
           for (int k = 0; k < KW; ++k)
-            y[j] += reinterpret_cast<const float*>(&red[k * RW + w][c * kRun + j][(om >> 2) * 16 + orow])[om & 3];
+            y[j] = fmaf(reinterpret_cast<const float*>(&red[RW > 1 ? w : k][c * kRun + j][(om >> 2) * 16 + orow])[om & 3], f[k], y[j]);
         }
         const int v = (j0 / kRun + c) * 16 * kRun + om * kRun;
         if (!whole) {
@@ -498,53 +509,78 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 3 : 2) void k_attend(const Att
   }
 }
 
-// Joins the workgroups along a cache: a workgroup per row and head, D / 4 threads per part.
-template <int DT, int D>
-__global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs A) {
+// Joins the workgroups along a cache: WR wavefronts per row and head, a lane D / 64 of its values.
+template <int DT, int D, int WR>
+__global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_attend_join(const AttendArgs A) {
   using T = stor_t<DT>;
-  constexpr int kLine = D / 4, kPer = kThreads / kLine;
-  __shared__ f32x4 acc[kPer][kLine];
-  __shared__ float sums[kPer];
-  const int head = static_cast<int>(blockIdx.x % A.c.heads);
-  const int64_t rest = blockIdx.x / A.c.heads;
+  constexpr int N = D / kWave, kRows = WR == 1 ? kWaves : 1;
+  using vec = __attribute__((ext_vector_type(N))) float;
+  __shared__ float acc[WR][D];
+  __shared__ float stats[WR][2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned item = blockIdx.x * kRows + (WR == 1 ? wave : 0);
+  const int head = static_cast<int>(item % A.c.heads);
+  const unsigned rest = item / A.c.heads;
   const int token = static_cast<int>(rest % A.max_tokens), b = static_cast<int>(rest / A.max_tokens);
+  if (b >= A.c.batch) return;
   const Span sp = span_of(A, b);
   if (token >= sp.n || sp.used <= 1) return;
   const int64_t line = (sp.lo + token) * A.c.heads + head;
-  const float* stat = A.stat + line * A.splits * 2;
-  const float* part = A.part + line * A.splits * D;
-  const int lane = threadIdx.x & 63;
-  float top = kNegInf;
-  for (int s = lane; s < sp.used; s += kWave) top = fmaxf(top, stat[2 * s]);
+  const float* __restrict__ stat = A.stat + line * A.splits * 2;
+  const float* __restrict__ part = A.part + line * A.splits * D + lane * N;
+  float top = kNegInf, sum = 0.f, y[N] = {};
+  // up to 64 parts at a time, a lane's maximum and sum each; several wavefronts take a run of parts each
+  const int per = WR == 1 ? sp.used : (sp.used + WR - 1) / WR, s1 = WR == 1 ? sp.used : min((wave + 1) * per, sp.used);
+  for (int s0 = WR == 1 ? 0 : wave * per; s0 < s1; s0 += kWave) {
+    const int s = s0 + lane;
+    const float ms = s < s1 ? stat[2 * s] : kNegInf, ls = s < s1 ? stat[2 * s + 1] : 0.f;
+    float now = ms;
 #pragma unroll
-  for (int d = 1; d < kWave; d *= 2) top = fmaxf(top, __shfl_xor(top, d, kWave));
-  const int p = threadIdx.x / kLine, v = threadIdx.x % kLine;
-  f32x4 y = {0.f, 0.f, 0.f, 0.f};
-  float sum = 0.f;
+    for (int d = 1; d < 16; d *= 2) now = fmaxf(now, __shfl_xor(now, d, kWave));
+    now = fmaxf(top, max4(now));
+    const float old = now == kNegInf ? 1.f : exp2_(top - now);
+    top = now;
+    const float f = ms == kNegInf ? 1.f : exp2_(ms - now);  // a part without a weight holds zeros, or NaN
+    sum = sum * old + wave_sum(ls * f);
+#pragma unroll
+    for (int e = 0; e < N; ++e) y[e] *= old;
+    const int n = min(s1 - s0, kWave);
 #pragma unroll 4
-  for (int s = p; s < sp.used; s += kPer) {
-    const float mw = stat[2 * s], lw = stat[2 * s + 1];
-    const f32x4 x = *reinterpret_cast<const f32x4*>(part + static_cast<int64_t>(s) * D + 4 * v);
-    const float f = mw == kNegInf ? 1.f : exp2_(mw - top);  // a part of no weight holds zeros, or NaN
-    y += x * f;
-    sum += lw * f;
-  }
-  acc[p][v] = y;
-  if (v == 0) sums[p] = sum;
-  __syncthreads();
-  if (p != 0) return;
-  sum = 0.f;
-  y = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < n; ++i) {
+      const vec x = *reinterpret_cast<const vec*>(part + static_cast<int64_t>(s0 + i) * D);
+      const float fi = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), i));
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    y += acc[i][v];
-    sum += sums[i];
+      for (int e = 0; e < N; ++e) y[e] = fmaf(x[e], fi, y[e]);
+    }
   }
-  float out[4];
+  if constexpr (WR > 1) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) out[e] = sum == 0.f ? 0.f : y[e] / sum;
-  store_f32<DT, 4>(static_cast<T*>(A.o) + (sp.lo + token) * A.o_stride + static_cast<int64_t>(head) * D + 4 * v, out);
-  if (v == 0 && A.lse != nullptr) A.lse[line] = natural_log_sum(top, sum);
+    for (int e = 0; e < N; ++e) acc[wave][lane * N + e] = y[e];
+    if (lane == 0) {
+      stats[wave][0] = top;
+      stats[wave][1] = sum;
+    }
+    __syncthreads();
+    if (wave != 0) return;
+    float most = kNegInf;
+#pragma unroll
+    for (int w = 0; w < WR; ++w) most = fmaxf(most, stats[w][0]);
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) y[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WR; ++w) {
+      const float f = stats[w][0] == kNegInf ? 1.f : exp2_(stats[w][0] - most);
+      sum += stats[w][1] * f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) y[e] = fmaf(acc[w][lane * N + e], f, y[e]);
+    }
+    top = most;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) y[e] = sum == 0.f ? 0.f : y[e] / sum;
+  store_f32<DT, N>(static_cast<T*>(A.o) + (sp.lo + token) * A.o_stride + static_cast<int64_t>(head) * D + lane * N, y);
+  if (lane == 0 && A.lse != nullptr) A.lse[line] = natural_log_sum(top, sum);
 }
 
 namespace {
@@ -555,24 +591,28 @@ int row_waves(const AttendArgs& a) {
   return rows <= 16 ? 1 : kWaves;
 }
 int64_t row_blocks(const AttendArgs& a) {
-  const int64_t rows = static_cast<int64_t>(a.max_tokens) * (a.c.heads / a.c.key_heads), of = 16 * row_waves(a);
+  const int64_t rows = static_cast<int64_t>(a.max_tokens) * a.share, of = 16 * row_waves(a);
   return (rows + of - 1) / of;
 }
 
-template <int DT, int D, int RW>
+template <int DT, int D, int RW, int NW>
 hipError_t attend(const AttendArgs& a, hipStream_t s) {
   const int64_t blocks = row_blocks(a), units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * a.splits;
-  k_attend<DT, D, RW><<<dim3(static_cast<unsigned>((units + 7) / 8 * 8 * blocks)), dim3(kThreads), 0, s>>>(
-      a, static_cast<unsigned>(blocks), static_cast<unsigned>(units));
+  const int64_t grid = RW == 1 ? units : (units + 7) / 8 * 8 * blocks;
+  k_attend<DT, D, RW, NW><<<dim3(static_cast<unsigned>(grid)), dim3(NW * kWave), 0, s>>>(a, static_cast<unsigned>(blocks),
+                                                                                       static_cast<unsigned>(units));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  k_attend_join<DT, D><<<dim3(static_cast<unsigned>(static_cast<int64_t>(a.c.batch) * a.max_tokens * a.c.heads)), dim3(kThreads), 0, s>>>(a);
+  const int64_t items = static_cast<int64_t>(a.c.batch) * a.max_tokens * a.c.heads;
+  if (a.splits <= 4) k_attend_join<DT, D, 1><<<dim3(static_cast<unsigned>((items + kWaves - 1) / kWaves)), dim3(kWaves * kWave), 0, s>>>(a);
+  else k_attend_join<DT, D, 8><<<dim3(static_cast<unsigned>(items)), dim3(8 * kWave), 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <int DT, int D>
 hipError_t by_rows(const AttendArgs& a, hipStream_t s) {
-  return row_waves(a) == 1 ? attend<DT, D, 1>(a, s) : attend<DT, D, kWaves>(a, s);
+  if (row_waves(a) > 1) return attend<DT, D, kWaves, kWaves>(a, s);
+  return a.many ? attend<DT, D, 1, kMany>(a, s) : attend<DT, D, 1, kWaves>(a, s);
 }
 
 template <int DT>
@@ -583,18 +623,25 @@ hipError_t pick(const AttendArgs& a, hipStream_t s) {
 }  // namespace
 
 void plan_attend(int32_t io_dtype, AttendArgs& a) {
-  const int64_t kStep = (io_dtype == SEED_BF16 ? 32 : 16) * kWaves / row_waves(a);  // keys of one turn of a workgroup
-  constexpr int64_t kGroups = 2048;
+  const int tile = io_dtype == SEED_BF16 ? 32 : 16;
+  const int64_t step = tile * (row_waves(a) > 1 ? 1 : kWaves);  // keys of one turn of a workgroup
   const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * row_blocks(a);
   int64_t span = a.capacity;
   if (a.window > 0) {
     const int64_t near = static_cast<int64_t>(a.window) + a.max_tokens - 1 + 31;
     span = near < span ? near : span;
   }
-  int64_t splits = (kGroups + units - 1) / units;
-  const int64_t most = (span + 127) / 128;
-  splits = splits < most ? splits : most;
-  a.chunk = static_cast<int32_t>(((span + splits - 1) / splits + kStep - 1) / kStep * kStep);
+  const int64_t fill = a.c.dim == 256 ? 512 : 256;  // workgroups that fill the chip when they are equal
+  int64_t splits = (fill + units - 1) / units;
+  if (a.c.batch > 1) {
+    const int64_t more = std::min((2048 + units - 1) / units, span / 1024);
+    splits = std::max(splits, more);
+  }
+  splits = std::max(std::min(splits, (span + 127) / 128), int64_t{1});
+  const int64_t few = (io_dtype == SEED_BF16 ? 1024 : 512) / (a.c.dim == 256 ? 4 : 1);
+  a.many = splits > 1 && span <= few && row_waves(a) == 1;
+  if (a.many) splits = 1;
+  a.chunk = static_cast<int32_t>(((span + splits - 1) / splits + step - 1) / step * step);
   a.splits = static_cast<int32_t>((span + a.chunk - 1) / a.chunk);
 }
 

@@ -49,9 +49,12 @@ struct AppendArgs {
 struct AttendArgs {
   CacheArgs c;
   int32_t max_tokens, capacity, window;
+  int32_t share;            // heads / key_heads
+  float per_share;          // 1 / share
   float scale2;             // |scale| log2(e)
   uint32_t negate;          // the sign bits of a word of q, where scale is negative
   int32_t chunk, splits;    // keys of a workgroup, and workgroups along the longest cache
+  bool many;                // more wavefronts in the place of more workgroups
   int64_t q_stride, o_stride;
   const void* q;
   void* o;
@@ -77,7 +80,7 @@ struct VerifyArgs {
 
 hipError_t launch_rotate_rows(int32_t io_dtype, const RotateArgs& a, hipStream_t s);
 hipError_t launch_cache_append(int32_t io_dtype, const AppendArgs& a, hipStream_t s);
-// Sets chunk and splits from the sizes.
+// Sets chunk, splits and many from the sizes.
 void plan_attend(int32_t io_dtype, AttendArgs& a);
 hipError_t launch_attend(int32_t io_dtype, const AttendArgs& a, hipStream_t s);
 int32_t verify_segments(int32_t vocab);

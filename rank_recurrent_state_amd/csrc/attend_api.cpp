@@ -14,6 +14,7 @@ using namespace seed;
 
 constexpr int64_t kMostBlocks = (int64_t{1} << 24) - 1;  // of 256 threads: a launch has fewer than 2^32
 constexpr int64_t kMostTokenStride = int64_t{1} << 24;   // 16 positions' bytes are 32-bit offsets
+constexpr int32_t kMostShare = 1 << 14;                  // a row's token is found in fp32
 constexpr int64_t kMostPositions = int64_t{1} << 30;     // positions and their tiles' ends are int32
 
 int check_rotary(const seed_rotary* r, int32_t dim) {
@@ -128,15 +129,16 @@ int check_attend(const seed_cache* c, const seed_tokens* t, const seed_attend* w
   const double scale2 = fabs(static_cast<double>(w->scale)) * 1.4426950408889634;
   if (!isfinite(static_cast<float>(scale2)) || static_cast<float>(scale2) == 0.f) return SEED_ERR_ARG;
   a.c = cache_args(c, t);
+  a.share = t->heads / c->key_heads;
+  a.per_share = 1.f / static_cast<float>(a.share);
   a.max_tokens = w->max_tokens;
   a.capacity = w->max_length;
   a.window = w->window >= w->max_length ? 0 : w->window;  // a window that holds every position
   a.scale2 = static_cast<float>(scale2);
   a.negate = w->scale < 0.f ? (c->io_dtype == SEED_F32 ? 0x80000000u : 0x80008000u) : 0u;
-  // a row block of 16 at least: the launch has to hold a workgroup for each, and one per row to join them
+  // the launch has to hold a workgroup for every 16 rows, and one per row to join them
   const int64_t rows = static_cast<int64_t>(w->max_tokens) * t->heads;
-  if (rows > kMostBlocks / c->batch || (static_cast<int64_t>(c->batch) * c->key_heads + 8) * (rows / c->key_heads / 16 + 1) > kMostBlocks)
-    return SEED_ERR_UNSUPPORTED;
+  if (a.share > kMostShare || rows > kMostBlocks / c->batch) return SEED_ERR_UNSUPPORTED;
   plan_attend(c->io_dtype, a);
   return SEED_OK;
 }
