@@ -25,6 +25,12 @@ namespace {
 
 constexpr int kWaves = 4;  // of a workgroup; short caches take kMany
 constexpr int kMany = 8;
+constexpr int64_t kGroups = 512;  // workgroups of a call that share its keys
+
+// Turns of a workgroup: equal shares of them all.
+__device__ __forceinline__ int share_of(int turns, int groups) {
+  return max((turns + groups - 1) / groups, 1);
+}
 constexpr float kNegInf = -__builtin_inff();
 
 using f32x4 = __attribute__((ext_vector_type(4))) float;
@@ -99,7 +105,9 @@ __device__ __forceinline__ int token_of(const AttendArgs& A, int r) { return sta
 // The positions that the rows of a request see between them: keys [k0, k1), row i at first + i.
 struct Span {
   int64_t lo;
-  int n, first, k0, k1, base, used;  // base: k0 at a tile's start; used: workgroups that have keys
+  int n, first, k0, k1, base;  // base: k0 at a tile's start
+  // turns of `step` keys; a request with rows has one, if only to write their zeros
+  __device__ __forceinline__ int turns(int step) const { return n == 0 ? 0 : k1 > k0 ? (k1 - base + step - 1) / step : 1; }
 };
 __device__ __forceinline__ Span span_of(const AttendArgs& A, int b) {
   Span s;
@@ -114,8 +122,18 @@ __device__ __forceinline__ Span span_of(const AttendArgs& A, int b) {
   s.k1 = static_cast<int>(k1);
   s.k0 = static_cast<int>(min(k0, k1));
   s.base = s.k0 & ~31;
-  s.used = s.k1 > s.k0 ? static_cast<int>((static_cast<int64_t>(s.k1) - s.base + A.chunk - 1) / A.chunk) : 0;
   return s;
+}
+
+// Sum of the lanes up to each, and of all.
+__device__ __forceinline__ int scan(int v, int lane, int& total) {
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) {
+    const int up = __shfl_up(v, d, kWave);
+    if (lane >= d) v += up;
+  }
+  total = __builtin_amdgcn_readlane(v, kWave - 1);
+  return v;
 }
 
 template <int DT, int D>
@@ -142,41 +160,33 @@ struct Tile {
 
 }  // namespace
 
-// NW wavefronts: RW = 1: of the same 16 rows and keys of their own each; RW = NW: of 16 rows each and the same keys.
+// A workgroup's shared memory.
 template <int DT, int D, int RW, int NW>
-__global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_attend(const AttendArgs A, unsigned row_blocks, unsigned units) {
+struct Shared {
+  using L = Tile<DT, D>;
+  static constexpr int GT = L::kOut < 8 ? L::kOut : 8;  // accumulators joined at a time
+  // A wavefront's keys (RW = 1), or all wavefronts' keys and values, twice; at the end the accumulators.
+  static constexpr int kJoin = NW * GT * kWave * 16, kTiles = RW == 1 ? NW * L::kTile : 4 * L::kTile;
+  __attribute__((aligned(16))) char tiles[kJoin > kTiles ? kJoin : kTiles];
+  float weights[NW][L::kKeys * 16];
+  float stat[NW][16][2];
+};
+
+// Rows [16 RW rb, ..) of request b and key head kh over the keys [from, to): written to o, or as maximum, sum and
+// accumulators of each row to stat and part (nullptr: o). NW wavefronts: RW = 1: of the same 16 rows and keys of
+// their own each; RW = NW: of 16 rows each and the same keys.
+template <int DT, int D, int RW, int NW>
+__device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, RW, NW>& sm, const Span& sp, int b, int kh, int rb, int from,
+                                            int to, float* part, float* part_stat) {
   using L = Tile<DT, D>;
   using T = stor_t<DT>;
   static_assert(RW == 1 || RW == NW, "rows or keys of their own");
-  constexpr int KW = NW / RW;
-  constexpr int GT = L::kOut < 8 ? L::kOut : 8;  // accumulators joined at a time
-  // A wavefront's keys (RW = 1), or all wavefronts' keys and values, twice; at the end the accumulators.
-  constexpr int kJoin = NW * GT * kWave * 16, kTiles = RW == 1 ? NW * L::kTile : 4 * L::kTile;
-  __shared__ __attribute__((aligned(16))) char smem[kJoin > kTiles ? kJoin : kTiles];
-  __shared__ float weights[NW][L::kKeys * 16];
-  __shared__ float stat[NW][16][2];
-
+  constexpr int KW = NW / RW, GT = Shared<DT, D, RW, NW>::GT;
   const CacheArgs& C = A.c;
-  unsigned unit = blockIdx.x;
-  int rb = 0;
-  if constexpr (RW > 1) {
-    // Workgroups go to the 8 XCDs in turn: the row blocks of a unit, which read the same keys, follow one another
-    // on one XCD. Neighbouring heads, whose keys lie side by side, run on different ones (5 % faster than on the same).
-    const unsigned group = blockIdx.x / (8 * row_blocks), within = blockIdx.x % (8 * row_blocks);
-    rb = static_cast<int>(within / 8);
-    unit = group * 8 + within % 8;
-    if (unit >= units) return;
-  }
-  const int kh = static_cast<int>(unit % C.key_heads);
-  const unsigned rest = unit / C.key_heads;
-  const int b = static_cast<int>(rest % C.batch), split = static_cast<int>(rest / C.batch);
-
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const Span sp = span_of(A, b);
   const int share = A.share;
   const int rows = sp.n * share, block0 = rb * RW * 16;
-  if (block0 >= rows || split >= max(sp.used, 1)) return;
 
   // this lane's row of the wavefront's 16: a query of key head kh
   const int row0 = block0 + (RW > 1 ? 16 * wave : 0);
@@ -198,14 +208,12 @@ __global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_a
 #pragma unroll
   for (int j = 0; j < L::kOut; ++j) O[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int from = sp.base + split * A.chunk;
-  const int to = static_cast<int>(min(static_cast<int64_t>(from) + A.chunk, static_cast<int64_t>(sp.k1)));
   const int last_pos = sp.first + sp.n - 1;
   const scalar_int* table = reinterpret_cast<const scalar_int*>(reinterpret_cast<uintptr_t>(C.table + static_cast<int64_t>(b) * C.width));
   // a lane's place within 16 positions, in bytes; the positions' page is the same for the whole wavefront
   const char* __restrict__ kb = reinterpret_cast<const char*>(static_cast<const T*>(C.k) + kh * C.head_stride);
   const char* __restrict__ vb = reinterpret_cast<const char*>(static_cast<const T*>(C.v) + kh * C.head_stride);
-  const int64_t ts = C.token_stride * L::kBytes;
+  const int64_t ts = C.token_stride * L::kBytes, page_stride = C.page_stride * L::kBytes;
   const uint32_t in_k = static_cast<uint32_t>(l16 * ts) + g * 16, in_v = static_cast<uint32_t>(4 * g * ts) + l16 * L::VE * L::kBytes;
   const int in_page = (1 << C.page_shift) - 1;
 
@@ -214,14 +222,22 @@ __global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_a
     int64_t at[L::kSub];
     bool there[L::kSub];
   };
-  auto find = [&](int t0) {
+  struct Pages {
+    int number[L::kSub];
+  };
+  auto part_at = [&](int t0, int u) { return min(t0 + 16 * u, (to - 1) & ~15); };
+  auto look_up = [&](int t0) {
+    Pages p;
+#pragma unroll
+    for (int u = 0; u < L::kSub; ++u) p.number[u] = table[part_at(t0, u) >> C.page_shift];
+    return p;
+  };
+  auto find = [&](int t0, const Pages& p) {
     Where w;
 #pragma unroll
     for (int u = 0; u < L::kSub; ++u) {
-      const int p = min(t0 + 16 * u, (to - 1) & ~15);
-      const int number = table[p >> C.page_shift];
-      w.there[u] = number >= 0 && number < C.pages;
-      w.at[u] = (w.there[u] ? number : 0) * C.page_stride * L::kBytes + (p & in_page) * ts;
+      w.there[u] = static_cast<uint32_t>(p.number[u]) < A.pages;
+      w.at[u] = static_cast<int64_t>(w.there[u] ? p.number[u] : 0) * page_stride + (part_at(t0, u) & in_page) * ts;
     }
     return w;
   };
@@ -269,13 +285,15 @@ __global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_a
   Where here{};
   const int start = from + (RW == 1 ? wave * L::kKeys : 0);
   if (from < to) {
-    here = find(start);
+    here = find(start, look_up(start));
     load_rows(kb, here, K);
     if constexpr (RW > 1) load_rows(vb, here, Vr);
   }
+  Pages ahead{};  // of the next turn: looked up a turn ahead too
+  if (from < to) ahead = look_up(start + kTurn);
   int turn = 0;
   for (int t0 = start; t0 < to; t0 += kTurn) {
-    char* keys = smem + (RW == 1 ? wave * L::kTile : turn * 2 * L::kTile);
+    char* keys = sm.tiles + (RW == 1 ? wave * L::kTile : turn * 2 * L::kTile);
     turn ^= 1;
     if constexpr (RW == 1) load_v(here);
     __builtin_amdgcn_sched_barrier(0);
@@ -285,7 +303,8 @@ __global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_a
       *reinterpret_cast<u32x4*>(keys + L::piece(row, my_piece)) = K[i];
       if constexpr (RW > 1) *reinterpret_cast<u32x4*>(keys + L::kTile + row * L::kRow + my_piece * 16) = Vr[i];
     }
-    const Where next = find(t0 + kTurn);
+    const Where next = find(t0 + kTurn, ahead);
+    ahead = look_up(t0 + 2 * kTurn);
     load_rows(kb, next, K);  // behind the last tile one that is there: the loads on their way are then the same in number
     if constexpr (RW > 1) {
       load_rows(vb, next, Vr);
@@ -399,8 +418,10 @@ __global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_a
       for (int c = 0; c < L::VC; ++c)
 #pragma unroll
         for (int e = 0; e < L::kWords; ++e) most = largest<DT>(most, V[i][c][e]);
-    if (__builtin_expect(__any(not_finite<DT>(most)), 0)) {
-      float* mine = weights[wave];  // [key][row]
+    const bool odd = __any(not_finite<DT>(most));
+    if (__builtin_expect(odd, 0)) {
+      float* mine = sm.weights[wave];  // [key][row]
+      wave_lds_sync();
 #pragma unroll
       for (int i = 0; i < 4 * L::kSub; ++i) {
         mine[(16 * (i / 4) + 4 * g + i % 4) * 16 + l16] = P[i];
@@ -410,6 +431,12 @@ __global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_a
           for (int e = 0; e < L::kWords; ++e) V[i][c][e] = finite_only<DT>(V[i][c][e]);
       }
       wave_lds_sync();
+    }
+#pragma unroll
+    for (int c = 0; c < L::VC; ++c)
+#pragma unroll
+      for (int j = 0; j < L::VE; ++j) O[c * L::VE + j] = product(c, j, O[c * L::VE + j]);
+    if (__builtin_expect(odd, 0)) {
 #pragma unroll 1
       for (int k = 0; k < L::kKeys; ++k) {
         const int key = t0 + k, last = L::kSub - 1;  // no run-time index into here: it would leave the registers
@@ -417,7 +444,7 @@ __global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_a
         const int64_t at = k < 16 ? here.at[0] : here.at[last];
         const bool seen = page && key <= pos && (A.window <= 0 || key > pos - A.window);
         if (!seen) continue;
-        const float p = mine[k * 16 + l16];
+        const float p = sm.weights[wave][k * 16 + l16];
         const char* base = vb + at + k % 16 * ts;
 #pragma unroll
         for (int c = 0; c < L::VC; ++c)
@@ -433,23 +460,18 @@ __global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_a
           }
       }
     }
-#pragma unroll
-    for (int c = 0; c < L::VC; ++c)
-#pragma unroll
-      for (int j = 0; j < L::VE; ++j) O[c * L::VE + j] = product(c, j, O[c * L::VE + j]);
     here = next;
   }
 
   constexpr bool kOwn = RW == 1 && L::kTile == GT * kWave * 16;  // a wavefront's accumulators take the place of its own tile
   // Join the wavefronts of the same rows: sums and accumulators brought to the largest maximum. The tiles' place
   // takes the accumulators, a few at a time.
-  f32x4(*red)[GT][kWave] = reinterpret_cast<f32x4(*)[GT][kWave]>(smem);
+  f32x4(*red)[GT][kWave] = reinterpret_cast<f32x4(*)[GT][kWave]>(sm.tiles);
   l = sum4(l);
   if (g == 0) {
-    stat[wave][l16][0] = m;
-    stat[wave][l16][1] = l;
+    sm.stat[wave][l16][0] = m;
+    sm.stat[wave][l16][1] = l;
   }
-  const bool whole = sp.used <= 1;
   const int tid = threadIdx.x & 255, orow = tid & 15, om = tid >> 4;  // the row of each 16 and the 16th of its values that this thread writes
   const int half = threadIdx.x >> 8;                                  // NW = 8: which of the accumulators
 #pragma unroll
@@ -464,20 +486,19 @@ __global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_a
       if (out >= rows) continue;
       float top = kNegInf, sum = 0.f, f[KW];
 #pragma unroll
-      for (int k = 0; k < KW; ++k) top = fmaxf(top, stat[RW > 1 ? w : k][orow][0]);
+      for (int k = 0; k < KW; ++k) top = fmaxf(top, sm.stat[RW > 1 ? w : k][orow][0]);
 #pragma unroll
       for (int k = 0; k < KW; ++k) {
-        const float mw = stat[RW > 1 ? w : k][orow][0];
+        const float mw = sm.stat[RW > 1 ? w : k][orow][0];
         f[k] = mw == kNegInf ? 1.f : exp2_(mw - top);  // without a weight: zeros, or NaN
-        sum += stat[RW > 1 ? w : k][orow][1] * f[k];
+        sum += sm.stat[RW > 1 ? w : k][orow][1] * f[k];
       }
       const int ot = token_of(A, out), head = kh * share + out - ot * share;
       const int64_t line = (sp.lo + ot) * C.heads + head;
       if (om == 0 && half == 0 && j0 == 0) {
-        if (!whole) {
-          float* st = A.stat + (line * A.splits + split) * 2;
-          st[0] = top;
-          st[1] = sum;
+        if (part != nullptr) {
+          part_stat[2 * (out - block0)] = top;
+          part_stat[2 * (out - block0) + 1] = sum;
         } else if (A.lse != nullptr) {
           A.lse[line] = natural_log_sum(top, sum);
         }
@@ -496,8 +517,8 @@ __global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_a
             y[j] = fmaf(reinterpret_cast<const float*>(&red[RW > 1 ? w : k][c * kRun + j][(om >> 2) * 16 + orow])[om & 3], f[k], y[j]);
         }
         const int v = (j0 / kRun + c) * 16 * kRun + om * kRun;
-        if (!whole) {
-          store_f32<0, kRun>(A.part + (line * A.splits + split) * D + v, y);
+        if (part != nullptr) {
+          store_f32<0, kRun>(part + static_cast<int64_t>(out - block0) * D + v, y);
         } else {
           const float inv = 1.f / sum;
 #pragma unroll
@@ -509,7 +530,83 @@ __global__ __launch_bounds__(NW* kWave, NW > kWaves || D > 128 ? 2 : 3) void k_a
   }
 }
 
-// Joins the workgroups along a cache: WR wavefronts per row and head, a lane D / 64 of its values.
+// A workgroup per request and key head.
+template <int DT, int D>
+__global__ __launch_bounds__(kMany* kWave, 2) void k_attend_whole(const AttendArgs A) {
+  __shared__ Shared<DT, D, 1, kMany> sm;
+  const int kh = static_cast<int>(blockIdx.x % A.c.key_heads), b = static_cast<int>(blockIdx.x / A.c.key_heads);
+  const Span sp = span_of(A, b);
+  if (sp.n == 0) return;
+  attend_keys<DT, D, 1, kMany>(A, sm, sp, b, kh, 0, sp.base, sp.k1, nullptr, nullptr);
+}
+
+// The turns of all requests (of `step` keys, row block after row block) are cut into equal shares, one for each of
+// a key head's workgroups; the requests' lengths are known here only. A share that ends inside a row block leaves
+// partial results in the workgroup's second place, one that begins inside in its first; the workgroup that begins a
+// row block notes which ones hold it.
+template <int DT, int D, int RW>
+__global__ __launch_bounds__(kWaves * kWave, 2) void k_attend(const AttendArgs A) {
+  __shared__ Shared<DT, D, RW, kWaves> sm;
+  constexpr int kStep = Tile<DT, D>::kKeys * kWaves / RW;
+  const CacheArgs& C = A.c;
+  // neighbouring heads, whose keys lie side by side, run at the same time
+  const int kh = static_cast<int>(blockIdx.x % C.key_heads), me = static_cast<int>(blockIdx.x / C.key_heads);
+  const int lane = threadIdx.x & 63;
+  auto turns = [&](int i) {
+    const Span sp = span_of(A, min(i, C.batch - 1));
+    return i < C.batch ? sp.turns(kStep) * ((sp.n * A.share + 16 * RW - 1) / (16 * RW)) : 0;
+  };
+  // every wavefront for itself: the sum of all turns, then the request in which this share begins
+  int total = 0, here = 0;
+  int mine = turns(lane), run = scan(mine, lane, here);
+  total = here;
+  for (int i = kWave; i < C.batch; i += kWave) {
+    int more;
+    scan(turns(i + lane), lane, more);
+    total += more;
+  }
+  const int share = share_of(total, A.groups), w0 = me * share, w1 = min(w0 + share, total);
+  if (w0 >= total) return;
+  int b = 0, begin = 0;  // request, and its first turn
+  for (;;) {
+    const uint64_t past = __ballot(begin + run > w0);
+    if (past != 0) {
+      const int at = __builtin_ctzll(past);
+      begin += __builtin_amdgcn_readlane(run - mine, at);
+      b += at;
+      break;
+    }
+    begin += here;
+    b += kWave;
+    mine = turns(b + lane);
+    run = scan(mine, lane, here);
+  }
+  Span sp = span_of(A, b);
+  for (int w = w0; w < w1;) {
+    const int each = sp.turns(kStep), blocks = (sp.n * A.share + 16 * RW - 1) / (16 * RW);
+    const int rb = RW == 1 ? 0 : (w - begin) / each, t0 = w - begin - rb * each, n = min(each - t0, w1 - w);
+    const bool whole = n == each;
+    const int64_t place = (static_cast<int64_t>(me) * C.key_heads + kh) * 2 + (t0 == 0 ? 1 : 0);
+    if (t0 == 0 && kh == 0 && threadIdx.x == 0) {
+      int32_t* note = A.notes + (static_cast<int64_t>(b) * A.row_blocks + rb) * 2;
+      note[0] = me;
+      note[1] = me + (each - n + share - 1) / share;
+    }
+    if (w > w0) __syncthreads();  // the last part's results have been read
+    const int from = sp.base + t0 * kStep;
+    const int to = static_cast<int>(min(static_cast<int64_t>(from) + static_cast<int64_t>(n) * kStep, static_cast<int64_t>(sp.k1)));
+    attend_keys<DT, D, RW, kWaves>(A, sm, sp, b, kh, rb, from, to, whole ? nullptr : A.part + place * A.block_rows * D,
+                                   A.stat + place * A.block_rows * 2);
+    w += n;
+    while (w < w1 && w == begin + sp.turns(kStep) * ((sp.n * A.share + 16 * RW - 1) / (16 * RW))) {  // on to the next request with rows
+      begin = w;
+      sp = span_of(A, ++b);
+    }
+  }
+}
+
+// Joins the parts of the rows that more than one workgroup has: WR wavefronts per row and head, a lane D / 64 of
+// its values.
 template <int DT, int D, int WR>
 __global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_attend_join(const AttendArgs A) {
   using T = stor_t<DT>;
@@ -517,23 +614,28 @@ __global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_atten
   using vec = __attribute__((ext_vector_type(N))) float;
   __shared__ float acc[WR][D];
   __shared__ float stats[WR][2];
+  const CacheArgs& C = A.c;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned item = blockIdx.x * kRows + (WR == 1 ? wave : 0);
-  const int head = static_cast<int>(item % A.c.heads);
-  const unsigned rest = item / A.c.heads;
+  const int head = static_cast<int>(item % C.heads);
+  const unsigned rest = item / C.heads;
   const int token = static_cast<int>(rest % A.max_tokens), b = static_cast<int>(rest / A.max_tokens);
-  if (b >= A.c.batch) return;
+  if (b >= C.batch) return;
   const Span sp = span_of(A, b);
-  if (token >= sp.n || sp.used <= 1) return;
-  const int64_t line = (sp.lo + token) * A.c.heads + head;
-  const float* __restrict__ stat = A.stat + line * A.splits * 2;
-  const float* __restrict__ part = A.part + line * A.splits * D + lane * N;
+  if (token >= sp.n) return;
+  const int kh = head / A.share, row = token * A.share + head - kh * A.share, rb = row / A.block_rows, in_block = row - rb * A.block_rows;
+  const int32_t* note = A.notes + (static_cast<int64_t>(b) * A.row_blocks + rb) * 2;
+  const int first = note[0], parts = note[1] - first + 1;
+  if (parts == 1) return;
+  // part 0 in the second place of its workgroup, the others in the first of theirs
+  auto place = [&](int s) { return ((static_cast<int64_t>(first + s) * C.key_heads + kh) * 2 + (s == 0 ? 1 : 0)) * A.block_rows + in_block; };
   float top = kNegInf, sum = 0.f, y[N] = {};
   // up to 64 parts at a time, a lane's maximum and sum each; several wavefronts take a run of parts each
-  const int per = WR == 1 ? sp.used : (sp.used + WR - 1) / WR, s1 = WR == 1 ? sp.used : min((wave + 1) * per, sp.used);
+  const int per = WR == 1 ? parts : (parts + WR - 1) / WR, s1 = WR == 1 ? parts : min((wave + 1) * per, parts);
   for (int s0 = WR == 1 ? 0 : wave * per; s0 < s1; s0 += kWave) {
     const int s = s0 + lane;
-    const float ms = s < s1 ? stat[2 * s] : kNegInf, ls = s < s1 ? stat[2 * s + 1] : 0.f;
+    const float* stat = A.stat + place(s) * 2;
+    const float ms = s < s1 ? stat[0] : kNegInf, ls = s < s1 ? stat[1] : 0.f;
     float now = ms;
 #pragma unroll
     for (int d = 1; d < 16; d *= 2) now = fmaxf(now, __shfl_xor(now, d, kWave));
@@ -545,12 +647,16 @@ __global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_atten
 #pragma unroll
     for (int e = 0; e < N; ++e) y[e] *= old;
     const int n = min(s1 - s0, kWave);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const vec x = *reinterpret_cast<const vec*>(part + static_cast<int64_t>(s0 + i) * D);
-      const float fi = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), i));
+    for (int i0 = 0; i0 < n; i0 += 4) {  // four at a time, the last again where there are fewer
+      vec x[4];
 #pragma unroll
-      for (int e = 0; e < N; ++e) y[e] = fmaf(x[e], fi, y[e]);
+      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const vec*>(A.part + place(s0 + min(i0 + i, n - 1)) * D + lane * N);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float fi = i0 + i < n ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), min(i0 + i, n - 1))) : 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) y[e] = i0 + i < n ? fmaf(x[i][e], fi, y[e]) : y[e];
+      }
     }
   }
   if constexpr (WR > 1) {
@@ -580,72 +686,68 @@ __global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_atten
 #pragma unroll
   for (int e = 0; e < N; ++e) y[e] = sum == 0.f ? 0.f : y[e] / sum;
   store_f32<DT, N>(static_cast<T*>(A.o) + (sp.lo + token) * A.o_stride + static_cast<int64_t>(head) * D + lane * N, y);
-  if (lane == 0 && A.lse != nullptr) A.lse[line] = natural_log_sum(top, sum);
+  if (lane == 0 && A.lse != nullptr) A.lse[(sp.lo + token) * C.heads + head] = natural_log_sum(top, sum);
 }
 
 namespace {
 
-// Wavefronts of a workgroup that take rows of their own.
-int row_waves(const AttendArgs& a) {
-  const int64_t rows = static_cast<int64_t>(a.max_tokens) * (a.c.heads / a.c.key_heads);
-  return rows <= 16 ? 1 : kWaves;
-}
-int64_t row_blocks(const AttendArgs& a) {
-  const int64_t rows = static_cast<int64_t>(a.max_tokens) * a.share, of = 16 * row_waves(a);
-  return (rows + of - 1) / of;
-}
-
-template <int DT, int D, int RW, int NW>
-hipError_t attend(const AttendArgs& a, hipStream_t s) {
-  const int64_t blocks = row_blocks(a), units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * a.splits;
-  const int64_t grid = RW == 1 ? units : (units + 7) / 8 * 8 * blocks;
-  k_attend<DT, D, RW, NW><<<dim3(static_cast<unsigned>(grid)), dim3(NW * kWave), 0, s>>>(a, static_cast<unsigned>(blocks),
-                                                                                       static_cast<unsigned>(units));
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t items = static_cast<int64_t>(a.c.batch) * a.max_tokens * a.c.heads;
-  if (a.splits <= 4) k_attend_join<DT, D, 1><<<dim3(static_cast<unsigned>((items + kWaves - 1) / kWaves)), dim3(kWaves * kWave), 0, s>>>(a);
-  else k_attend_join<DT, D, 8><<<dim3(static_cast<unsigned>(items)), dim3(8 * kWave), 0, s>>>(a);
-  return hipGetLastError();
-}
-
 template <int DT, int D>
-hipError_t by_rows(const AttendArgs& a, hipStream_t s) {
-  if (row_waves(a) > 1) return attend<DT, D, kWaves, kWaves>(a, s);
-  return a.many ? attend<DT, D, 1, kMany>(a, s) : attend<DT, D, 1, kWaves>(a, s);
+hipError_t attend(const AttendArgs& a, hipStream_t s) {
+  const int64_t heads = a.c.key_heads;
+  if (a.groups == 0) {
+    k_attend_whole<DT, D><<<dim3(static_cast<unsigned>(a.c.batch * heads)), dim3(kMany * kWave), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const dim3 grid(static_cast<unsigned>(a.groups * heads)), threads(kWaves * kWave);
+  if (a.block_rows <= 16) k_attend<DT, D, 1><<<grid, threads, 0, s>>>(a);
+  else k_attend<DT, D, kWaves><<<grid, threads, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t items = static_cast<int64_t>(a.c.batch) * a.max_tokens * a.c.heads;
+  // many rows: a wavefront each
+  if (items > 512)
+    k_attend_join<DT, D, 1><<<dim3(static_cast<unsigned>((items + kWaves - 1) / kWaves)), threads, 0, s>>>(a);
+  else
+    k_attend_join<DT, D, 8><<<dim3(static_cast<unsigned>(items)), dim3(8 * kWave), 0, s>>>(a);
+  return hipGetLastError();
 }
 
 template <int DT>
 hipError_t pick(const AttendArgs& a, hipStream_t s) {
-  return a.c.dim == 64 ? by_rows<DT, 64>(a, s) : a.c.dim == 128 ? by_rows<DT, 128>(a, s) : by_rows<DT, 256>(a, s);
+  return a.c.dim == 64 ? attend<DT, 64>(a, s) : a.c.dim == 128 ? attend<DT, 128>(a, s) : attend<DT, 256>(a, s);
 }
 
 }  // namespace
 
-void plan_attend(int32_t io_dtype, AttendArgs& a) {
-  const int tile = io_dtype == SEED_BF16 ? 32 : 16;
-  const int64_t step = tile * (row_waves(a) > 1 ? 1 : kWaves);  // keys of one turn of a workgroup
-  const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * row_blocks(a);
+bool plan_attend(int32_t io_dtype, AttendArgs& a) {
+  const int64_t rows = static_cast<int64_t>(a.max_tokens) * a.share, tile = io_dtype == SEED_BF16 ? 32 : 16;
+  a.block_rows = static_cast<int32_t>(rows <= 16 ? rows : 16 * kWaves);
+  a.row_blocks = static_cast<int32_t>((rows + a.block_rows - 1) / a.block_rows);
+  const int64_t step = rows <= 16 ? tile * kWaves : tile;  // keys of one turn of a workgroup
   int64_t span = a.capacity;
-  if (a.window > 0) {
-    const int64_t near = static_cast<int64_t>(a.window) + a.max_tokens - 1 + 31;
-    span = near < span ? near : span;
-  }
-  const int64_t fill = a.c.dim == 256 ? 512 : 256;  // workgroups that fill the chip when they are equal
-  int64_t splits = (fill + units - 1) / units;
-  if (a.c.batch > 1) {
-    const int64_t more = std::min((2048 + units - 1) / units, span / 1024);
-    splits = std::max(splits, more);
-  }
-  splits = std::max(std::min(splits, (span + 127) / 128), int64_t{1});
+  if (a.window > 0) span = std::min(span, static_cast<int64_t>(a.window) + a.max_tokens - 1 + 31);
+  const int64_t turns = static_cast<int64_t>(a.c.batch) * a.row_blocks * ((span + step - 1) / step);  // at most, of a key head
+  if (turns >= int64_t{1} << 30) return false;
   const int64_t few = (io_dtype == SEED_BF16 ? 1024 : 512) / (a.c.dim == 256 ? 4 : 1);
-  a.many = splits > 1 && span <= few && row_waves(a) == 1;
-  if (a.many) splits = 1;
-  a.chunk = static_cast<int32_t>(((span + splits - 1) / splits + step - 1) / step * step);
-  a.splits = static_cast<int32_t>((span + a.chunk - 1) / a.chunk);
+  a.groups = 0;
+  if (rows <= 16 && span <= few && static_cast<int64_t>(a.c.batch) * a.c.key_heads <= 256) return true;
+  a.groups = static_cast<int32_t>(std::max(std::min((kGroups + a.c.key_heads - 1) / a.c.key_heads, turns), int64_t{1}));
+  return true;
 }
 
-hipError_t launch_attend(int32_t io_dtype, const AttendArgs& a, hipStream_t s) {
+int64_t attend_workspace(const AttendArgs& a) {
+  if (a.groups == 0) return 0;
+  const int64_t places = static_cast<int64_t>(a.groups) * a.c.key_heads * 2 * a.block_rows;
+  return places * (a.c.dim + 2) * 4 + static_cast<int64_t>(a.c.batch) * a.row_blocks * 8;
+}
+
+hipError_t launch_attend(int32_t io_dtype, AttendArgs a, void* ws, hipStream_t s) {
+  if (a.groups > 0) {
+    const int64_t places = static_cast<int64_t>(a.groups) * a.c.key_heads * 2 * a.block_rows;
+    a.part = static_cast<float*>(ws);
+    a.stat = a.part + places * a.c.dim;
+    a.notes = reinterpret_cast<int32_t*>(a.stat + places * 2);
+  }
   return io_dtype == SEED_BF16 ? pick<1>(a, s) : pick<0>(a, s);
 }
 

@@ -53,14 +53,17 @@ struct AttendArgs {
   float per_share;          // 1 / share
   float scale2;             // |scale| log2(e)
   uint32_t negate;          // the sign bits of a word of q, where scale is negative
-  int32_t chunk, splits;    // keys of a workgroup, and workgroups along the longest cache
-  bool many;                // more wavefronts in the place of more workgroups
+  uint32_t pages;           // of the pool, as far as table entries reach
+  int32_t block_rows;       // rows that a workgroup takes at a time, of max_tokens share,
+  int32_t row_blocks;       // and how many times
+  int32_t groups;           // workgroups that share a key head's turns; 0: a workgroup per request and key head
   int64_t q_stride, o_stride;
   const void* q;
   void* o;
-  float* lse;   // nullptr: not written
-  float* part;  // [tokens][heads][splits][dim], then [tokens][heads][splits][2]: weights' maximum and sum
-  float* stat;
+  float* lse;      // nullptr: not written
+  float* part;     // [groups][key_heads][2][block_rows][dim]: accumulators of rows that several workgroups have,
+  float* stat;     // and their maximum and sum [..][block_rows][2]
+  int32_t* notes;  // [batch][row_blocks][2]: the first and last workgroup of each
 };
 
 struct VerifyArgs {
@@ -80,9 +83,10 @@ struct VerifyArgs {
 
 hipError_t launch_rotate_rows(int32_t io_dtype, const RotateArgs& a, hipStream_t s);
 hipError_t launch_cache_append(int32_t io_dtype, const AppendArgs& a, hipStream_t s);
-// Sets chunk, splits and many from the sizes.
-void plan_attend(int32_t io_dtype, AttendArgs& a);
-hipError_t launch_attend(int32_t io_dtype, const AttendArgs& a, hipStream_t s);
+// Sets block_rows, row_blocks and groups from the sizes; false: more turns than are counted.
+bool plan_attend(int32_t io_dtype, AttendArgs& a);
+int64_t attend_workspace(const AttendArgs& a);
+hipError_t launch_attend(int32_t io_dtype, AttendArgs a, void* ws, hipStream_t s);
 int32_t verify_segments(int32_t vocab);
 hipError_t launch_verify(int32_t io_dtype, const VerifyArgs& a, hipStream_t s);
 

@@ -133,22 +133,15 @@ int check_attend(const seed_cache* c, const seed_tokens* t, const seed_attend* w
   a.per_share = 1.f / static_cast<float>(a.share);
   a.max_tokens = w->max_tokens;
   a.capacity = w->max_length;
+  a.pages = static_cast<uint32_t>(c->pages < (int64_t{1} << 31) ? c->pages : int64_t{1} << 31);
   a.window = w->window >= w->max_length ? 0 : w->window;  // a window that holds every position
   a.scale2 = static_cast<float>(scale2);
   a.negate = w->scale < 0.f ? (c->io_dtype == SEED_F32 ? 0x80000000u : 0x80008000u) : 0u;
   // the launch has to hold a workgroup for every 16 rows, and one per row to join them
   const int64_t rows = static_cast<int64_t>(w->max_tokens) * t->heads;
   if (a.share > kMostShare || rows > kMostBlocks / c->batch) return SEED_ERR_UNSUPPORTED;
-  plan_attend(c->io_dtype, a);
-  return SEED_OK;
+  return plan_attend(c->io_dtype, a) ? SEED_OK : SEED_ERR_UNSUPPORTED;
 }
-// Bytes of the partial results, 0 for none, -1 for too many.
-int64_t attend_workspace(const AttendArgs& a) {
-  if (a.splits <= 1) return 0;
-  const int64_t lines = a.c.tokens * a.c.heads, line = static_cast<int64_t>(a.splits) * (a.c.dim + 2) * 4;
-  return a.c.tokens > kMostRows || lines > kMostBytes / line ? -1 : lines * line;
-}
-
 int check_drafts(const seed_drafts* d) {
   if (!d || d->batch <= 0 || d->vocab <= 0 || d->rows < 0 || !io_ok(d->io_dtype)) return SEED_ERR_ARG;
   if (d->io_dtype == SEED_F16) return SEED_ERR_UNSUPPORTED;
@@ -276,8 +269,7 @@ int seed_cache_append(const seed_cache* cache, const seed_tokens* tokens, const 
 size_t seed_attend_workspace_bytes(const seed_cache* cache, const seed_tokens* tokens, const seed_attend* attend) {
   AttendArgs a{};
   if (check_attend(cache, tokens, attend, a) != SEED_OK) return 0;
-  const int64_t need = attend_workspace(a);
-  return need > 0 ? static_cast<size_t>(need) : 0;
+  return static_cast<size_t>(attend_workspace(a));
 }
 
 int seed_decode_attend(const seed_cache* cache, const seed_tokens* tokens, const seed_attend* attend, const void* q,
@@ -295,7 +287,7 @@ int seed_decode_attend(const seed_cache* cache, const seed_tokens* tokens, const
   const Rows rl = flat(lse, n, static_cast<int64_t>(tokens->heads) * 4);
   const Rows fb = table_of(cache), fo = offsets_of(cache, tokens), fl = lengths_of(cache, tokens);
   const int64_t need = attend_workspace(a);
-  if (need < 0 || !pool_fits(cache) || !all_fit({rq, ro, rl, fb, fo, fl})) return SEED_ERR_UNSUPPORTED;
+  if (!pool_fits(cache) || !all_fit({rq, ro, rl, fb, fo, fl})) return SEED_ERR_UNSUPPORTED;
   if (pools_meet(cache) || any_overlap({ro, rl}, {rq, fb, fo, fl})) return SEED_ERR_ARG;
   for (const Rows& r : {ro, rl})
     if (meets(r, cache, cache->k) || meets(r, cache, cache->v)) return SEED_ERR_ARG;
@@ -306,15 +298,13 @@ int seed_decode_attend(const seed_cache* cache, const seed_tokens* tokens, const
     const Rows fw = flat(ws, need, 1);
     if (!fw.fits()) return SEED_ERR_UNSUPPORTED;
     if (any_overlap({fw}, {rq, ro, rl, fb, fo, fl}) || meets(fw, cache, cache->k) || meets(fw, cache, cache->v)) return SEED_ERR_ARG;
-    a.part = static_cast<float*>(ws);
-    a.stat = a.part + n * tokens->heads * a.splits * cache->dim;
   }
   a.q_stride = tokens->q_stride;
   a.o_stride = tokens->o_stride;
   a.q = q;
   a.o = o;
   a.lse = lse;
-  return hip_status(launch_attend(cache->io_dtype, a, static_cast<hipStream_t>(stream)));
+  return hip_status(launch_attend(cache->io_dtype, a, ws, static_cast<hipStream_t>(stream)));
 }
 
 size_t seed_verify_workspace_bytes(const seed_drafts* drafts) {
