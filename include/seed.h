@@ -648,7 +648,7 @@ typedef struct seed_drafts {
   int64_t target_stride, draft_stride;  /* elements between rows (of an absent draft ignored)    */
 } seed_drafts;
 
-/* Workspace bytes of seed_verify_drafts (0 for invalid arguments). Host-only, pure. */
+/* Workspace bytes of seed_verify_drafts (0: none needed, or invalid arguments). Host-only, pure. */
 size_t seed_verify_workspace_bytes(const seed_drafts *drafts);
 
 /*
@@ -664,8 +664,8 @@ size_t seed_verify_workspace_bytes(const seed_drafts *drafts);
  *   drafts    int32 [rows]; uniforms float [rows], draws float [batch], in [0, 1).
  *   out       int32 [rows], written: a request's kept drafts, the drawn token, then -1. May be drafts.
  *   counts    int32 [batch], written: tokens the request gained, drafts kept + 1 (0 for a request of no rows).
- *   ws        workspace of seed_verify_workspace_bytes bytes, 16-byte aligned; it must not be shared by
- *             calls that may run at the same time.
+ *   ws        workspace of seed_verify_workspace_bytes bytes, 16-byte aligned (NULL when that is 0); it must not
+ *             be shared by calls that may run at the same time.
  */
 int seed_verify_drafts(const seed_drafts *d, const void *target, const void *draft, const int32_t *drafts,
                        const float *uniforms, const float *draws, int32_t *out, int32_t *counts, void *ws,

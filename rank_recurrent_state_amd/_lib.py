@@ -591,7 +591,7 @@ class _Args:
     __slots__ = ("torch", "device", "guard")
 
     def __init__(self, torch):
-        self.torch, self.device, self.guard = torch, -1, None
+        self.torch, self.device, self.guard = torch, -2, None  # no device yet: -1 is what host tensors give
 
     def _on(self, name, t):
         if not t.is_cuda:
@@ -606,7 +606,8 @@ class _Args:
         """A contiguous tensor of numel elements, or None."""
         if t is None:
             return None
-        self._on(name, t)
+        if t.get_device() != self.device:
+            self._on(name, t)
         if t.dtype is not dtype:
             raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
         if t.numel() != numel:
@@ -620,7 +621,8 @@ class _Args:
         and the row stride in elements. (None, width) for None."""
         if t is None:
             return None, width
-        self._on(name, t)
+        if t.get_device() != self.device:
+            self._on(name, t)
         if t.dtype is not dtype:
             raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
         if t.shape != shape:

@@ -77,7 +77,7 @@ struct VerifyArgs {
   const float* draws;
   int32_t* out;
   int32_t* counts;
-  double* sums;   // [batch][segments][2]: of the weights, and of target
+  double* sums;   // [batch][segments] of the weights
   int32_t* kept;  // [batch]
 };
 
@@ -88,6 +88,7 @@ bool plan_attend(int32_t io_dtype, AttendArgs& a);
 int64_t attend_workspace(const AttendArgs& a);
 hipError_t launch_attend(int32_t io_dtype, AttendArgs a, void* ws, hipStream_t s);
 int32_t verify_segments(int32_t vocab);
+int32_t verify_alone();  // most segments of a request that one workgroup does without a workspace
 hipError_t launch_verify(int32_t io_dtype, const VerifyArgs& a, hipStream_t s);
 
 #ifdef __HIPCC__

@@ -150,7 +150,8 @@ int check_drafts(const seed_drafts* d) {
   return SEED_OK;
 }
 int64_t verify_workspace(const seed_drafts* d) {
-  return static_cast<int64_t>(d->batch) * verify_segments(d->vocab) * 16 + static_cast<int64_t>(d->batch) * 4;
+  if (verify_segments(d->vocab) <= verify_alone()) return 0;
+  return static_cast<int64_t>(d->batch) * verify_segments(d->vocab) * 8 + static_cast<int64_t>(d->batch) * 4;
 }
 
 }  // namespace
@@ -329,11 +330,13 @@ int seed_verify_drafts(const seed_drafts* d, const void* target, const void* dra
   if (!all_fit({rt, rd, fo, fx, fu, fr, out_rows, fc})) return SEED_ERR_UNSUPPORTED;
   if (any_overlap({out_rows, fc}, {rt, rd, fo, fu, fr}) || overlap(fc, fx) || (overlap(out_rows, fx) && out != drafts)) return SEED_ERR_ARG;
   const int64_t need = verify_workspace(d);
-  if (!ws || ws_bytes < static_cast<size_t>(need)) return SEED_ERR_WORKSPACE;
-  if (!aligned(ws, 16)) return SEED_ERR_ARG;
-  const Rows fw = flat(ws, need, 1);
-  if (!fw.fits()) return SEED_ERR_UNSUPPORTED;
-  if (any_overlap({fw}, {rt, rd, fo, fx, fu, fr, out_rows, fc})) return SEED_ERR_ARG;
+  if (need > 0) {
+    if (!ws || ws_bytes < static_cast<size_t>(need)) return SEED_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return SEED_ERR_ARG;
+    const Rows fw = flat(ws, need, 1);
+    if (!fw.fits()) return SEED_ERR_UNSUPPORTED;
+    if (any_overlap({fw}, {rt, rd, fo, fx, fu, fr, out_rows, fc})) return SEED_ERR_ARG;
+  }
   VerifyArgs a{};
   a.batch = d->batch;
   a.vocab = d->vocab;
@@ -349,8 +352,10 @@ int seed_verify_drafts(const seed_drafts* d, const void* target, const void* dra
   a.draws = draws;
   a.out = out;
   a.counts = counts;
-  a.sums = static_cast<double*>(ws);
-  a.kept = reinterpret_cast<int32_t*>(a.sums + static_cast<int64_t>(d->batch) * a.segments * 2);
+  if (need > 0) {
+    a.sums = static_cast<double*>(ws);
+    a.kept = reinterpret_cast<int32_t*>(a.sums + static_cast<int64_t>(d->batch) * a.segments);
+  }
   return hip_status(launch_verify(d->io_dtype, a, static_cast<hipStream_t>(stream)));
 }
 

@@ -1,11 +1,13 @@
 // Verification of drafted tokens: a request's drafts x are kept in turn while u q(x) < p(x); the token at the
 // first refused row is the smallest t with draw W < w_0 + .. + w_t, w = max(p - q, 0) (behind the last draft: p).
 //
-// What bounds it: one row of p and one of q per request, read once from HBM; for few requests the two
-// launches. Rows are cut into segments of kSegment tokens: the first kernel sums each (fp64: exact products and
-// differences, and borders between tokens that do not move with the order of the sums by more than 1e-13), the
-// second finds the segment that holds the draw and walks its tokens. Every workgroup finds the request's first
-// refused row by itself, from a few gathered values.
+// What bounds it: one row of p and one of q per request, read once from HBM; for few requests the latency of
+// what follows from what: the row's number, a few drafts' probabilities, the row, the sums, the segment that holds
+// the draw. Rows are cut into segments of 1024 tokens, a wavefront each: it sums them (fp64: exact products and
+// differences, and borders between tokens that do not move with the order of the sums by more than 1e-13), then the
+// segment that holds the draw is read again and its tokens are walked. Every wavefront finds the request's first
+// refused row by itself, from a few gathered values, and no step needs more than one wavefront: a row that one
+// workgroup reads as fast as a second launch takes is summed and walked by it, larger ones in two launches.
 #include "attend.hpp"
 #include "common.hpp"
 
@@ -13,42 +15,80 @@ namespace seed {
 
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / kWave;
-constexpr int kRun = 16;  // tokens of a thread
-constexpr int kSegment = kThreads * kRun;
+constexpr int kRun = 16;                  // tokens of a lane
+constexpr int kSegment = kWave * kRun;    // and of a segment
+constexpr int kWaves = 4;                 // of a workgroup that sums
+constexpr int kMany = 16;                 // of one that does a request alone
+constexpr int kMost = 32;                 // segments of such a request
+constexpr int kPair = 2;                  // segments that a wavefront loads at once
+
+// 16 bytes at any address that holds a value: rows of an odd length start anywhere.
+template <int DT> struct Any16;
+template <> struct Any16<0> { using T = __attribute__((ext_vector_type(4), aligned(4))) uint32_t; };
+template <> struct Any16<1> { using T = __attribute__((ext_vector_type(4), aligned(2))) uint32_t; };
 
 // Weights of a row's tokens: p less q, or p with token x taken out; NaN and negative ones are 0.
 template <int DT>
 struct Weights {
+  static constexpr int N = DT == 0 ? 4 : 8;  // values of 16 bytes
   const stor_t<DT>* p;
   const stor_t<DT>* q;  // nullptr: nothing to take away
   int x;                // -1: no token taken out
-  // of tokens [t0, t0 + N), and of p alone
-  template <int N>
-  __device__ __forceinline__ void load(int t0, int vocab, double (&w)[N], double (&full)[N]) const {
-    float pt[N], qt[N];
-    values<N>(p, t0, vocab, pt);
-    if (q != nullptr) values<N>(q, t0, vocab, qt);
+
+  // K times N tokens, the k-th from t0 + k step on; inside: the whole wavefront's tokens are below vocab
+  template <int K>
+  __device__ __forceinline__ void load(int t0, int step, int vocab, bool inside, double (&w)[K * N]) const {
+    float pt[K][N], qt[K][N];
+    if (inside) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      full[e] = pt[e] > 0.f ? static_cast<double>(pt[e]) : 0.0;
+      for (int k = 0; k < K; ++k) wide(p + t0 + k * step, pt[k]);
       if (q != nullptr) {
-        const double d = static_cast<double>(pt[e]) - static_cast<double>(qt[e]);
-        w[e] = d > 0.0 ? d : 0.0;
-      } else {
-        w[e] = t0 + e == x ? 0.0 : full[e];
+#pragma unroll
+        for (int k = 0; k < K; ++k) wide(q + t0 + k * step, qt[k]);
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < N; ++e) pt[k][e] = qt[k][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (t0 + k * step <= vocab - N) {
+          wide(p + t0 + k * step, pt[k]);
+          if (q != nullptr) wide(q + t0 + k * step, qt[k]);
+        }
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (t0 + k * step > vocab - N && t0 + k * step < vocab) {  // the row's last tokens: one lane's
+#pragma unroll
+          for (int e = 0; e < N - 1; ++e)
+            if (t0 + k * step + e < vocab) {
+              pt[k][e] = to_f32<DT>(p[t0 + k * step + e]);
+              if (q != nullptr) qt[k][e] = to_f32<DT>(q[t0 + k * step + e]);
+            }
+        }
     }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const double pe = pt[k][e];
+        const double d = q != nullptr ? pe - static_cast<double>(qt[k][e]) : (t0 + k * step + e == x ? 0.0 : pe);
+        w[k * N + e] = fmax(d, 0.0);  // of NaN: 0
+      }
   }
 
  private:
-  template <int N>
-  static __device__ __forceinline__ void values(const stor_t<DT>* row, int t0, int vocab, float (&v)[N]) {
-    if (t0 <= vocab - N && (reinterpret_cast<uintptr_t>(row + t0) & 15) == 0) {
-      load_f32<DT, N>(row + t0, v);
-    } else {
+  static __device__ __forceinline__ void wide(const stor_t<DT>* p, float (&v)[N]) {
+    const auto x = __builtin_nontemporal_load(reinterpret_cast<const typename Any16<DT>::T*>(p));
 #pragma unroll
-      for (int e = 0; e < N; ++e) v[e] = t0 < vocab - e ? to_f32<DT>(row[t0 + e]) : 0.f;
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (DT == 0) {
+        v[e] = __uint_as_float(x[e]);
+      } else {
+        v[2 * e] = lo16<DT>(x[e]);
+        v[2 * e + 1] = hi16<DT>(x[e]);
+      }
     }
   }
 };
@@ -87,168 +127,221 @@ __device__ __forceinline__ Weights<DT> weights_at(const VerifyArgs& A, int64_t r
   return w;
 }
 
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_mov_dpp(static_cast<int>(u), CTRL, 0xF, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_mov_dpp(static_cast<int>(u >> 32), CTRL, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// Sum over all lanes, the same in each.
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d, kWave);
+  v += dpp64<0xB1>(v);
+  v += dpp64<0x4E>(v);
+  v += dpp64<0x141>(v);
+  v += dpp64<0x140>(v);
+  v += __shfl_xor(v, 16, kWave);
+  v += __shfl_xor(v, 32, kWave);
   return v;
 }
-
-// Sum of the values of the threads before this one, and of all.
-__device__ __forceinline__ double sum_before(double v, double* red, double& total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Sum of the lanes before this one, and of all.
+__device__ __forceinline__ double sum_before(double v, double& total) {
+  const int lane = threadIdx.x & 63;
   double run = v;
 #pragma unroll
   for (int d = 1; d < kWave; d *= 2) {
     const double up = __shfl_up(run, d, kWave);
     if (lane >= d) run += up;
   }
+  total = __shfl(run, kWave - 1, kWave);
   const double above = __shfl_up(run, 1, kWave);
-  __syncthreads();  // the last call's sums have been read
-  if (lane == kWave - 1) red[wave] = run;
-  __syncthreads();
-  double before = 0.0;
-  total = 0.0;
+  return lane == 0 ? 0.0 : above;
+}
+
+// Sums of K neighbouring segments' weights.
+template <int DT, int K>
+__device__ __forceinline__ void sum_segments(const Weights<DT>& W, int seg, int vocab, double (&s)[K]) {
+  constexpr int N = Weights<DT>::N;
+  double w[K * kRun];
+  W.template load<K * kRun / N>(seg * kSegment + (static_cast<int>(threadIdx.x) & 63) * N, kWave * N, vocab, (seg + K) * kSegment <= vocab, w);
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w == wave) before = total;
-    total += red[w];
+  for (int k = 0; k < K; ++k) {
+    s[k] = 0.0;
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) s[k] += w[k * kRun + e];
+    s[k] = wave_sum64(s[k]);
   }
-  return lane == 0 ? before : before + above;
+}
+
+// The token of segment seg that passes target, base the sum of the segments before; where none does (passes: whether
+// one is meant to), the last of positive weight. One wavefront.
+template <int DT>
+__device__ __forceinline__ int walk(const Weights<DT>& W, int seg, int vocab, double base, double target, bool passes) {
+  constexpr int N = Weights<DT>::N;
+  const int t0 = seg * kSegment + (static_cast<int>(threadIdx.x) & 63) * kRun;
+  double w[kRun], sum = 0.0, all;
+  W.template load<kRun / N>(t0, N, vocab, (seg + 1) * kSegment <= vocab, w);
+#pragma unroll
+  for (int e = 0; e < kRun; ++e) sum += w[e];
+  double c = base + sum_before(sum, all);
+  int first = -1, last = -1;
+#pragma unroll
+  for (int e = 0; e < kRun; ++e) {
+    c += w[e];
+    if (w[e] > 0.0) last = t0 + e;
+    if (first < 0 && w[e] > 0.0 && c > target) first = t0 + e;
+  }
+  const uint64_t passed = passes ? __ballot(first >= 0) : 0, left = __ballot(last >= 0);
+  return passed != 0 ? __shfl(first, __builtin_ctzll(passed), kWave) : __shfl(last, 63 - __builtin_clzll(left), kWave);
+}
+
+// The token drawn from target alone, where nothing is left of it: every segment is summed here. -1: none has a
+// positive weight.
+template <int DT>
+__device__ __noinline__ int pick_plain(const stor_t<DT>* p, int segments, int vocab, double draw) {
+  const Weights<DT> W{p, nullptr, -1};
+  double total = 0.0, s[1];
+  int last = -1;
+  for (int i = 0; i < segments; ++i) {
+    sum_segments<DT, 1>(W, i, vocab, s);
+    total += s[0];
+    if (s[0] > 0.0) last = i;
+  }
+  if (last < 0) return -1;
+  const double target = draw * total;
+  double c = 0.0;
+  for (int i = 0; i < segments; ++i) {
+    sum_segments<DT, 1>(W, i, vocab, s);
+    if (s[0] > 0.0 && c + s[0] > target) return walk<DT>(W, i, vocab, c, target, true);
+    c += s[0];
+  }
+  return walk<DT>(W, last, vocab, c, target, false);
+}
+
+// The token drawn, from the segments' sums: one wavefront.
+template <int DT>
+__device__ __forceinline__ int pick(const Weights<DT>& W, const double* sums, int segments, int vocab, double draw) {
+  const int lane = threadIdx.x & 63, per = (segments + kWave - 1) / kWave;
+  const int i0 = min(lane * per, segments), i1 = min(i0 + per, segments);
+  double total, mine = 0.0;
+  for (int i = i0; i < i1; ++i) mine += sums[i];
+  double c = sum_before(mine, total), base = 0.0;
+  if (!(total > 0.0)) return pick_plain<DT>(W.p, segments, vocab, draw);
+  const double target = draw * total;
+  // the first segment that passes the draw, else the last one of positive sum
+  int first = -1, last = -1;
+  for (int i = i0; i < i1; ++i) {
+    const double s = sums[i];
+    if (s > 0.0) last = i;
+    if (first < 0 && s > 0.0 && c + s > target) {
+      first = i;
+      base = c;
+    }
+    c += s;
+  }
+  const uint64_t hit = __ballot(first >= 0), some = __ballot(last >= 0);
+  const int at = hit != 0 ? __builtin_ctzll(hit) : 63 - __builtin_clzll(some);
+  const int seg = __shfl(hit != 0 ? first : last, at, kWave);
+  return walk<DT>(W, seg, vocab, __shfl(base, at, kWave), target, hit != 0);
+}
+
+// A request's results, by one wavefront. out may be drafts: what is read of them here is written by the same lane.
+__device__ __forceinline__ void finish(const VerifyArgs& A, int b, int64_t lo, int64_t hi, int64_t row, int token) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t r = lo + lane; r < hi; r += kWave) A.out[r] = r < row ? A.drafts[r] : (r == row ? token : -1);
+  if (lane == 0) A.counts[b] = static_cast<int32_t>(row - lo) + 1;
 }
 
 }  // namespace
 
+// A wavefront per kPair segments.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void k_verify_sums(const VerifyArgs A) {
-  __shared__ double red[2][kWaves];
-  const int seg = static_cast<int>(blockIdx.x % A.segments), b = static_cast<int>(blockIdx.x / A.segments);
+__global__ __launch_bounds__(kWaves* kWave) void k_verify_sums(const VerifyArgs A) {
+  const int groups = (A.segments + kWaves * kPair - 1) / (kWaves * kPair);
+  const int b = static_cast<int>(blockIdx.x / groups);
+  const int seg = (static_cast<int>(blockIdx.x % groups) * kWaves + static_cast<int>(threadIdx.x >> 6)) * kPair;
   int64_t lo, hi;
   sequence_rows(A.offsets, b, A.rows, lo, hi);
-  if (lo >= hi) return;
+  if (lo >= hi || seg >= A.segments) return;
   const int64_t row = first_refused<DT>(A, lo, hi);
-  if (seg == 0 && threadIdx.x == 0) A.kept[b] = static_cast<int32_t>(row - lo);
-  const Weights<DT> W = weights_at<DT>(A, row, hi);
-  constexpr int N = DT == 0 ? 4 : 8;
-  double s = 0.0, f = 0.0;
-#pragma unroll
-  for (int i = 0; i < kRun / N; ++i) {
-    double w[N], full[N];
-    W.load(seg * kSegment + (i * kThreads + static_cast<int>(threadIdx.x)) * N, A.vocab, w, full);
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      s += w[e];
-      f += full[e];
-    }
-  }
-  s = wave_sum64(s);
-  f = wave_sum64(f);
+  double s[kPair];
+  sum_segments<DT, kPair>(weights_at<DT>(A, row, hi), seg, A.vocab, s);
   if ((threadIdx.x & 63) == 0) {
-    red[0][threadIdx.x >> 6] = s;
-    red[1][threadIdx.x >> 6] = f;
-  }
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    const double* r = red[threadIdx.x];
-    A.sums[(static_cast<int64_t>(b) * A.segments + seg) * 2 + threadIdx.x] = (r[0] + r[1]) + (r[2] + r[3]);
+#pragma unroll
+    for (int k = 0; k < kPair; ++k)
+      if (seg + k < A.segments) A.sums[static_cast<int64_t>(b) * A.segments + seg + k] = s[k];
+    if (seg == 0) A.kept[b] = static_cast<int32_t>(row - lo);
   }
 }
 
-// A workgroup per request: the segment whose sums pass the draw, then the token in it.
+// A wavefront per request.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void k_verify_pick(const VerifyArgs A) {
-  constexpr int kNone = 0x7fffffff;
-  __shared__ double red[kWaves], start;
-  __shared__ int hit, last;  // the first of the segments or tokens that passes the draw, the last one of positive weight
-  const int b = blockIdx.x, tid = threadIdx.x;
+__global__ __launch_bounds__(kWave) void k_verify_pick(const VerifyArgs A) {
+  const int b = blockIdx.x;
+  const double draw = A.draws[b];
+  const int kept = A.kept[b];  // of a request without rows: anything
   int64_t lo, hi;
   sequence_rows(A.offsets, b, A.rows, lo, hi);
   if (lo >= hi) {
-    if (tid == 0) A.counts[b] = 0;
+    if (threadIdx.x == 0) A.counts[b] = 0;
     return;
   }
-  const int kept = A.kept[b];
-  Weights<DT> W = weights_at<DT>(A, lo + kept, hi);
-  const double* sums = A.sums + static_cast<int64_t>(b) * A.segments * 2;
-  const int per = (A.segments + kThreads - 1) / kThreads;
-  const int64_t i0 = static_cast<int64_t>(tid) * per, i1 = min(i0 + per, static_cast<int64_t>(A.segments));
-  if (tid == 0) {
-    hit = kNone;
-    last = -1;
-  }
-  double total = 0.0, c = 0.0;
-  int k = 0;
-  for (; k < 2; ++k) {  // where no weight is positive: target itself
-    double mine = 0.0;
-    for (int64_t i = i0; i < i1; ++i) mine += sums[2 * i + k];
-    c = sum_before(mine, red, total);
-    if (total > 0.0) break;
-  }
-  if (k == 1) {
-    W.q = nullptr;
-    W.x = -1;
-  }
-  int token = -1;
-  if (k < 2) {
-    const double target = static_cast<double>(A.draws[b]) * total;
-    int mine = kNone, positive = -1;
-    double base = 0.0;
-    for (int64_t i = i0; i < i1; ++i) {
-      const double s = sums[2 * i + k];
-      if (s > 0.0) positive = static_cast<int>(i);
-      if (mine == kNone && s > 0.0 && c + s > target) {
-        mine = static_cast<int>(i);
-        base = c;
-      }
-      c += s;
-    }
-    if (mine != kNone) atomicMin(&hit, mine);
-    if (positive >= 0) atomicMax(&last, positive);
-    __syncthreads();
-    const bool passed = hit != kNone;
-    const int seg = passed ? hit : last;
-    if (passed && mine == hit) start = base;
-    __syncthreads();
-    const double from = passed ? start : 0.0;
-    if (tid == 0) {
-      hit = kNone;
-      last = -1;
-    }
-    double w[kRun], full[kRun];
-    const int t0 = seg * kSegment + tid * kRun;
-    W.template load<kRun>(t0, A.vocab, w, full);
-    double sum = 0.0, all;
-#pragma unroll
-    for (int e = 0; e < kRun; ++e) sum += w[e];
-    c = from + sum_before(sum, red, all);
-    mine = kNone;
-    positive = -1;
-#pragma unroll
-    for (int e = 0; e < kRun; ++e) {
-      c += w[e];
-      if (w[e] > 0.0) positive = t0 + e;
-      if (mine == kNone && w[e] > 0.0 && c > target) mine = t0 + e;
-    }
-    if (passed && mine != kNone) atomicMin(&hit, mine);
-    if (positive >= 0) atomicMax(&last, positive);
-    __syncthreads();
-    token = hit != kNone ? hit : last;
-  }
-  const int64_t rows = hi - lo;
-  for (int64_t i = tid; i < rows; i += kThreads) A.out[lo + i] = i < kept ? A.drafts[lo + i] : (i == kept ? token : -1);
-  if (tid == 0) A.counts[b] = kept + 1;
+  const int64_t row = lo + kept;
+  const int token = pick<DT>(weights_at<DT>(A, row, hi), A.sums + static_cast<int64_t>(b) * A.segments, A.segments, A.vocab, draw);
+  finish(A, b, lo, hi, row, token);
 }
+
+// A workgroup per request, the sums in LDS.
+template <int DT>
+__global__ __launch_bounds__(kMany* kWave) void k_verify_whole(const VerifyArgs A) {
+  __shared__ double sums[kMost + kPair];
+  const int b = blockIdx.x, wave = threadIdx.x >> 6;
+  const double draw = A.draws[b];
+  int64_t lo, hi;
+  sequence_rows(A.offsets, b, A.rows, lo, hi);
+  if (lo >= hi) {
+    if (threadIdx.x == 0) A.counts[b] = 0;
+    return;
+  }
+  const int64_t row = first_refused<DT>(A, lo, hi);
+  const Weights<DT> W = weights_at<DT>(A, row, hi);
+  for (int seg = wave * kPair; seg < A.segments; seg += kMany * kPair) {
+    double s[kPair];
+    sum_segments<DT, kPair>(W, seg, A.vocab, s);
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int k = 0; k < kPair; ++k) sums[seg + k] = s[k];
+    }
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  finish(A, b, lo, hi, row, pick<DT>(W, sums, A.segments, A.vocab, draw));
+}
+
+namespace {
+
+template <int DT>
+hipError_t verify(const VerifyArgs& a, hipStream_t s) {
+  if (a.segments <= verify_alone()) {
+    k_verify_whole<DT><<<dim3(static_cast<unsigned>(a.batch)), dim3(kMany * kWave), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const int64_t groups = (a.segments + kWaves * kPair - 1) / (kWaves * kPair);
+  k_verify_sums<DT><<<dim3(static_cast<unsigned>(a.batch * groups)), dim3(kWaves * kWave), 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_verify_pick<DT><<<dim3(static_cast<unsigned>(a.batch)), dim3(kWave), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
 
 int32_t verify_segments(int32_t vocab) { return static_cast<int32_t>((static_cast<int64_t>(vocab) + kSegment - 1) / kSegment); }
 
+int32_t verify_alone() { return kMost; }
+
 hipError_t launch_verify(int32_t io_dtype, const VerifyArgs& a, hipStream_t s) {
-  const dim3 sums(static_cast<unsigned>(static_cast<int64_t>(a.batch) * a.segments)), pick(static_cast<unsigned>(a.batch)), threads(kThreads);
-  if (io_dtype == SEED_BF16) k_verify_sums<1><<<sums, threads, 0, s>>>(a);
-  else k_verify_sums<0><<<sums, threads, 0, s>>>(a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (io_dtype == SEED_BF16) k_verify_pick<1><<<pick, threads, 0, s>>>(a);
-  else k_verify_pick<0><<<pick, threads, 0, s>>>(a);
-  return hipGetLastError();
+  return io_dtype == SEED_BF16 ? verify<1>(a, s) : verify<0>(a, s);
 }
 
 }  // namespace seed

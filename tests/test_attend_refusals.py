@@ -196,8 +196,7 @@ def test_attend_workspace():
     one = _tokens(r, n=1, offsets=None)
     how = r.seed_attend(1, 1 << 18, 0, 0.1)
     need = r.LIB.seed_attend_workspace_bytes(ctypes.byref(long), ctypes.byref(one), ctypes.byref(how))
-    # a few parts for each row and head, of a row's fp32 values, a maximum and a sum
-    assert need > 0 and need % (4 * (128 + 2) * 4) == 0
+    assert 0 < need < 1 << 28  # does not grow with the cache
     for bad in (dict(ws=None), dict(size=need - 1), dict(ws=None, size=need)):
         assert _attend(r, long, one, length=1 << 18, **bad) == r.SEED_ERR_WORKSPACE, bad
     for ws in (6 * FAR + 4, BASE, FAR + 16, 16 * FAR, 8 * FAR - 64):
@@ -211,7 +210,7 @@ def test_attend_workspace():
 
 # ---- verification ---------------------------------------------------------------------------------
 
-def _verify(r, batch=3, vocab=1000, io=None, n=8, offsets=2 * FAR, tstride=1000, dstride=1000, target=BASE, draft=4 * FAR,
+def _verify(r, batch=3, vocab=500000, io=None, n=8, offsets=2 * FAR, tstride=500000, dstride=500000, target=BASE, draft=4 * FAR,
             drafts=5 * FAR, uniforms=6 * FAR, draws=7 * FAR, out=8 * FAR, counts=9 * FAR, ws=10 * FAR, size=1 << 30):
     d = r.seed_drafts(batch, vocab, r.SEED_F32 if io is None else io, n, offsets, tstride, dstride)
     return r.LIB.seed_verify_drafts(ctypes.byref(d), target, draft, drafts, uniforms, draws, out, counts, ws, size, None)
@@ -221,7 +220,7 @@ def test_verify():
     r = _lib()
     arg, un = r.SEED_ERR_ARG, r.SEED_ERR_UNSUPPORTED
     assert r.LIB.seed_verify_drafts(None, *[BASE] * 8, 0, None) == arg
-    for bad in (dict(batch=0), dict(vocab=0), dict(n=-1), dict(io=9), dict(offsets=None), dict(tstride=999), dict(dstride=999),
+    for bad in (dict(batch=0), dict(vocab=0), dict(n=-1), dict(io=9), dict(offsets=None), dict(tstride=499999), dict(dstride=499999),
                 dict(target=None), dict(drafts=None), dict(uniforms=None), dict(draws=None), dict(out=None), dict(counts=None),
                 dict(target=BASE + 2), dict(draft=4 * FAR + 1), dict(offsets=2 * FAR + 2), dict(drafts=5 * FAR + 1), dict(out=8 * FAR + 2),
                 dict(counts=9 * FAR + 3), dict(ws=10 * FAR + 8),
@@ -233,11 +232,11 @@ def test_verify():
     assert _verify(r, n=1 << 31) == un
     assert _verify(r, batch=1 << 20, vocab=1 << 20) == un
     assert _verify(r, n=(1 << 31) - 1, tstride=1 << 40) == un
-    need = r.seed_verify_workspace_bytes(3, 1000)
-    assert need > 0
+    need = r.seed_verify_workspace_bytes(3, 500000)
+    assert need > 0 and r.seed_verify_workspace_bytes(3, 1000) == 0  # small ones are done in one launch
     for bad in (dict(ws=None), dict(size=need - 1)):
         assert _verify(r, **bad) == r.SEED_ERR_WORKSPACE
-    assert r.seed_verify_workspace_bytes(0, 1000) == 0
+    assert r.seed_verify_workspace_bytes(0, 500000) == 0
 
 
 def test_wrappers_refuse_wrong_tensors():
