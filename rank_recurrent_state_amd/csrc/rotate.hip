@@ -1,9 +1,10 @@
 // Rotary positions of packed rows, and new keys and values stored into a paged cache:
 //   (a, b) <- amplitude (a cos - b sin, a sin + b cos), the angle 2 pi frac(position turns_i).
 //
-// What bounds it: every value is read once and written once, so HBM. A thread owns some neighbouring pairs of
-// a token, forms their sines once (the angle in fp64: a position of 10^6 times a frequency of 1 loses 0.06
-// in fp32) and applies them to one head after another; the fewer tokens, the more threads share a token's heads.
+// What bounds it: every value is read once and written once, so HBM. A workgroup takes a few tokens: a thread forms
+// the sine and cosine of one angle (fp64: a position of 10^6 times a frequency of 1 loses 0.06 in fp32) and leaves
+// them in LDS, and all run over the tokens' heads as they lie, twice 16 bytes each a time. Heads, rotated parts or
+// addresses that do not divide so go value by value.
 #include "attend.hpp"
 #include "common.hpp"
 
@@ -12,206 +13,360 @@ namespace seed {
 namespace {
 
 constexpr int kThreads = 256;
+using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
 
-// The pairs of VEC neighbouring angles: values [0, VEC) and [VEC, 2 VEC) of an item. In halves they are two
-// accesses rot / 2 apart; interleaved they are one run of 2 VEC values.
+// The sine and cosine of a pair's angle, times the amplitude. fp32 rows: in fp64, rounded once.
+template <int DT>
+__device__ __forceinline__ float2 turn_of(double turns, int64_t position, float amplitude) {
+  double t = turns * static_cast<double>(position);
+  t -= rint(t);
+  if constexpr (DT == 0) {
+    double sn, cs;
+    sincospi(2.0 * t, &sn, &cs);
+    return make_float2(static_cast<float>(amplitude * cs), static_cast<float>(amplitude * sn));
+  } else {
+    float sn, cs;
+    sincospif(2.f * static_cast<float>(t), &sn, &cs);
+    return make_float2(amplitude * cs, amplitude * sn);
+  }
+}
+
+// 16 bytes as VEC floats, and back.
 template <int DT, int VEC>
-struct Pairs {
-  float c[VEC], s[VEC];
-  __device__ __forceinline__ void angles(const double* __restrict__ turns, int i, int64_t position, float amplitude) {
+__device__ __forceinline__ void unpack(const u32x4& x, float (&v)[VEC]) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      double t = turns[i + e] * static_cast<double>(position);
-      t -= rint(t);
-      float sn, cs;
-      sincospif(2.f * static_cast<float>(t), &sn, &cs);
-      c[e] = amplitude * cs;
-      s[e] = amplitude * sn;
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (DT == 0) {
+      v[e] = __uint_as_float(x[e]);
+    } else {
+      v[2 * e] = lo16<DT>(x[e]);
+      v[2 * e + 1] = hi16<DT>(x[e]);
     }
   }
-  __device__ __forceinline__ void turn(const stor_t<DT>* __restrict__ x, stor_t<DT>* __restrict__ y, int i, int rot,
-                                       int interleaved) const {
-    float a[VEC], b[VEC], p[VEC], q[VEC];
-    const int at = interleaved ? 2 * i : i, to = interleaved ? 2 * i + VEC : i + rot / 2;
-    load_f32<DT, VEC>(x + at, a);
-    load_f32<DT, VEC>(x + to, b);
-    if (interleaved) {
-      if constexpr (VEC == 1) {
-        p[0] = a[0] * c[0] - b[0] * s[0];
-        q[0] = a[0] * s[0] + b[0] * c[0];
-      } else {
+}
+template <int DT, int VEC>
+__device__ __forceinline__ u32x4 pack(const float (&v)[VEC]) {
+  u32x4 x;
 #pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) {
-          p[2 * e] = a[2 * e] * c[e] - a[2 * e + 1] * s[e];
-          p[2 * e + 1] = a[2 * e] * s[e] + a[2 * e + 1] * c[e];
-          q[2 * e] = b[2 * e] * c[VEC / 2 + e] - b[2 * e + 1] * s[VEC / 2 + e];
-          q[2 * e + 1] = b[2 * e] * s[VEC / 2 + e] + b[2 * e + 1] * c[VEC / 2 + e];
-        }
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (DT == 0) x[e] = __float_as_uint(v[e]);
+    else x[e] = pack2<DT>(v[2 * e], v[2 * e + 1]);
+  }
+  return x;
+}
+
+// n over what `per` stands for (Cut).
+__device__ __forceinline__ int divide(int n, uint32_t per) { return per == 0 ? n : static_cast<int>(__umulhi(n, per)); }
+
+// An item of a head of `dim` values whose first `rot` are turned: 16 bytes of the first half of the turned values, or of
+// the rest, and the 16 bytes half of them further on, so that neighbouring threads write neighbouring bytes (32 bytes
+// in a row each take twice as long). Halved pairs meet as (a[e], b[e]); interleaved ones are neighbours inside a and b.
+template <int DT, int VEC>
+__device__ __forceinline__ void item_of_head(const stor_t<DT>* x, stor_t<DT>* y, const float2* cs, int item, int dim, int rot, int interleaved) {
+  const int turned = rot / (2 * VEC), half = item < turned ? rot / 2 : (dim - rot) / 2;
+  const int at = item < turned ? item * VEC : rot + (item - turned) * VEC;
+  u32x4 lo = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + at));
+  u32x4 hi = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + at + half));
+  if (item < turned) {
+    float a[VEC], b[VEC];
+    unpack<DT, VEC>(lo, a);
+    unpack<DT, VEC>(hi, b);
+    if (interleaved) {
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) {
+        const float2 p = cs[(at + e) / 2], q = cs[(at + half + e) / 2];
+        const float a0 = a[e], a1 = a[e + 1], b0 = b[e], b1 = b[e + 1];
+        a[e] = a0 * p.x - a1 * p.y;
+        a[e + 1] = a0 * p.y + a1 * p.x;
+        b[e] = b0 * q.x - b1 * q.y;
+        b[e + 1] = b0 * q.y + b1 * q.x;
       }
     } else {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        p[e] = a[e] * c[e] - b[e] * s[e];
-        q[e] = a[e] * s[e] + b[e] * c[e];
+        const float2 c = cs[at + e];
+        const float a0 = a[e], b0 = b[e];
+        a[e] = a0 * c.x - b0 * c.y;
+        b[e] = a0 * c.y + b0 * c.x;
       }
     }
-    store_f32<DT, VEC>(y + at, p);
-    store_f32<DT, VEC>(y + to, q);
+    lo = pack<DT, VEC>(a);
+    hi = pack<DT, VEC>(b);
   }
-};
-
-template <int DT, int VEC>
-__device__ __forceinline__ void copy(const stor_t<DT>* __restrict__ x, stor_t<DT>* __restrict__ y) {
-  if constexpr (VEC == 1) *y = *x;
-  else *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(x);
+  __builtin_nontemporal_store(lo, reinterpret_cast<u32x4*>(y + at));
+  __builtin_nontemporal_store(hi, reinterpret_cast<u32x4*>(y + at + half));
 }
+
+// Where a new token goes: its request's position, and the place of it in the cache (-1: not there).
+struct Place {
+  int64_t position, slot;
+  bool mine;  // of a request at all
+};
+__device__ __forceinline__ Place place_of(const CacheArgs& C, int64_t row, int b) {
+  Place p{0, -1, false};
+  if (b >= C.batch) return p;
+  int64_t lo, hi;
+  request_rows(C, b, lo, hi);
+  if (row < lo || row >= hi) return p;
+  p.mine = true;
+  p.position = static_cast<int64_t>(C.lengths[b]) - (hi - row);
+  const int64_t entry = p.position >> C.page_shift;
+  if (p.position < 0 || entry >= C.width) return p;
+  const int64_t number = C.table[static_cast<int64_t>(b) * C.width + entry];
+  if (number >= 0 && number < C.pages)
+    p.slot = number * C.page_stride + (p.position & ((int64_t{1} << C.page_shift) - 1)) * C.token_stride;
+  return p;
+}
+// The number of requests that end at or before row `first`, found by a whole wavefront.
+__device__ __forceinline__ int requests_before(const CacheArgs& C, int64_t first) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int b = 0;
+  for (int j = 0; j < C.batch; j += kWave)
+    b += __popcll(__ballot(j + lane < C.batch && C.offsets[min(j + lane, C.batch - 1) + 1] <= first));
+  return b;
+}
+__device__ __forceinline__ int request_of(const CacheArgs& C, int64_t row, int b) {
+  while (b < C.batch && C.offsets[b + 1] <= row) ++b;
+  return b;
+}
+
+constexpr int kMostTokens = 16;   // of a workgroup
+constexpr int kMostPairs = 2048;  // angles of a workgroup's tokens
 
 }  // namespace
 
-// Thread (token, part, item): item < rot / 2 / VEC turns VEC pairs, the ones behind copy VEC values of the rest;
-// heads part, part + parts, .. of the token.
-template <int DT, int VEC>
-__global__ __launch_bounds__(kThreads) void k_rotate_rows(const RotateArgs A, int items, int parts) {
+// tokens tokens of a workgroup (blockIdx.x), heads [blockIdx.y heads_each, ..): items runs of 2 VEC values each.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_rotate_rows(const RotateArgs A, int tokens, int heads_each, int items, uint32_t per_item,
+                                                          uint32_t per_token) {
+  using T = stor_t<DT>;
+  constexpr int VEC = DT == 0 ? 4 : 8;
+  __shared__ float2 cs[kMostPairs];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  const int pairs = A.rot / 2;
+  const int h0 = static_cast<int>(blockIdx.y) * heads_each, heads = min(heads_each, A.heads - h0);
+  const int rows = static_cast<int>(min(static_cast<int64_t>(tokens), A.rows - row0));
+  for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
+    const int t = i / pairs;
+    cs[i] = turn_of<DT>(A.turns[i - t * pairs], A.positions[row0 + t], A.amplitude);
+  }
+  __syncthreads();
+  const int n = rows * heads_each * items;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int t = divide(i, per_token), in_token = i - t * heads_each * items;
+    const int h = divide(in_token, per_item), item = in_token - h * items;
+    if (h >= heads) continue;
+    const int64_t head = static_cast<int64_t>(h0 + h) * A.dim;
+    item_of_head<DT, VEC>(static_cast<const T*>(A.x) + (row0 + t) * A.x_stride + head, static_cast<T*>(A.y) + (row0 + t) * A.y_stride + head,
+                          cs + t * pairs, item, A.dim, A.rot, A.interleaved);
+  }
+}
+
+// The same for the rows of seed_cache_append: of all heads of a token, the queries come first, then the keys, then the
+// values.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_cache_append(const AppendArgs A, int tokens, int heads_each, int items, uint32_t per_item,
+                                                           uint32_t per_token) {
+  using T = stor_t<DT>;
+  constexpr int VEC = DT == 0 ? 4 : 8;
+  __shared__ float2 cs[kMostPairs];
+  __shared__ Place places[kMostTokens];
+  const CacheArgs& C = A.c;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  const int pairs = A.rot / 2;
+  const int queries = A.q != nullptr ? C.heads : 0, all = queries + 2 * C.key_heads;
+  const int h0 = static_cast<int>(blockIdx.y) * heads_each, heads = min(heads_each, all - h0);
+  const int rows = static_cast<int>(min(static_cast<int64_t>(tokens), C.tokens - row0));
+  if (threadIdx.x < kWave) {
+    const int first = C.offsets != nullptr ? requests_before(C, row0) : 0;
+    if (static_cast<int>(threadIdx.x) < rows) {
+      const int64_t row = row0 + threadIdx.x;
+      places[threadIdx.x] = place_of(C, row, C.offsets != nullptr ? request_of(C, row, first) : static_cast<int>(row));
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
+    const int t = i / pairs;
+    cs[i] = turn_of<DT>(A.turns[i - t * pairs], places[t].position, A.amplitude);
+  }
+  __syncthreads();
+  const int n = rows * heads_each * items;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int t = divide(i, per_token), in_token = i - t * heads_each * items;
+    const int in_part = divide(in_token, per_item), item = in_token - in_part * items;
+    if (in_part >= heads) continue;
+    const Place p = places[t];
+    const int h = h0 + in_part, kh = h - queries, vh = kh - C.key_heads;
+    if (!p.mine || (kh >= 0 && p.slot < 0)) continue;
+    const int64_t row = row0 + t;
+    const T* x = kh < 0 ? static_cast<const T*>(A.q) + row * A.q_stride + static_cast<int64_t>(h) * C.dim
+                 : vh < 0 ? static_cast<const T*>(A.k) + row * A.k_stride + static_cast<int64_t>(kh) * C.dim
+                          : static_cast<const T*>(A.v) + row * A.v_stride + static_cast<int64_t>(vh) * C.dim;
+    T* y = kh < 0 ? static_cast<T*>(A.q_out) + row * A.o_stride + static_cast<int64_t>(h) * C.dim
+           : vh < 0 ? static_cast<T*>(C.k) + p.slot + kh * C.head_stride
+                    : static_cast<T*>(C.v) + p.slot + vh * C.head_stride;
+    item_of_head<DT, VEC>(x, y, cs + t * pairs, item, C.dim, vh < 0 ? A.rot : 0, A.interleaved);
+  }
+}
+
+// Value by value: a thread has one pair of a token, or one value of the rest, for heads part, part + parts, ..
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_rotate_values(const RotateArgs A, int items, int parts) {
   using T = stor_t<DT>;
   const int64_t all = A.rows * parts * items, step = static_cast<int64_t>(gridDim.x) * kThreads;
-  const int turned = A.rot / 2 / VEC;
+  const int pairs = A.rot / 2;
   for (int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; id < all; id += step) {
-    const int64_t group = id / items;
-    const int item = static_cast<int>(id - group * items);
-    const int64_t row = group / parts;
-    const int part = static_cast<int>(group - row * parts);
+    const int64_t group = id / items, row = group / parts;
+    const int item = static_cast<int>(id - group * items), part = static_cast<int>(group - row * parts);
     const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
     T* y = static_cast<T*>(A.y) + row * A.y_stride;
-    if (item < turned) {
-      Pairs<DT, VEC> pr;
-      pr.angles(A.turns, item * VEC, A.positions[row], A.amplitude);
+    if (item < pairs) {
+      const float2 c = turn_of<DT>(A.turns[item], A.positions[row], A.amplitude);
+      const int at = A.interleaved ? 2 * item : item, to = A.interleaved ? at + 1 : at + pairs;
       for (int h = part; h < A.heads; h += parts) {
-        const int64_t at = static_cast<int64_t>(h) * A.dim;
-        pr.turn(x + at, y + at, item * VEC, A.rot, A.interleaved);
+        const int64_t head = static_cast<int64_t>(h) * A.dim;
+        const float a = to_f32<DT>(x[head + at]), b = to_f32<DT>(x[head + to]);
+        y[head + at] = from_f32<DT>(a * c.x - b * c.y);
+        y[head + to] = from_f32<DT>(a * c.y + b * c.x);
       }
     } else {
-      const int i = A.rot + (item - turned) * VEC;
       for (int h = part; h < A.heads; h += parts) {
-        const int64_t at = static_cast<int64_t>(h) * A.dim + i;
-        copy<DT, VEC>(x + at, y + at);
+        const int64_t at = static_cast<int64_t>(h) * A.dim + pairs + item;
+        y[at] = x[at];
       }
     }
   }
 }
 
-// The same for the rows of seed_cache_append: heads 0 .. heads - 1 are the queries, then the keys, then the values.
-template <int DT, int VEC>
-__global__ __launch_bounds__(kThreads) void k_cache_append(const AppendArgs A, int items, int parts) {
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_append_values(const AppendArgs A, int items, int parts) {
   using T = stor_t<DT>;
   const CacheArgs& C = A.c;
   const int64_t all = C.tokens * parts * items, step = static_cast<int64_t>(gridDim.x) * kThreads;
-  const int turned = A.rot / 2 / VEC;
-  const int queries = A.q != nullptr ? C.heads : 0;
+  const int pairs = A.rot / 2, queries = A.q != nullptr ? C.heads : 0;
   const int lane = threadIdx.x & (kWave - 1);
   // whole wavefronts stay in the loop together: they look for their first row's request with all lanes
   for (int64_t id0 = static_cast<int64_t>(blockIdx.x) * kThreads + (threadIdx.x - lane); id0 < all; id0 += step) {
-    const int64_t id = id0 + lane;
-    const int64_t group = id / items;
-    const int item = static_cast<int>(id - group * items);
-    const int64_t row = group / parts;
-    const int part = static_cast<int>(group - row * parts);
-    int b = 0;
-    if (C.offsets == nullptr) {
-      b = static_cast<int>(row);
-    } else {  // the number of requests that end at or before the wavefront's first row, then on to this thread's
-      const int64_t first = id0 / items / parts;
-      for (int j = 0; j < C.batch; j += kWave)
-        b += __popcll(__ballot(j + lane < C.batch && C.offsets[min(j + lane, C.batch - 1) + 1] <= first));
-      while (b < C.batch && C.offsets[b + 1] <= row) ++b;
-    }
-    if (id >= all || b >= C.batch) continue;
-    int64_t lo, hi;
-    request_rows(C, b, lo, hi);
-    if (row < lo || row >= hi) continue;
-    const int64_t position = static_cast<int64_t>(C.lengths[b]) - (hi - row);
-    const int64_t entry = position >> C.page_shift;
-    int64_t number = -1;
-    if (position >= 0 && entry < C.width) number = C.table[static_cast<int64_t>(b) * C.width + entry];
-    const bool there = number >= 0 && number < C.pages;
-    const int64_t slot = there ? number * C.page_stride + (position & ((int64_t{1} << C.page_shift) - 1)) * C.token_stride : 0;
+    const int64_t id = id0 + lane, group = id / items, row = group / parts;
+    const int item = static_cast<int>(id - group * items), part = static_cast<int>(group - row * parts);
+    const int first = C.offsets != nullptr ? requests_before(C, id0 / items / parts) : 0;
+    if (id >= all) continue;
+    const Place p = place_of(C, row, C.offsets != nullptr ? request_of(C, row, first) : static_cast<int>(row));
+    if (!p.mine) continue;
     const T* q = static_cast<const T*>(A.q) + row * A.q_stride;
     const T* k = static_cast<const T*>(A.k) + row * A.k_stride;
     const T* v = static_cast<const T*>(A.v) + row * A.v_stride;
     T* qo = static_cast<T*>(A.q_out) + row * A.o_stride;
-    T* ko = static_cast<T*>(C.k) + slot;
-    T* vo = static_cast<T*>(C.v) + slot;
-    const int last = queries + (there ? C.key_heads : 0);
-    if (item < turned) {
-      Pairs<DT, VEC> pr;
-      pr.angles(A.turns, item * VEC, position, A.amplitude);
-      for (int h = part; h < last; h += parts) {
-        const int kh = h - queries;
-        const int64_t at = static_cast<int64_t>(kh < 0 ? h : kh) * C.dim;
-        pr.turn((kh < 0 ? q : k) + at, kh < 0 ? qo + at : ko + kh * C.head_stride, item * VEC, A.rot, A.interleaved);
-      }
-    } else {
-      const int i = A.rot + (item - turned) * VEC;
-      for (int h = part; h < last; h += parts) {
-        const int kh = h - queries;
-        const int64_t at = static_cast<int64_t>(kh < 0 ? h : kh) * C.dim + i;
-        copy<DT, VEC>((kh < 0 ? q : k) + at, kh < 0 ? qo + at : ko + kh * C.head_stride + i);
+    T* ko = static_cast<T*>(C.k) + p.slot;
+    T* vo = static_cast<T*>(C.v) + p.slot;
+    const int last = queries + (p.slot >= 0 ? C.key_heads : 0);
+    float2 c = make_float2(1.f, 0.f);
+    int at = pairs + item, to = at;
+    if (item < pairs) {
+      c = turn_of<DT>(A.turns[item], p.position, A.amplitude);
+      at = A.interleaved ? 2 * item : item;
+      to = A.interleaved ? at + 1 : at + pairs;
+    }
+    for (int h = part; h < last; h += parts) {
+      const int kh = h - queries;
+      const T* x = kh < 0 ? q + static_cast<int64_t>(h) * C.dim : k + static_cast<int64_t>(kh) * C.dim;
+      T* y = kh < 0 ? qo + static_cast<int64_t>(h) * C.dim : ko + kh * C.head_stride;
+      if (item < pairs) {
+        const float a = to_f32<DT>(x[at]), b = to_f32<DT>(x[to]);
+        y[at] = from_f32<DT>(a * c.x - b * c.y);
+        y[to] = from_f32<DT>(a * c.y + b * c.x);
+      } else {
+        y[at] = x[at];
       }
     }
-    if (there) {
+    if (p.slot >= 0) {
       for (int h = part; h < C.key_heads; h += parts)
-        for (int i = item * VEC; i < C.dim; i += items * VEC)
-          copy<DT, VEC>(v + static_cast<int64_t>(h) * C.dim + i, vo + h * C.head_stride + i);
+        for (int i = item; i < C.dim; i += items) vo[h * C.head_stride + i] = v[static_cast<int64_t>(h) * C.dim + i];
     }
   }
 }
 
 namespace {
 
-// Threads enough to fill the chip before a thread takes more than one head.
+// Value by value: threads enough to fill the chip before a thread takes more than one head.
 int parts_of(int64_t threads, int heads) {
   constexpr int64_t kFill = 256 * 1024;
   const int64_t p = threads > 0 ? (kFill + threads - 1) / threads : 1;
   return static_cast<int>(p < heads ? p : heads);
 }
 
-template <int DT, int VEC>
-hipError_t rotate(const RotateArgs& a, hipStream_t s) {
+// The launch over tokens whose heads divide into items: tokens of a workgroup, and heads of one where tokens are few.
+struct Cut {
+  int tokens, heads_each;
+  uint32_t per_item, per_token;  // 2^32 over what an index is divided by, rounded up (0 for 1): exact for products below 2^32
+  dim3 grid;
+};
+Cut cut(int64_t rows, int heads, int items, int pairs) {
+  Cut c;
+  c.tokens = 1;
+  c.heads_each = heads;
+  if (rows * heads * items >= int64_t{1} << 20) {  // enough for every compute unit
+    c.tokens = pairs > 0 ? kThreads / pairs : 4;
+    c.tokens = c.tokens < 1 ? 1 : c.tokens > kMostTokens ? kMostTokens : c.tokens;
+  } else if (items > 0) {
+    c.heads_each = (kThreads + items - 1) / items;
+    c.heads_each = c.heads_each < heads ? c.heads_each : heads;
+  }
+  const uint64_t each = static_cast<uint64_t>(c.heads_each) * items;
+  c.per_item = static_cast<uint32_t>((0xffffffffull + items) / items);
+  c.per_token = static_cast<uint32_t>((0xffffffffull + each) / each);
+  c.grid = dim3(static_cast<unsigned>((rows + c.tokens - 1) / c.tokens), static_cast<unsigned>((heads + c.heads_each - 1) / c.heads_each));
+  return c;
+}
+// Whether heads and their rotated part divide into items, and the launch's indexes stay small.
+bool whole(int64_t rows, int64_t heads, int dim, int rot, int vec) {
+  return dim % (2 * vec) == 0 && rot % (2 * vec) == 0 && rot / 2 <= kMostPairs && heads * dim <= 16384 && rows < (1 << 24);
+}
+
+template <int DT>
+hipError_t rotate(const RotateArgs& a, bool v, hipStream_t s) {
+  constexpr int VEC = DT == 0 ? 4 : 8;
   const bool in_place = a.x == a.y;
-  const int items = a.rot / 2 / VEC + (in_place ? 0 : (a.dim - a.rot) / VEC);
-  const int parts = parts_of(a.rows * items, a.heads);
-  const int64_t blocks = (a.rows * parts * items + kThreads - 1) / kThreads;
-  k_rotate_rows<DT, VEC><<<dim3(loop_blocks(blocks)), dim3(kThreads), 0, s>>>(a, items, parts);
+  if (v) {
+    const int items = (in_place ? a.rot : a.dim) / (2 * VEC);
+    const Cut c = cut(a.rows, a.heads, items, a.rot / 2);
+    k_rotate_rows<DT><<<c.grid, dim3(kThreads), 0, s>>>(a, c.tokens, c.heads_each, items, c.per_item, c.per_token);
+  } else {
+    const int items = in_place ? a.rot / 2 : a.dim - a.rot / 2, parts = parts_of(a.rows * items, a.heads);
+    k_rotate_values<DT><<<dim3(loop_blocks((a.rows * parts * items + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(a, items, parts);
+  }
   return hipGetLastError();
 }
 
-template <int DT, int VEC>
-hipError_t append(const AppendArgs& a, hipStream_t s) {
-  const int items = a.rot / 2 / VEC + (a.c.dim - a.rot) / VEC;
-  const int heads = (a.q != nullptr ? a.c.heads : 0) + a.c.key_heads;
-  const int parts = parts_of(a.c.tokens * items, heads);
-  const int64_t blocks = (a.c.tokens * parts * items + kThreads - 1) / kThreads;
-  k_cache_append<DT, VEC><<<dim3(loop_blocks(blocks)), dim3(kThreads), 0, s>>>(a, items, parts);
+template <int DT>
+hipError_t append(const AppendArgs& a, bool v, hipStream_t s) {
+  constexpr int VEC = DT == 0 ? 4 : 8;
+  const int queries = a.q != nullptr ? a.c.heads : 0;
+  if (v) {
+    const int items = a.c.dim / (2 * VEC);
+    const Cut c = cut(a.c.tokens, queries + 2 * a.c.key_heads, items, a.rot / 2);
+    k_cache_append<DT><<<c.grid, dim3(kThreads), 0, s>>>(a, c.tokens, c.heads_each, items, c.per_item, c.per_token);
+  } else {
+    const int items = a.c.dim - a.rot / 2, parts = parts_of(a.c.tokens * items, queries + a.c.key_heads);
+    k_append_values<DT><<<dim3(loop_blocks((a.c.tokens * parts * items + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(a, items, parts);
+  }
   return hipGetLastError();
 }
-
-// Whether heads and their rotated part divide into 16-byte accesses.
-bool whole(int dim, int rot, int vec) { return dim % vec == 0 && rot % (2 * vec) == 0; }
 
 }  // namespace
 
 hipError_t launch_rotate_rows(int32_t io_dtype, const RotateArgs& a, hipStream_t s) {
-  const int bytes = io_dtype == SEED_BF16 ? 2 : 4, vec = 16 / bytes;
-  const bool v = whole(a.dim, a.rot, vec) && rows_aligned16(a.x, a.x_stride, bytes) && rows_aligned16(a.y, a.y_stride, bytes);
-  if (io_dtype == SEED_BF16) return v ? rotate<1, 8>(a, s) : rotate<1, 1>(a, s);
-  return v ? rotate<0, 4>(a, s) : rotate<0, 1>(a, s);
+  const int bytes = io_dtype == SEED_BF16 ? 2 : 4;
+  const bool v = whole(a.rows, a.heads, a.dim, a.rot, 16 / bytes) && rows_aligned16(a.x, a.x_stride, bytes) && rows_aligned16(a.y, a.y_stride, bytes);
+  return io_dtype == SEED_BF16 ? rotate<1>(a, v, s) : rotate<0>(a, v, s);
 }
 
 hipError_t launch_cache_append(int32_t io_dtype, const AppendArgs& a, hipStream_t s) {
-  const int bytes = io_dtype == SEED_BF16 ? 2 : 4, vec = 16 / bytes;
-  bool v = whole(a.c.dim, a.rot, vec) && rows_aligned16(a.k, a.k_stride, bytes) && rows_aligned16(a.v, a.v_stride, bytes);
+  const int bytes = io_dtype == SEED_BF16 ? 2 : 4;
+  bool v = whole(a.c.tokens, (a.q != nullptr ? a.c.heads : 0) + 2 * static_cast<int64_t>(a.c.key_heads), a.c.dim, a.rot, 16 / bytes) &&
+           rows_aligned16(a.k, a.k_stride, bytes) && rows_aligned16(a.v, a.v_stride, bytes);
   if (a.q != nullptr) v = v && rows_aligned16(a.q, a.q_stride, bytes) && rows_aligned16(a.q_out, a.o_stride, bytes);
-  if (io_dtype == SEED_BF16) return v ? append<1, 8>(a, s) : append<1, 1>(a, s);
-  return v ? append<0, 4>(a, s) : append<0, 1>(a, s);
+  return io_dtype == SEED_BF16 ? append<1>(a, v, s) : append<0>(a, v, s);
 }
 
 }  // namespace seed
