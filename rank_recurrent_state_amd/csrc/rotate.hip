@@ -1,9 +1,9 @@
 // Rotary positions of packed rows, and new keys and values stored into a paged cache:
 //   (a, b) <- amplitude (a cos - b sin, a sin + b cos), the angle 2 pi frac(position turns_i).
 //
-// What bounds it: every value is read once and written once, so HBM. A workgroup takes a few tokens: a thread forms
-// the sine and cosine of one angle (fp64: a position of 10^6 times a frequency of 1 loses 0.06 in fp32) and leaves
-// them in LDS, and all run over the tokens' heads as they lie, twice 16 bytes each a time. Heads, rotated parts or
+// What bounds it: every value is read once and written once, so HBM. A workgroup takes a token: a thread forms the
+// sine and cosine of an angle (fp64: a position of 10^6 times a frequency of 1 loses 0.06 in fp32) and leaves
+// them in LDS, and all run over the token's heads as they lie, twice 16 bytes each a time. Heads, rotated parts or
 // addresses that do not divide so go value by value.
 #include "attend.hpp"
 #include "common.hpp"
@@ -61,41 +61,56 @@ __device__ __forceinline__ int divide(int n, uint32_t per) { return per == 0 ? n
 // An item of a head of `dim` values whose first `rot` are turned: 16 bytes of the first half of the turned values, or of
 // the rest, and the 16 bytes half of them further on, so that neighbouring threads write neighbouring bytes (32 bytes
 // in a row each take twice as long). Halved pairs meet as (a[e], b[e]); interleaved ones are neighbours inside a and b.
-template <int DT, int VEC>
-__device__ __forceinline__ void item_of_head(const stor_t<DT>* x, stor_t<DT>* y, const float2* cs, int item, int dim, int rot, int interleaved) {
-  const int turned = rot / (2 * VEC), half = item < turned ? rot / 2 : (dim - rot) / 2;
-  const int at = item < turned ? item * VEC : rot + (item - turned) * VEC;
-  u32x4 lo = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + at));
-  u32x4 hi = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + at + half));
-  if (item < turned) {
-    float a[VEC], b[VEC];
-    unpack<DT, VEC>(lo, a);
-    unpack<DT, VEC>(hi, b);
-    if (interleaved) {
-#pragma unroll
-      for (int e = 0; e < VEC; e += 2) {
-        const float2 p = cs[(at + e) / 2], q = cs[(at + half + e) / 2];
-        const float a0 = a[e], a1 = a[e + 1], b0 = b[e], b1 = b[e + 1];
-        a[e] = a0 * p.x - a1 * p.y;
-        a[e + 1] = a0 * p.y + a1 * p.x;
-        b[e] = b0 * q.x - b1 * q.y;
-        b[e + 1] = b0 * q.y + b1 * q.x;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float2 c = cs[at + e];
-        const float a0 = a[e], b0 = b[e];
-        a[e] = a0 * c.x - b0 * c.y;
-        b[e] = a0 * c.y + b0 * c.x;
-      }
-    }
-    lo = pack<DT, VEC>(a);
-    hi = pack<DT, VEC>(b);
+template <int DT>
+struct Item {
+  static constexpr int VEC = DT == 0 ? 4 : 8;
+  using T = stor_t<DT>;
+  u32x4 lo, hi;
+  T* y = nullptr;  // nullptr: no item
+  int at, half;
+  bool turned;
+  __device__ __forceinline__ void load(const T* x, T* to, int item, int dim, int rot) {
+    const int turns = rot / (2 * VEC);
+    turned = item < turns;
+    half = turned ? rot / 2 : (dim - rot) / 2;
+    at = turned ? item * VEC : rot + (item - turns) * VEC;
+    y = to;
+    lo = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + at));
+    hi = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + at + half));
   }
-  __builtin_nontemporal_store(lo, reinterpret_cast<u32x4*>(y + at));
-  __builtin_nontemporal_store(hi, reinterpret_cast<u32x4*>(y + at + half));
-}
+  __device__ __forceinline__ void finish(const float2* cs, int interleaved) {
+    if (y == nullptr) return;
+    if (turned) {
+      float a[VEC], b[VEC];
+      unpack<DT, VEC>(lo, a);
+      unpack<DT, VEC>(hi, b);
+      if (interleaved) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          const float2 p = cs[(at + e) / 2], q = cs[(at + half + e) / 2];
+          const float a0 = a[e], a1 = a[e + 1], b0 = b[e], b1 = b[e + 1];
+          a[e] = a0 * p.x - a1 * p.y;
+          a[e + 1] = a0 * p.y + a1 * p.x;
+          b[e] = b0 * q.x - b1 * q.y;
+          b[e + 1] = b0 * q.y + b1 * q.x;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float2 c = cs[at + e];
+          const float a0 = a[e], b0 = b[e];
+          a[e] = a0 * c.x - b0 * c.y;
+          b[e] = a0 * c.y + b0 * c.x;
+        }
+      }
+      lo = pack<DT, VEC>(a);
+      hi = pack<DT, VEC>(b);
+    }
+    __builtin_nontemporal_store(lo, reinterpret_cast<u32x4*>(y + at));
+    __builtin_nontemporal_store(hi, reinterpret_cast<u32x4*>(y + at + half));
+    y = nullptr;
+  }
+};
 
 // Where a new token goes: its request's position, and the place of it in the cache (-1: not there).
 struct Place {
@@ -130,82 +145,71 @@ __device__ __forceinline__ int request_of(const CacheArgs& C, int64_t row, int b
   return b;
 }
 
-constexpr int kMostTokens = 16;   // of a workgroup
-constexpr int kMostPairs = 2048;  // angles of a workgroup's tokens
+constexpr int kMostPairs = 2048;  // angles of a token
 
 }  // namespace
 
-// tokens tokens of a workgroup (blockIdx.x), heads [blockIdx.y heads_each, ..): items runs of 2 VEC values each.
+// A workgroup per token and heads_each of its heads (blockIdx.y), `items` items each. The first items are on their way
+// while the angles are formed. One token: with several, whose sines are formed together, 32768 rows x 40
+// heads take 112 us (two) to 132 (sixteen) in the place of 106.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void k_rotate_rows(const RotateArgs A, int tokens, int heads_each, int items, uint32_t per_item,
-                                                          uint32_t per_token) {
+__global__ __launch_bounds__(kThreads) void k_rotate_rows(const RotateArgs A, int heads_each, int items, uint32_t per_item) {
   using T = stor_t<DT>;
-  constexpr int VEC = DT == 0 ? 4 : 8;
   __shared__ float2 cs[kMostPairs];
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * tokens;
-  const int pairs = A.rot / 2;
-  const int h0 = static_cast<int>(blockIdx.y) * heads_each, heads = min(heads_each, A.heads - h0);
-  const int rows = static_cast<int>(min(static_cast<int64_t>(tokens), A.rows - row0));
-  for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
-    const int t = i / pairs;
-    cs[i] = turn_of<DT>(A.turns[i - t * pairs], A.positions[row0 + t], A.amplitude);
-  }
+  const int64_t row = blockIdx.x;
+  const int h0 = static_cast<int>(blockIdx.y) * heads_each, n = min(heads_each, A.heads - h0) * items;
+  const T* x = static_cast<const T*>(A.x) + row * A.x_stride + static_cast<int64_t>(h0) * A.dim;
+  T* y = static_cast<T*>(A.y) + row * A.y_stride + static_cast<int64_t>(h0) * A.dim;
+  Item<DT> it;
+  auto fetch = [&](int i) {
+    const int h = divide(i, per_item);
+    it.load(x + h * A.dim, y + h * A.dim, i - h * items, A.dim, A.rot);
+  };
+  if (static_cast<int>(threadIdx.x) < n) fetch(threadIdx.x);
+  const int position = A.positions[row];
+  for (int i = threadIdx.x; i < A.rot / 2; i += kThreads) cs[i] = turn_of<DT>(A.turns[i], position, A.amplitude);
   __syncthreads();
-  const int n = rows * heads_each * items;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int t = divide(i, per_token), in_token = i - t * heads_each * items;
-    const int h = divide(in_token, per_item), item = in_token - h * items;
-    if (h >= heads) continue;
-    const int64_t head = static_cast<int64_t>(h0 + h) * A.dim;
-    item_of_head<DT, VEC>(static_cast<const T*>(A.x) + (row0 + t) * A.x_stride + head, static_cast<T*>(A.y) + (row0 + t) * A.y_stride + head,
-                          cs + t * pairs, item, A.dim, A.rot, A.interleaved);
+  it.finish(cs, A.interleaved);
+  for (int i = threadIdx.x + kThreads; i < n; i += kThreads) {
+    fetch(i);
+    it.finish(cs, A.interleaved);
   }
 }
 
 // The same for the rows of seed_cache_append: of all heads of a token, the queries come first, then the keys, then the
 // values.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void k_cache_append(const AppendArgs A, int tokens, int heads_each, int items, uint32_t per_item,
-                                                           uint32_t per_token) {
+__global__ __launch_bounds__(kThreads) void k_cache_append(const AppendArgs A, int heads_each, int items, uint32_t per_item) {
   using T = stor_t<DT>;
-  constexpr int VEC = DT == 0 ? 4 : 8;
   __shared__ float2 cs[kMostPairs];
-  __shared__ Place places[kMostTokens];
   const CacheArgs& C = A.c;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * tokens;
-  const int pairs = A.rot / 2;
+  const int64_t row = blockIdx.x;
   const int queries = A.q != nullptr ? C.heads : 0, all = queries + 2 * C.key_heads;
-  const int h0 = static_cast<int>(blockIdx.y) * heads_each, heads = min(heads_each, all - h0);
-  const int rows = static_cast<int>(min(static_cast<int64_t>(tokens), C.tokens - row0));
-  if (threadIdx.x < kWave) {
-    const int first = C.offsets != nullptr ? requests_before(C, row0) : 0;
-    if (static_cast<int>(threadIdx.x) < rows) {
-      const int64_t row = row0 + threadIdx.x;
-      places[threadIdx.x] = place_of(C, row, C.offsets != nullptr ? request_of(C, row, first) : static_cast<int>(row));
-    }
-  }
+  const int h0 = static_cast<int>(blockIdx.y) * heads_each, n = min(heads_each, all - h0) * items;
+  const T* q = static_cast<const T*>(A.q) + row * A.q_stride;
+  const T* k = static_cast<const T*>(A.k) + row * A.k_stride;
+  const T* v = static_cast<const T*>(A.v) + row * A.v_stride;
+  // every wavefront for itself
+  const Place p = place_of(C, row, C.offsets != nullptr ? request_of(C, row, requests_before(C, row)) : static_cast<int>(row));
+  if (!p.mine) return;
+  T* qo = static_cast<T*>(A.q_out) + row * A.o_stride;
+  T* ko = static_cast<T*>(C.k) + p.slot;
+  T* vo = static_cast<T*>(C.v) + p.slot;
+  Item<DT> it;
+  auto fetch = [&](int i) {
+    const int part = divide(i, per_item), item = i - part * items, h = h0 + part, kh = h - queries, vh = kh - C.key_heads;
+    if (kh < 0) it.load(q + static_cast<int64_t>(h) * C.dim, qo + static_cast<int64_t>(h) * C.dim, item, C.dim, A.rot);
+    else if (p.slot < 0) return;
+    else if (vh < 0) it.load(k + static_cast<int64_t>(kh) * C.dim, ko + kh * C.head_stride, item, C.dim, A.rot);
+    else it.load(v + static_cast<int64_t>(vh) * C.dim, vo + vh * C.head_stride, item, C.dim, 0);
+  };
+  if (static_cast<int>(threadIdx.x) < n) fetch(threadIdx.x);
+  for (int i = threadIdx.x; i < A.rot / 2; i += kThreads) cs[i] = turn_of<DT>(A.turns[i], p.position, A.amplitude);
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
-    const int t = i / pairs;
-    cs[i] = turn_of<DT>(A.turns[i - t * pairs], places[t].position, A.amplitude);
-  }
-  __syncthreads();
-  const int n = rows * heads_each * items;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int t = divide(i, per_token), in_token = i - t * heads_each * items;
-    const int in_part = divide(in_token, per_item), item = in_token - in_part * items;
-    if (in_part >= heads) continue;
-    const Place p = places[t];
-    const int h = h0 + in_part, kh = h - queries, vh = kh - C.key_heads;
-    if (!p.mine || (kh >= 0 && p.slot < 0)) continue;
-    const int64_t row = row0 + t;
-    const T* x = kh < 0 ? static_cast<const T*>(A.q) + row * A.q_stride + static_cast<int64_t>(h) * C.dim
-                 : vh < 0 ? static_cast<const T*>(A.k) + row * A.k_stride + static_cast<int64_t>(kh) * C.dim
-                          : static_cast<const T*>(A.v) + row * A.v_stride + static_cast<int64_t>(vh) * C.dim;
-    T* y = kh < 0 ? static_cast<T*>(A.q_out) + row * A.o_stride + static_cast<int64_t>(h) * C.dim
-           : vh < 0 ? static_cast<T*>(C.k) + p.slot + kh * C.head_stride
-                    : static_cast<T*>(C.v) + p.slot + vh * C.head_stride;
-    item_of_head<DT, VEC>(x, y, cs + t * pairs, item, C.dim, vh < 0 ? A.rot : 0, A.interleaved);
+  it.finish(cs, A.interleaved);
+  for (int i = threadIdx.x + kThreads; i < n; i += kThreads) {
+    fetch(i);
+    it.finish(cs, A.interleaved);
   }
 }
 
@@ -295,27 +299,21 @@ int parts_of(int64_t threads, int heads) {
   return static_cast<int>(p < heads ? p : heads);
 }
 
-// The launch over tokens whose heads divide into items: tokens of a workgroup, and heads of one where tokens are few.
+// The launch over tokens whose heads divide into items: the heads of a workgroup, all but where tokens are few.
 struct Cut {
-  int tokens, heads_each;
-  uint32_t per_item, per_token;  // 2^32 over what an index is divided by, rounded up (0 for 1): exact for products below 2^32
+  int heads_each;
+  uint32_t per_item;  // 2^32 over items, rounded up (0 for 1): exact for indexes below 2^32 / items
   dim3 grid;
 };
-Cut cut(int64_t rows, int heads, int items, int pairs) {
+Cut cut(int64_t rows, int heads, int items) {
   Cut c;
-  c.tokens = 1;
   c.heads_each = heads;
-  if (rows * heads * items >= int64_t{1} << 20) {  // enough for every compute unit
-    c.tokens = pairs > 0 ? kThreads / pairs : 4;
-    c.tokens = c.tokens < 1 ? 1 : c.tokens > kMostTokens ? kMostTokens : c.tokens;
-  } else if (items > 0) {
+  if (rows < 2048) {  // a turn of the threads each
     c.heads_each = (kThreads + items - 1) / items;
     c.heads_each = c.heads_each < heads ? c.heads_each : heads;
   }
-  const uint64_t each = static_cast<uint64_t>(c.heads_each) * items;
   c.per_item = static_cast<uint32_t>((0xffffffffull + items) / items);
-  c.per_token = static_cast<uint32_t>((0xffffffffull + each) / each);
-  c.grid = dim3(static_cast<unsigned>((rows + c.tokens - 1) / c.tokens), static_cast<unsigned>((heads + c.heads_each - 1) / c.heads_each));
+  c.grid = dim3(static_cast<unsigned>(rows), static_cast<unsigned>((heads + c.heads_each - 1) / c.heads_each));
   return c;
 }
 // Whether heads and their rotated part divide into items, and the launch's indexes stay small.
@@ -329,8 +327,8 @@ hipError_t rotate(const RotateArgs& a, bool v, hipStream_t s) {
   const bool in_place = a.x == a.y;
   if (v) {
     const int items = (in_place ? a.rot : a.dim) / (2 * VEC);
-    const Cut c = cut(a.rows, a.heads, items, a.rot / 2);
-    k_rotate_rows<DT><<<c.grid, dim3(kThreads), 0, s>>>(a, c.tokens, c.heads_each, items, c.per_item, c.per_token);
+    const Cut c = cut(a.rows, a.heads, items);
+    k_rotate_rows<DT><<<c.grid, dim3(kThreads), 0, s>>>(a, c.heads_each, items, c.per_item);
   } else {
     const int items = in_place ? a.rot / 2 : a.dim - a.rot / 2, parts = parts_of(a.rows * items, a.heads);
     k_rotate_values<DT><<<dim3(loop_blocks((a.rows * parts * items + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(a, items, parts);
@@ -344,8 +342,8 @@ hipError_t append(const AppendArgs& a, bool v, hipStream_t s) {
   const int queries = a.q != nullptr ? a.c.heads : 0;
   if (v) {
     const int items = a.c.dim / (2 * VEC);
-    const Cut c = cut(a.c.tokens, queries + 2 * a.c.key_heads, items, a.rot / 2);
-    k_cache_append<DT><<<c.grid, dim3(kThreads), 0, s>>>(a, c.tokens, c.heads_each, items, c.per_item, c.per_token);
+    const Cut c = cut(a.c.tokens, queries + 2 * a.c.key_heads, items);
+    k_cache_append<DT><<<c.grid, dim3(kThreads), 0, s>>>(a, c.heads_each, items, c.per_item);
   } else {
     const int items = a.c.dim - a.rot / 2, parts = parts_of(a.c.tokens * items, queries + a.c.key_heads);
     k_append_values<DT><<<dim3(loop_blocks((a.c.tokens * parts * items + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(a, items, parts);
