@@ -567,14 +567,16 @@ def seed_dense_decode_step(shape: seed_shape, S, q, k, v, beta, g, o, stream=Non
 
 _IO = None  # (torch, {io code: dtype})
 _RAW_STREAM = None  # device index -> its current stream's handle
+_DEVICE = None  # () -> the current device's index
 
 
 def _io():
-    global _IO, _RAW_STREAM
+    global _IO, _RAW_STREAM, _DEVICE
     if _IO is None:
         import torch
         _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream",  # without a Stream object around it
                               lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # its tensors have brought up the GPU
         _IO = (torch, {SEED_F32: torch.float32, SEED_BF16: torch.bfloat16, SEED_F16: torch.float16})
     return _IO
 
@@ -646,21 +648,21 @@ class _Args:
         if ws is None and need > 0:
             # made on the stream that uses it, so that its memory's next use is ordered behind
             torch = self.torch
-            if stream is None and self.device == torch.cuda.current_device():
+            if stream is None and self.device == _DEVICE():
                 ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             else:
                 on = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
                 with torch.cuda.device(self.device), torch.cuda.stream(on):
                     ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            return ws.data_ptr(), need, ws
         if ws is None:
             return None, 0, None
         return self.dense("ws", ws, ws.numel(), ws.dtype), ws.numel() * ws.element_size(), ws
 
     def launch(self, fn_name, stream, *args):
         """Calls the entry point on the tensors' device, with its current stream unless one is given."""
-        cuda = self.torch.cuda
-        if self.device >= 0 and self.device != cuda.current_device():
-            with cuda.device(self.device):
+        if self.device >= 0 and self.device != _DEVICE():
+            with self.torch.cuda.device(self.device):
                 self._call(fn_name, stream, args)
         else:
             self._call(fn_name, stream, args)
@@ -843,12 +845,7 @@ class Cache:
         self.c = seed_cache(table.shape[0], heads, dim, code, page, table.shape[1], pages, p, s, h, k.data_ptr(), v.data_ptr(),
                             table.data_ptr())
         self.ref = ctypes.byref(self.c)
-
-
-def _attention_rows(x, name, heads, dim):
-    if x.dim() != 3 or x.shape[2] != dim or (heads is not None and x.shape[1] != heads):
-        raise ValueError(f"{name}: expected [tokens, {'heads' if heads is None else heads}, {dim}], got {tuple(x.shape)}")
-    return x.shape
+        self.need = {}  # workspace bytes of its calls, by their sizes
 
 
 def seed_rotate_rows(rotary: Rotary, x, positions, y, stream=None) -> None:
@@ -878,26 +875,31 @@ def seed_cache_append(cache: Cache, lengths, k, v, offsets=None, rotary: Rotary 
     torch, _ = _io()
     c, i32 = cache.c, torch.int32
     a, dt, dim, kh = _Args(torch), cache.dtype, c.dim, c.key_heads
-    a._on("cache", cache.k)
-    ks = _attention_rows(k, "k", kh, dim)
-    n = ks[0]
+    a.device = cache.device
+    n = k.shape[0]
+    ks = (n, kh, dim)
     kp, k_stride = a.rows("k", k, ks, kh * dim, dt)
     vp, v_stride = a.rows("v", v, ks, kh * dim, dt)
     heads, qp, op, q_stride, o_stride = 0, None, None, 0, 0
     if q is not None:
-        heads = _attention_rows(q, "q", None, dim)[1]
-        qp, q_stride = a.rows("q", q, (n, heads, dim), heads * dim, dt)
+        if q.dim() != 3:
+            raise ValueError(f"q: expected [tokens, heads, dim], got {tuple(q.shape)}")
+        heads = q.shape[1]
+        qs = (n, heads, dim)
+        qp, q_stride = a.rows("q", q, qs, heads * dim, dt)
         if q_out is None:
             raise ValueError("q_out: expected a tensor for the queries")
-        op, o_stride = a.rows("q_out", q_out, (n, heads, dim), heads * dim, dt)
+        op, o_stride = a.rows("q_out", q_out, qs, heads * dim, dt)
     elif q_out is not None:
         raise ValueError("q: expected the queries of q_out")
+    turn = None
     if rotary is not None:
-        a._on("rotary", rotary.turns)
+        if rotary.turns.get_device() != a.device:
+            a._on("rotary", rotary.turns)
+        turn = ctypes.byref(rotary.c)
     new = seed_tokens(n, a.dense("offsets", offsets, c.batch + 1, i32), a.dense("lengths", lengths, c.batch, i32), heads,
                       q_stride, k_stride, v_stride, o_stride)
-    a.launch("seed_cache_append", stream, cache.ref, ctypes.byref(new), None if rotary is None else ctypes.byref(rotary.c),
-             qp, kp, vp, op)
+    a.launch("seed_cache_append", stream, cache.ref, ctypes.byref(new), turn, qp, kp, vp, op)
 
 
 def seed_attend_workspace_bytes(cache: Cache, tokens: int, heads: int, max_tokens: int = 1, max_length: int | None = None,
@@ -920,17 +922,27 @@ def seed_decode_attend(cache: Cache, lengths, q, o, offsets=None, max_tokens: in
     torch, _ = _io()
     c, i32 = cache.c, torch.int32
     a, dt, dim = _Args(torch), cache.dtype, c.dim
-    a._on("cache", cache.k)
-    shape = _attention_rows(q, "q", None, dim)
+    a.device = cache.device
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError(f"q: expected [tokens, heads, {dim}], got {tuple(shape)}")
     n, heads = shape[0], shape[1]
     qp, q_stride = a.rows("q", q, shape, heads * dim, dt)
     op, o_stride = a.rows("o", o, shape, heads * dim, dt)
     new = ctypes.byref(seed_tokens(n, a.dense("offsets", offsets, c.batch + 1, i32), a.dense("lengths", lengths, c.batch, i32),
                                    heads, q_stride, 0, 0, o_stride))
-    how = ctypes.byref(seed_attend(max_tokens, c.page * c.width if max_length is None else max_length, window,
-                                   dim ** -0.5 if scale is None else scale))
+    if max_length is None:
+        max_length = c.page * c.width
+    how = ctypes.byref(seed_attend(max_tokens, max_length, window, dim ** -0.5 if scale is None else scale))
     lp = a.dense("lse", lse, n * heads, torch.float32)
-    need = LIB.seed_attend_workspace_bytes(cache.ref, new, how) if ws is None else 0
+    need = 0
+    if ws is None:
+        key = (n, heads, max_tokens, max_length, window, offsets is None)
+        need = cache.need.get(key)
+        if need is None:
+            if len(cache.need) >= 1024:  # a serving loop's ever new sizes
+                cache.need.clear()
+            need = cache.need[key] = LIB.seed_attend_workspace_bytes(cache.ref, new, how)
     wp, size, ws = a.workspace(need, ws, stream)
     a.launch("seed_decode_attend", stream, cache.ref, new, how, qp, op, lp, wp, size)
 
