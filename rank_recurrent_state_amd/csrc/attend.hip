@@ -168,7 +168,10 @@ struct Shared {
   // A wavefront's keys (RW = 1), or all wavefronts' keys and values, twice; at the end the accumulators.
   static constexpr int kJoin = NW * GT * kWave * 16, kTiles = RW == 1 ? NW * L::kTile : 4 * L::kTile;
   __attribute__((aligned(16))) char tiles[kJoin > kTiles ? kJoin : kTiles];
-  float weights[NW][L::kKeys * 16];
+  // 16-bit queries of 256 values (RW = 1): in registers they leave too few for the loads
+  static constexpr bool kQueries = DT != 0 && D == 256 && RW == 1;
+  u32x4 q[kQueries ? L::kQ : 1][kQueries ? kWave : 1];
+  float weights[RW == 1 ? 1 : NW][RW == 1 ? 1 : L::kKeys * 16];  // RW = 1: in the place of a wavefront's keys
   float stat[NW][16][2];
 };
 
@@ -202,6 +205,14 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
   }
 #pragma unroll
   for (int c = 0; c < L::kQ; ++c) Q[c] ^= A.negate;
+  constexpr bool kQueries = Shared<DT, D, RW, NW>::kQueries;
+  if constexpr (kQueries) {
+    if (wave == 0) {
+#pragma unroll
+      for (int c = 0; c < L::kQ; ++c) sm.q[c][lane] = Q[c];
+    }
+    __syncthreads();
+  }
 
   f32x4 O[L::kOut];
   float m = kNegInf, l = 0.f;
@@ -321,12 +332,13 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
 #pragma unroll
       for (int c = 0; c < L::kQ; ++c) {
         const u32x4 k = *reinterpret_cast<const u32x4*>(keys + L::piece(16 * u + l16, 4 * c + g));
+        const u32x4 q = kQueries ? sm.q[kQueries ? c : 0][kQueries ? lane : 0] : Q[c];
         if constexpr (DT == 0) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            S[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[e]), __uint_as_float(Q[c][e]), S[u], 0, 0, 0);
+            S[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[e]), __uint_as_float(q[e]), S[u], 0, 0, 0);
         } else {
-          S[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k), __builtin_bit_cast(bf16x8, Q[c]), S[u], 0, 0, 0);
+          S[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k), __builtin_bit_cast(bf16x8, q), S[u], 0, 0, 0);
         }
       }
     }
@@ -419,12 +431,12 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
 #pragma unroll
         for (int e = 0; e < L::kWords; ++e) most = largest<DT>(most, V[i][c][e]);
     const bool odd = __any(not_finite<DT>(most));
+    float* weights = RW == 1 ? reinterpret_cast<float*>(keys) : sm.weights[RW == 1 ? 0 : wave];  // [key][row]
     if (__builtin_expect(odd, 0)) {
-      float* mine = sm.weights[wave];  // [key][row]
       wave_lds_sync();
 #pragma unroll
       for (int i = 0; i < 4 * L::kSub; ++i) {
-        mine[(16 * (i / 4) + 4 * g + i % 4) * 16 + l16] = P[i];
+        weights[(16 * (i / 4) + 4 * g + i % 4) * 16 + l16] = P[i];
 #pragma unroll
         for (int c = 0; c < L::VC; ++c)
 #pragma unroll
@@ -444,7 +456,7 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
         const int64_t at = k < 16 ? here.at[0] : here.at[last];
         const bool seen = page && key <= pos && (A.window <= 0 || key > pos - A.window);
         if (!seen) continue;
-        const float p = sm.weights[wave][k * 16 + l16];
+        const float p = weights[k * 16 + l16];
         const char* base = vb + at + k % 16 * ts;
 #pragma unroll
         for (int c = 0; c < L::VC; ++c)
