@@ -151,11 +151,10 @@ struct Tile {
   static constexpr int kLine = kRow / 16;             // lanes that load a row of 16 bytes each,
   static constexpr int kAtOnce = kWave / kLine;       // and rows of one load
   static constexpr int kTile = kKeys * kRow;
-  // Where LDS holds 16-byte piece c of key r: the pieces of a row trade places so that 16 rows' pieces of one
-  // number lie in different banks.
-  static __device__ __forceinline__ uint32_t piece(int r, int c) {
-    return r * kRow + ((c ^ (kLine == 8 ? (r >> 1) & 7 : r & 15)) << 4);
-  }
+  // LDS holds 16-byte piece c of key r at r kRow + 16 (c ^ swap(r)): pieces trade places so that 16 rows' pieces of one
+  // number lie in different banks. swap(r + s) = swap(r) ^ swap(s) where r is a multiple of kAtOnce and s below it,
+  // or r of 16: a place is one exclusive or away from a lane's first.
+  static __device__ __forceinline__ constexpr uint32_t swap(int r) { return kLine == 8 ? (r >> 1) & 7 : r & 15; }
 };
 
 }  // namespace
@@ -300,6 +299,7 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
     load_rows(kb, here, K);
     if constexpr (RW > 1) load_rows(vb, here, Vr);
   }
+  const uint32_t write_at = my_row * L::kRow + ((my_piece ^ L::swap(my_row)) << 4), read_at = l16 * L::kRow + ((g ^ L::swap(l16)) << 4);
   Pages ahead{};  // of the next turn: looked up a turn ahead too
   if (from < to) ahead = look_up(start + kTurn);
   int turn = 0;
@@ -308,11 +308,13 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
     turn ^= 1;
     if constexpr (RW == 1) load_v(here);
     __builtin_amdgcn_sched_barrier(0);
+    uint32_t write = write_at, read = read_at;  // the places follow from these, and need no registers between turns
+    asm volatile("" : "+v"(write), "+v"(read));
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int row = (i * RW + share_of) * L::kAtOnce + my_row;
-      *reinterpret_cast<u32x4*>(keys + L::piece(row, my_piece)) = K[i];
-      if constexpr (RW > 1) *reinterpret_cast<u32x4*>(keys + L::kTile + row * L::kRow + my_piece * 16) = Vr[i];
+      const int first = (i * RW + share_of) * L::kAtOnce;
+      *reinterpret_cast<u32x4*>(keys + first * L::kRow + (write ^ (L::swap(first) << 4))) = K[i];
+      if constexpr (RW > 1) *reinterpret_cast<u32x4*>(keys + L::kTile + (first + my_row) * L::kRow + my_piece * 16) = Vr[i];
     }
     const Where next = find(t0 + kTurn, ahead);
     ahead = look_up(t0 + 2 * kTurn);
@@ -327,12 +329,13 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
 
     f32x4 S[L::kSub];
 #pragma unroll
-    for (int u = 0; u < L::kSub; ++u) {
-      S[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < L::kSub; ++u) S[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < L::kQ; ++c) {
-        const u32x4 k = *reinterpret_cast<const u32x4*>(keys + L::piece(16 * u + l16, 4 * c + g));
-        const u32x4 q = kQueries ? sm.q[kQueries ? c : 0][kQueries ? lane : 0] : Q[c];
+    for (int c = 0; c < L::kQ; ++c) {
+      const u32x4 q = kQueries ? sm.q[kQueries ? c : 0][kQueries ? lane : 0] : Q[c];
+#pragma unroll
+      for (int u = 0; u < L::kSub; ++u) {
+        const u32x4 k = *reinterpret_cast<const u32x4*>(keys + 16 * u * L::kRow + (read ^ (c << 6)));
         if constexpr (DT == 0) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
