@@ -170,6 +170,7 @@ struct Shared {
   // 16-bit queries of 256 values (RW = 1): in registers they leave too few for the loads
   static constexpr bool kQueries = DT != 0 && D == 256 && RW == 1;
   u32x4 q[kQueries ? L::kQ : 1][kQueries ? kWave : 1];
+  int odd[2][NW];  // RW > 1: whether a wavefront's values of a tile hold an infinity or NaN
   float weights[RW == 1 ? 1 : NW][RW == 1 ? 1 : L::kKeys * 16];  // RW = 1: in the place of a wavefront's keys
   float stat[NW][16][2];
 };
@@ -267,7 +268,7 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
       x[i] = load<u32x4>(scalar(pool + at + row % 16 * ts) + in_row);
     }
   };
-  uint32_t V[4 * L::kSub][L::VC][L::kWords];
+  uint32_t V[RW == 1 ? L::VC : 1][4 * L::kSub][L::kWords];
   // RW = 1: values straight to where the products take them
   auto load_v = [&](const Where& w) {
 #pragma unroll
@@ -279,11 +280,11 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
         if constexpr (L::kWords == 4) {
           const u32x4 x = load<u32x4>(p);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) V[i][c][e] = x[e];
+          for (int e = 0; e < 4; ++e) V[c][i][e] = x[e];
         } else {
           const u32x2 x = load<u32x2>(p);
-          V[i][c][0] = x[0];
-          V[i][c][1] = x[1];
+          V[c][i][0] = x[0];
+          V[c][i][1] = x[1];
         }
       }
     }
@@ -305,9 +306,30 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
   int turn = 0;
   for (int t0 = start; t0 < to; t0 += kTurn) {
     char* keys = sm.tiles + (RW == 1 ? wave * L::kTile : turn * 2 * L::kTile);
-    turn ^= 1;
     if constexpr (RW == 1) load_v(here);
     __builtin_amdgcn_sched_barrier(0);
+    // Values that no row sees become 0: a weight of 0 does not keep an infinity or NaN out of a product.
+    bool outside = t0 < sp.k0 || t0 + L::kKeys > sp.k1;
+#pragma unroll
+    for (int u = 0; u < L::kSub; ++u) outside = outside || !here.there[u];
+    if constexpr (RW > 1) {
+      if (outside) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int row = (i * RW + share_of) * L::kAtOnce + my_row;
+          const bool seen = (row < 16 ? here.there[0] : here.there[L::kSub - 1]) && t0 + row >= sp.k0 && t0 + row < sp.k1;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) Vr[i][e] = seen ? Vr[i][e] : 0u;
+        }
+      }
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = largest<DT>(most, Vr[i][e]);
+      const bool odd = __any(not_finite<DT>(most));
+      if (lane == 0) sm.odd[turn][wave] = odd;
+    }
     uint32_t write = write_at, read = read_at;  // the places follow from these, and need no registers between turns
     asm volatile("" : "+v"(write), "+v"(read));
 #pragma unroll
@@ -323,6 +345,11 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
       load_rows(vb, next, Vr);
       // the tile is whole; the other one is free once every wavefront is past this point in the next turn
       __syncthreads();
+      turn ^= 1;
+      if (row0 >= rows) {  // a wavefront that only loads
+        here = next;
+        continue;
+      }
     } else {
       wave_lds_sync();
     }
@@ -345,18 +372,7 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
         }
       }
     }
-    if constexpr (RW > 1) {
-#pragma unroll
-      for (int i = 0; i < 4 * L::kSub; ++i)
-#pragma unroll
-        for (int c = 0; c < L::VC; ++c) {
-          const char* p = keys + L::kTile + (16 * (i / 4) + 4 * g + i % 4) * L::kRow + (c * 16 + l16) * L::VE * L::kBytes;
-#pragma unroll
-          for (int e = 0; e < L::kWords; ++e) V[i][c][e] = reinterpret_cast<const uint32_t*>(p)[e];
-        }
-    } else {
-      wave_lds_sync();  // the next tile's keys go to the same place
-    }
+    if constexpr (RW == 1) wave_lds_sync();  // the next tile's keys go to the same place
 
     // some row does not see some position of the tile
     bool edge = t0 < sp.k0 || t0 + L::kKeys > sp.first + 1 || (A.window > 0 && t0 <= last_pos - A.window);
@@ -398,59 +414,78 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
         lo[i] = pack2<1>(P[2 * i] - lo16<1>(hi[i]), P[2 * i + 1] - hi16<1>(hi[i]));
       }
     }
-    auto product = [&](int c, int j, f32x4 z) {
+    auto product = [&](const uint32_t (&v)[4 * L::kSub][L::kWords], int j, f32x4 z) {
       if constexpr (DT == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(V[i][c][j]), P[i], z, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) z = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(v[i][j]), P[i], z, 0, 0, 0);
       } else {
         u32x4 a;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          a[i] = __builtin_amdgcn_perm(V[2 * i + 1][c][j / 2], V[2 * i][c][j / 2], j % 2 == 0 ? 0x05040100u : 0x07060302u);
+          a[i] = __builtin_amdgcn_perm(v[2 * i + 1][j / 2], v[2 * i][j / 2], j % 2 == 0 ? 0x05040100u : 0x07060302u);
         z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, hi), z, 0, 0, 0);
         z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, lo), z, 0, 0, 0);
       }
       return z;
     };
-    // Values that no row sees become 0: a weight of 0 does not keep an infinity or NaN out of a product.
-    if (edge) {
+    bool odd = false;
+    if constexpr (RW == 1) {
+      if (outside) {
 #pragma unroll
-      for (int i = 0; i < 4 * L::kSub; ++i) {
-        const int key = t0 + 16 * (i / 4) + 4 * g + i % 4;
-        const bool seen = here.there[i / 4] && key >= sp.k0 && key < sp.k1;
+        for (int i = 0; i < 4 * L::kSub; ++i) {
+          const int key = t0 + 16 * (i / 4) + 4 * g + i % 4;
+          const bool seen = here.there[i / 4] && key >= sp.k0 && key < sp.k1;
+#pragma unroll
+          for (int c = 0; c < L::VC; ++c)
+#pragma unroll
+            for (int e = 0; e < L::kWords; ++e) V[c][i][e] = seen ? V[c][i][e] : 0u;
+        }
+      }
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < 4 * L::kSub; ++i)
 #pragma unroll
         for (int c = 0; c < L::VC; ++c)
 #pragma unroll
-          for (int e = 0; e < L::kWords; ++e) V[i][c][e] = seen ? V[i][c][e] : 0u;
-      }
+          for (int e = 0; e < L::kWords; ++e) most = largest<DT>(most, V[c][i][e]);
+      odd = __any(not_finite<DT>(most));
+    } else {
+      int any = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) any |= sm.odd[turn ^ 1][w];
+      odd = __builtin_amdgcn_readfirstlane(any) != 0;
     }
     // Neither does a second piece of 0, or the weight of a row that does not see them, keep out those that
     // are left: they are added one by one, and the products get 0 in their place.
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < 4 * L::kSub; ++i)
-#pragma unroll
-      for (int c = 0; c < L::VC; ++c)
-#pragma unroll
-        for (int e = 0; e < L::kWords; ++e) most = largest<DT>(most, V[i][c][e]);
-    const bool odd = __any(not_finite<DT>(most));
     float* weights = RW == 1 ? reinterpret_cast<float*>(keys) : sm.weights[RW == 1 ? 0 : wave];  // [key][row]
     if (__builtin_expect(odd, 0)) {
       wave_lds_sync();
 #pragma unroll
-      for (int i = 0; i < 4 * L::kSub; ++i) {
-        weights[(16 * (i / 4) + 4 * g + i % 4) * 16 + l16] = P[i];
-#pragma unroll
-        for (int c = 0; c < L::VC; ++c)
-#pragma unroll
-          for (int e = 0; e < L::kWords; ++e) V[i][c][e] = finite_only<DT>(V[i][c][e]);
-      }
+      for (int i = 0; i < 4 * L::kSub; ++i) weights[(16 * (i / 4) + 4 * g + i % 4) * 16 + l16] = P[i];
       wave_lds_sync();
     }
 #pragma unroll
-    for (int c = 0; c < L::VC; ++c)
+    for (int c = 0; c < L::VC; ++c) {
+      uint32_t v[4 * L::kSub][L::kWords];
 #pragma unroll
-      for (int j = 0; j < L::VE; ++j) O[c * L::VE + j] = product(c, j, O[c * L::VE + j]);
+      for (int i = 0; i < 4 * L::kSub; ++i)
+#pragma unroll
+        for (int e = 0; e < L::kWords; ++e) {
+          if constexpr (RW == 1)
+            v[i][e] = V[c][i][e];
+          else
+            v[i][e] = reinterpret_cast<const uint32_t*>(keys + L::kTile + (16 * (i / 4) + 4 * g + i % 4) * L::kRow +
+                                                        (c * 16 + l16) * L::VE * L::kBytes)[e];
+        }
+      if (__builtin_expect(odd, 0)) {
+#pragma unroll
+        for (int i = 0; i < 4 * L::kSub; ++i)
+#pragma unroll
+          for (int e = 0; e < L::kWords; ++e) v[i][e] = finite_only<DT>(v[i][e]);
+      }
+#pragma unroll
+      for (int j = 0; j < L::VE; ++j) O[c * L::VE + j] = product(v, j, O[c * L::VE + j]);
+    }
     if (__builtin_expect(odd, 0)) {
 #pragma unroll 1
       for (int k = 0; k < L::kKeys; ++k) {
