@@ -580,14 +580,15 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
   }
 }
 
-// A workgroup per request and key head.
-template <int DT, int D>
-__global__ __launch_bounds__(kMany* kWave, 2) void k_attend_whole(const AttendArgs A) {
-  __shared__ Shared<DT, D, 1, kMany> sm;
-  const int kh = static_cast<int>(blockIdx.x % A.c.key_heads), b = static_cast<int>(blockIdx.x / A.c.key_heads);
+// A workgroup per request, key head and row block.
+template <int DT, int D, int RW, int NW>
+__global__ __launch_bounds__(NW* kWave, 2) void k_attend_whole(const AttendArgs A) {
+  __shared__ Shared<DT, D, RW, NW> sm;
+  const int kh = static_cast<int>(blockIdx.x % A.c.key_heads), rest = static_cast<int>(blockIdx.x / A.c.key_heads);
+  const int b = RW == 1 ? rest : rest / A.row_blocks, rb = RW == 1 ? 0 : rest - b * A.row_blocks;
   const Span sp = span_of(A, b);
-  if (sp.n == 0) return;
-  attend_keys<DT, D, 1, kMany>(A, sm, sp, b, kh, 0, sp.base, sp.k1, nullptr, nullptr);
+  if (16 * RW * rb >= sp.n * A.share) return;
+  attend_keys<DT, D, RW, NW>(A, sm, sp, b, kh, rb, sp.base, sp.k1, nullptr, nullptr);
 }
 
 // The turns of all requests (of `step` keys, row block after row block) are cut into equal shares, one for each of
@@ -745,7 +746,9 @@ template <int DT, int D>
 hipError_t attend(const AttendArgs& a, hipStream_t s) {
   const int64_t heads = a.c.key_heads;
   if (a.groups == 0) {
-    k_attend_whole<DT, D><<<dim3(static_cast<unsigned>(a.c.batch * heads)), dim3(kMany * kWave), 0, s>>>(a);
+    const dim3 grid(static_cast<unsigned>(a.c.batch * heads * a.row_blocks));
+    if (a.block_rows <= 16) k_attend_whole<DT, D, 1, kMany><<<grid, dim3(kMany * kWave), 0, s>>>(a);
+    else k_attend_whole<DT, D, kWaves, kWaves><<<grid, dim3(kWaves * kWave), 0, s>>>(a);
     return hipGetLastError();
   }
   const dim3 grid(static_cast<unsigned>(a.groups * heads)), threads(kWaves * kWave);
@@ -778,9 +781,11 @@ bool plan_attend(int32_t io_dtype, AttendArgs& a) {
   if (a.window > 0) span = std::min(span, static_cast<int64_t>(a.window) + a.max_tokens - 1 + 31);
   const int64_t turns = static_cast<int64_t>(a.c.batch) * a.row_blocks * ((span + step - 1) / step);  // at most, of a key head
   if (turns >= int64_t{1} << 30) return false;
-  const int64_t few = (io_dtype == SEED_BF16 ? 1024 : 512) / (a.c.dim == 256 ? 4 : 1);
+  const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * a.row_blocks;
+  const int64_t few = rows <= 16 ? std::min(4 * tile * kMany, (int64_t{256} << 10) / (a.c.dim * (io_dtype == SEED_BF16 ? 2 : 4)))
+                                 : (units >= 512 ? 32 : 8) * step;
   a.groups = 0;
-  if (rows <= 16 && span <= few && static_cast<int64_t>(a.c.batch) * a.c.key_heads <= 256) return true;
+  if (span <= few) return true;
   a.groups = static_cast<int32_t>(std::max(std::min((kGroups + a.c.key_heads - 1) / a.c.key_heads, turns), int64_t{1}));
   return true;
 }
