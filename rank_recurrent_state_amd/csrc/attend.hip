@@ -3,13 +3,20 @@
 // in one pass over the keys with a running maximum m and sum l: weights are 2^(scale log2(e) q.k - m), and where
 // m grows, what was summed so far is multiplied by 2^(m_old - m_new).
 //
-// What bounds it: every key and value is read once for all rows that share it, so HBM. A wavefront takes 32 keys
-// at a time (fp32: 16), for 16 rows (queries of one key head, of all the request's new tokens) per matrix
-// tile, and holds everything in registers:
+// What bounds it: every key and value is read once for all rows that share it, so HBM. The rows, queries of one key
+// head of all the request's new tokens, are taken 16 at a time by a wavefront, over 32 keys (fp32: 16):
 //   S^T = K Q^T   a lane has row lane % 16 and keys 4 (lane / 16) + r of each 16,
 //   O^T = V^T P^T takes the weights as they lie: the order of keys inside a product is free, so V's rows are
-//                 loaded in the order in which the lanes hold the weights, whole rows of V by 16 lanes, and its
-//                 16-bit values are paired by key with byte permutes. No LDS until the wavefronts are joined.
+//                 read in the order in which the lanes hold the weights, whole rows of V by 16 lanes, and its
+//                 16-bit values are paired by key with byte permutes.
+// Keys are loaded as whole rows and pass through LDS to where the product takes them. Up to 16 rows: every wavefront
+// has keys of its own, and its values go straight to registers; the wavefronts are joined at the end. More: 4
+// wavefronts have 16 rows each and share two tiles of keys and values in LDS, each loading a quarter of the next.
+// The keys of all requests are cut into equal shares for two workgroups per compute unit, whose partial results
+// a second launch joins; short ones stay whole and need no second launch.
+// Measured: 64 requests of up to 16384 tokens, 8 key heads of 128, 1.75 GB: 286 us, 6.1 TB/s (the kernel alone 6.2; a
+// kernel that only reads such pages 6.5 - 6.7); one request of 131072 tokens 92 us, 5.9 TB/s; 6 tokens of 48 requests
+// (48 rows of a key head of 256), 298 MB: 73 us, 4.1 TB/s, where partial results and their join take the rest.
 // bf16 weights enter as two pieces (p and p - bf16(p)), so that o is off by its own rounding only: with one
 // piece the weights' rounding, 2^-9 each, is as large as o's. The products are far from the matrix unit's rate.
 // m is only moved when a score passes it by 8 (weights up to 2^8): most tiles then need no exchange between
@@ -25,7 +32,10 @@ namespace {
 
 constexpr int kWaves = 4;  // of a workgroup; short caches take kMany
 constexpr int kMany = 8;
-constexpr int64_t kGroups = 512;  // workgroups of a call that share its keys
+// Workgroups of a call that share its keys: two for each compute unit, as many as their registers and LDS admit. 6 tokens
+// of 48 requests 78 us, 85 with half as many and 91 with twice; 16 requests of 4096 keys 31, 33 and 33; one of 131072
+// keys 93, 92 and 94; each more part of a row is another one to write and to join.
+constexpr int64_t kGroups = 512;
 
 // Turns of a workgroup: equal shares of them all.
 __device__ __forceinline__ int share_of(int turns, int groups) {
@@ -225,7 +235,7 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
   const char* __restrict__ kb = reinterpret_cast<const char*>(static_cast<const T*>(C.k) + kh * C.head_stride);
   const char* __restrict__ vb = reinterpret_cast<const char*>(static_cast<const T*>(C.v) + kh * C.head_stride);
   const int64_t ts = C.token_stride * L::kBytes, page_stride = C.page_stride * L::kBytes;
-  const uint32_t in_k = static_cast<uint32_t>(l16 * ts) + g * 16, in_v = static_cast<uint32_t>(4 * g * ts) + l16 * L::VE * L::kBytes;
+  const uint32_t in_v = static_cast<uint32_t>(4 * g * ts) + l16 * L::VE * L::kBytes;
   const int in_page = (1 << C.page_shift) - 1;
 
   // The places of a tile's parts: 16 positions lie in one page; parts behind this workgroup's last read that again.
@@ -744,20 +754,25 @@ namespace {
 
 template <int DT, int D>
 hipError_t attend(const AttendArgs& a, hipStream_t s) {
+  constexpr bool kWide = Tile<DT, D>::kRow > 512;  // as in plan_attend
   const int64_t heads = a.c.key_heads;
-  if (a.groups == 0) {
-    const dim3 grid(static_cast<unsigned>(a.c.batch * heads * a.row_blocks));
-    if (a.block_rows <= 16) k_attend_whole<DT, D, 1, kMany><<<grid, dim3(kMany * kWave), 0, s>>>(a);
-    else k_attend_whole<DT, D, kWaves, kWaves><<<grid, dim3(kWaves * kWave), 0, s>>>(a);
-    return hipGetLastError();
+  const dim3 threads(kWaves * kWave);
+  if constexpr (!kWide) {
+    if (a.groups == 0) {
+      const dim3 grid(static_cast<unsigned>(a.c.batch * heads * a.row_blocks));
+      if (a.row_waves == 1) k_attend_whole<DT, D, 1, kMany><<<grid, dim3(kMany * kWave), 0, s>>>(a);
+      else k_attend_whole<DT, D, kWaves, kWaves><<<grid, threads, 0, s>>>(a);
+      return hipGetLastError();
+    }
   }
-  const dim3 grid(static_cast<unsigned>(a.groups * heads)), threads(kWaves * kWave);
-  if (a.block_rows <= 16) k_attend<DT, D, 1><<<grid, threads, 0, s>>>(a);
-  else k_attend<DT, D, kWaves><<<grid, threads, 0, s>>>(a);
+  const dim3 grid(static_cast<unsigned>(a.groups * heads));
+  if (kWide || a.row_waves > 1) k_attend<DT, D, kWaves><<<grid, threads, 0, s>>>(a);
+  else k_attend<DT, D, kWide ? kWaves : 1><<<grid, threads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  // Few rows: 8 wavefronts each (one request of 100000 keys, 32 rows: 73 us from 76 with one), many: one (64 requests,
+  // 2048 rows: 146 us from 150; 512 rows are the same).
   const int64_t items = static_cast<int64_t>(a.c.batch) * a.max_tokens * a.c.heads;
-  // many rows: a wavefront each
   if (items > 512)
     k_attend_join<DT, D, 1><<<dim3(static_cast<unsigned>((items + kWaves - 1) / kWaves)), threads, 0, s>>>(a);
   else
@@ -774,16 +789,27 @@ hipError_t pick(const AttendArgs& a, hipStream_t s) {
 
 bool plan_attend(int32_t io_dtype, AttendArgs& a) {
   const int64_t rows = static_cast<int64_t>(a.max_tokens) * a.share, tile = io_dtype == SEED_BF16 ? 32 : 16;
-  a.block_rows = static_cast<int32_t>(rows <= 16 ? rows : 16 * kWaves);
+  const int64_t row_bytes = static_cast<int64_t>(a.c.dim) * (io_dtype == SEED_BF16 ? 2 : 4);
+  // Up to 16 rows are one matrix tile's, and the wavefronts take keys of their own: against rows over wavefronts,
+  // 16 requests of 4096 keys of 128 values 31 us from 34, 64 of 3000 keys of 64 values 23 from 33, 32 of 5000 in fp32
+  // 97 from 121. Not fp32 of 256 values, which a wavefront has no registers for: 8 requests of 20000 keys 75 from 96
+  // with shared tiles; nor are those ever faster in one launch (120 keys: 13 us from 17).
+  const bool wide = row_bytes > 512;
+  a.row_waves = rows <= 16 && !wide ? 1 : kWaves;
+  a.block_rows = static_cast<int32_t>(std::min(rows, int64_t{16} * a.row_waves));
   a.row_blocks = static_cast<int32_t>((rows + a.block_rows - 1) / a.block_rows);
-  const int64_t step = rows <= 16 ? tile * kWaves : tile;  // keys of one turn of a workgroup
+  const int64_t step = a.row_waves == 1 ? tile * kWaves : tile;  // keys of one turn of a workgroup
   int64_t span = a.capacity;
   if (a.window > 0) span = std::min(span, static_cast<int64_t>(a.window) + a.max_tokens - 1 + 31);
   const int64_t turns = static_cast<int64_t>(a.c.batch) * a.row_blocks * ((span + step - 1) / step);  // at most, of a key head
   if (turns >= int64_t{1} << 30) return false;
+  // Short spans in one launch, a workgroup each. One request of 300 keys: 7.4 us from 11.4 with shares and a join;
+  // 64 requests of 1000 keys: 30 both; of 2000: 56 from 49 the other way. Rows over wavefronts take the keys one
+  // tile after another, so that where units leave compute units idle only a few are as fast: 8 requests of 6
+  // tokens over 256 keys 13 us, cut 11 (and 4 us of host time more), over 512 keys 21 and 13; but 64 of 512 keys
+  // 24 from 36, of 1000 39 from 44, of 2000 85 and 61.
   const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * a.row_blocks;
-  const int64_t few = rows <= 16 ? std::min(4 * tile * kMany, (int64_t{256} << 10) / (a.c.dim * (io_dtype == SEED_BF16 ? 2 : 4)))
-                                 : (units >= 512 ? 32 : 8) * step;
+  const int64_t few = wide ? 0 : a.row_waves == 1 ? std::min(4 * tile * kMany, (int64_t{256} << 10) / row_bytes) : (units >= 512 ? 32 : 8) * step;
   a.groups = 0;
   if (span <= few) return true;
   a.groups = static_cast<int32_t>(std::max(std::min((kGroups + a.c.key_heads - 1) / a.c.key_heads, turns), int64_t{1}));

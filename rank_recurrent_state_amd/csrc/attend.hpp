@@ -54,6 +54,7 @@ struct AttendArgs {
   float scale2;             // |scale| log2(e)
   uint32_t negate;          // the sign bits of a word of q, where scale is negative
   uint32_t pages;           // of the pool, as far as table entries reach
+  int32_t row_waves;        // wavefronts of a workgroup that have rows of their own
   int32_t block_rows;       // rows that a workgroup takes at a time, of max_tokens share,
   int32_t row_blocks;       // and how many times
   int32_t groups;           // workgroups that share a key head's turns; 0: a workgroup per request and key head
@@ -83,7 +84,7 @@ struct VerifyArgs {
 
 hipError_t launch_rotate_rows(int32_t io_dtype, const RotateArgs& a, hipStream_t s);
 hipError_t launch_cache_append(int32_t io_dtype, const AppendArgs& a, hipStream_t s);
-// Sets block_rows, row_blocks and groups from the sizes; false: more turns than are counted.
+// Sets row_waves, block_rows, row_blocks and groups from the sizes; false: more turns than are counted.
 bool plan_attend(int32_t io_dtype, AttendArgs& a);
 int64_t attend_workspace(const AttendArgs& a);
 hipError_t launch_attend(int32_t io_dtype, AttendArgs a, void* ws, hipStream_t s);
