@@ -22,6 +22,7 @@
 // m is only moved when a score passes it by 8 (weights up to 2^8): most tiles then need no exchange between
 // lanes and no rescaling, and every weight keeps its relative precision.
 #include <algorithm>
+#include <type_traits>
 
 #include "attend.hpp"
 #include "common.hpp"
@@ -146,11 +147,15 @@ __device__ __forceinline__ int scan(int v, int lane, int& total) {
   return v;
 }
 
-template <int DT, int D>
+constexpr int kShared = 16384;  // bytes of keys in a tile that the wavefronts share
+
+// Keys and values of a turn: a wavefront's own ones (RW = 1), or a tile of RW row blocks.
+template <int DT, int D, int RW>
 struct Tile {
   static constexpr int kBytes = DT == 0 ? 4 : 2;
   static constexpr int kVec = 16 / kBytes;            // values of a 16-byte access
-  static constexpr int kSub = DT == 0 ? 1 : 2;        // 16-key parts of a tile
+  static constexpr int kGroup = DT == 0 ? 1 : 2;      // 16-key parts whose values enter a product together
+  static constexpr int kSub = RW == 1 ? kGroup : kShared / (16 * D * kBytes);  // 16-key parts of a tile
   static constexpr int kKeys = 16 * kSub;
   static constexpr int kQ = D / (4 * kVec);           // 16-byte pieces of a row per lane
   static constexpr int VE = D / 16 < kVec ? D / 16 : kVec;  // values of V per lane and access
@@ -172,7 +177,7 @@ struct Tile {
 // A workgroup's shared memory.
 template <int DT, int D, int RW, int NW>
 struct Shared {
-  using L = Tile<DT, D>;
+  using L = Tile<DT, D, RW>;
   static constexpr int GT = L::kOut < 8 ? L::kOut : 8;  // accumulators joined at a time
   // A wavefront's keys (RW = 1), or all wavefronts' keys and values, twice; at the end the accumulators.
   static constexpr int kJoin = NW * GT * kWave * 16, kTiles = RW == 1 ? NW * L::kTile : 4 * L::kTile;
@@ -180,21 +185,23 @@ struct Shared {
   // 16-bit queries of 256 values (RW = 1): in registers they leave too few for the loads
   static constexpr bool kQueries = DT != 0 && D == 256 && RW == 1;
   u32x4 q[kQueries ? L::kQ : 1][kQueries ? kWave : 1];
-  int odd[2][NW];  // RW > 1: whether a wavefront's values of a tile hold an infinity or NaN
-  float weights[RW == 1 ? 1 : NW][RW == 1 ? 1 : L::kKeys * 16];  // RW = 1: in the place of a wavefront's keys
+  // RW > 1: what a wavefront found in its rows of a tile: 1: a value that is an infinity or NaN, 2: a page that is not there
+  __attribute__((aligned(16))) int found[2][NW];
+  float weights[RW == 1 ? 1 : NW][RW == 1 ? 1 : L::kGroup * 256];  // RW = 1: in the place of a wavefront's keys
   float stat[NW][16][2];
 };
 
 // Rows [16 RW rb, ..) of request b and key head kh over the keys [from, to): written to o, or as maximum, sum and
 // accumulators of each row to stat and part (nullptr: o). NW wavefronts: RW = 1: of the same 16 rows and keys of
-// their own each; RW = NW: of 16 rows each and the same keys.
+// their own each; else RW of 16 rows each by NW / RW parts of the tiles that they share.
 template <int DT, int D, int RW, int NW>
 __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, RW, NW>& sm, const Span& sp, int b, int kh, int rb, int from,
                                             int to, float* part, float* part_stat) {
-  using L = Tile<DT, D>;
+  using L = Tile<DT, D, RW>;
   using T = stor_t<DT>;
-  static_assert(RW == 1 || RW == NW, "rows or keys of their own");
   constexpr int KW = NW / RW, GT = Shared<DT, D, RW, NW>::GT;
+  constexpr int kParts = RW == 1 ? L::kSub : L::kSub / KW;  // of 16 keys, that a wavefront takes of a tile
+  static_assert(kParts % L::kGroup == 0 && (RW == 1 || KW <= 2), "whole products; a part of a tile is one of two");
   const CacheArgs& C = A.c;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -202,7 +209,7 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
   const int rows = sp.n * share, block0 = rb * RW * 16;
 
   // this lane's row of the wavefront's 16: a query of key head kh
-  const int row0 = block0 + (RW > 1 ? 16 * wave : 0);
+  const int row0 = block0 + 16 * (wave % RW), half = RW == 1 || KW == 1 ? 0 : wave / RW;
   const int r = row0 + l16, token = token_of(A, r);
   const int pos = r < rows ? sp.first + token : -1;
   u32x4 Q[L::kQ];
@@ -238,45 +245,44 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
   const uint32_t in_v = static_cast<uint32_t>(4 * g * ts) + l16 * L::VE * L::kBytes;
   const int in_page = (1 << C.page_shift) - 1;
 
-  // The places of a tile's parts: 16 positions lie in one page; parts behind this workgroup's last read that again.
+  // The places of the 16-key parts of the rows that this wavefront loads, of all of its own tile (RW = 1) or some
+  // of the shared one's: 16 positions lie in one page; parts behind this workgroup's last read that again.
+  constexpr int kLoaders = RW == 1 ? 1 : NW, kRows = L::kKeys / kLoaders, kMine = kRows < 16 ? 1 : kRows / 16;
+  const int mine = RW == 1 ? 0 : wave * kRows;  // the first of these rows
   struct Where {
-    int64_t at[L::kSub];
-    bool there[L::kSub];
+    int64_t at[kMine];
+    bool there[kMine];
   };
   struct Pages {
-    int number[L::kSub];
+    int number[kMine];
   };
-  auto part_at = [&](int t0, int u) { return min(t0 + 16 * u, (to - 1) & ~15); };
+  auto part_at = [&](int key) { return min(key, (to - 1) & ~15); };
+  auto page_of = [&](int key) { return table[part_at(key) >> C.page_shift]; };
   auto look_up = [&](int t0) {
     Pages p;
 #pragma unroll
-    for (int u = 0; u < L::kSub; ++u) p.number[u] = table[part_at(t0, u) >> C.page_shift];
+    for (int u = 0; u < kMine; ++u) p.number[u] = page_of(t0 + (mine & ~15) + 16 * u);
     return p;
   };
   auto find = [&](int t0, const Pages& p) {
     Where w;
 #pragma unroll
-    for (int u = 0; u < L::kSub; ++u) {
+    for (int u = 0; u < kMine; ++u) {
       w.there[u] = static_cast<uint32_t>(p.number[u]) < A.pages;
-      w.at[u] = static_cast<int64_t>(w.there[u] ? p.number[u] : 0) * page_stride + (part_at(t0, u) & in_page) * ts;
+      w.at[u] = static_cast<int64_t>(w.there[u] ? p.number[u] : 0) * page_stride +
+                ((part_at(t0 + (mine & ~15) + 16 * u) & in_page) + mine % 16) * ts;
     }
     return w;
   };
   // Whole rows per load, 16 bytes per lane: 6.6 TB/s of keys and values, 5.7 with the 64 bytes of 16 rows that the
   // products take; and past the caches, which keep nothing of a cache read once a step (5.9 with them).
-  constexpr int kLoads = L::kKeys / L::kAtOnce / RW;
-  const int my_row = lane / L::kLine, my_piece = lane % L::kLine, share_of = RW == 1 ? 0 : wave;
+  constexpr int kLoads = kRows / L::kAtOnce;
+  const int my_row = lane / L::kLine, my_piece = lane % L::kLine;
   const uint32_t in_row = static_cast<uint32_t>(my_row * ts) + my_piece * 16;
   u32x4 K[kLoads], Vr[kLoads];
   auto load_rows = [&](const char* pool, const Where& w, u32x4 (&x)[kLoads]) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int first = (i * RW) * L::kAtOnce;  // the first wavefront's first row
-      const int row = first + share_of * L::kAtOnce;
-      int64_t at = w.at[0];
-      if constexpr (L::kSub == 2) at = row < 16 ? w.at[0] : w.at[1];
-      x[i] = load<u32x4>(scalar(pool + at + row % 16 * ts) + in_row);
-    }
+    for (int i = 0; i < kLoads; ++i) x[i] = load<u32x4>(scalar(pool + w.at[i * L::kAtOnce / 16] + i * L::kAtOnce % 16 * ts) + in_row);
   };
   uint32_t V[RW == 1 ? L::VC : 1][4 * L::kSub][L::kWords];
   // RW = 1: values straight to where the products take them
@@ -302,7 +308,7 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
 
   // Keys are loaded a tile ahead, as soon as the last ones are in LDS, values while the scores are formed (RW > 1:
   // a tile ahead too): something is always on its way.
-  constexpr int kTurn = KW * L::kKeys;
+  constexpr int kTurn = (RW == 1 ? NW : 1) * L::kKeys;
   Where here{};
   const int start = from + (RW == 1 ? wave * L::kKeys : 0);
   if (from < to) {
@@ -310,7 +316,7 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
     load_rows(kb, here, K);
     if constexpr (RW > 1) load_rows(vb, here, Vr);
   }
-  const uint32_t write_at = my_row * L::kRow + ((my_piece ^ L::swap(my_row)) << 4), read_at = l16 * L::kRow + ((g ^ L::swap(l16)) << 4);
+  const uint32_t write_at = (mine + my_row) * L::kRow + ((my_piece ^ L::swap(mine) ^ L::swap(my_row)) << 4), read_at = l16 * L::kRow + ((g ^ L::swap(l16)) << 4);
   Pages ahead{};  // of the next turn: looked up a turn ahead too
   if (from < to) ahead = look_up(start + kTurn);
   int turn = 0;
@@ -319,15 +325,16 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
     if constexpr (RW == 1) load_v(here);
     __builtin_amdgcn_sched_barrier(0);
     // Values that no row sees become 0: a weight of 0 does not keep an infinity or NaN out of a product.
-    bool outside = t0 < sp.k0 || t0 + L::kKeys > sp.k1;
+    bool gap = false;
 #pragma unroll
-    for (int u = 0; u < L::kSub; ++u) outside = outside || !here.there[u];
+    for (int u = 0; u < kMine; ++u) gap = gap || !here.there[u];
+    const bool outside = t0 < sp.k0 || t0 + L::kKeys > sp.k1 || gap;
     if constexpr (RW > 1) {
       if (outside) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          const int row = (i * RW + share_of) * L::kAtOnce + my_row;
-          const bool seen = (row < 16 ? here.there[0] : here.there[L::kSub - 1]) && t0 + row >= sp.k0 && t0 + row < sp.k1;
+          const int key = t0 + mine + i * L::kAtOnce + my_row;
+          const bool seen = here.there[i * L::kAtOnce / 16] && key >= sp.k0 && key < sp.k1;
 #pragma unroll
           for (int e = 0; e < 4; ++e) Vr[i][e] = seen ? Vr[i][e] : 0u;
         }
@@ -337,20 +344,20 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
       for (int i = 0; i < kLoads; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) most = largest<DT>(most, Vr[i][e]);
-      const bool odd = __any(not_finite<DT>(most));
-      if (lane == 0) sm.odd[turn][wave] = odd;
+      const int odd = __any(not_finite<DT>(most)) ? 1 : 0;
+      if (lane == 0) sm.found[turn][wave] = odd | (gap ? 2 : 0);
     }
     uint32_t write = write_at, read = read_at;  // the places follow from these, and need no registers between turns
     asm volatile("" : "+v"(write), "+v"(read));
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int first = (i * RW + share_of) * L::kAtOnce;
-      *reinterpret_cast<u32x4*>(keys + first * L::kRow + (write ^ (L::swap(first) << 4))) = K[i];
-      if constexpr (RW > 1) *reinterpret_cast<u32x4*>(keys + L::kTile + (first + my_row) * L::kRow + my_piece * 16) = Vr[i];
+      constexpr int kStep = L::kAtOnce * L::kRow;
+      *reinterpret_cast<u32x4*>(keys + i * kStep + (write ^ (L::swap(i * L::kAtOnce) << 4))) = K[i];
+      if constexpr (RW > 1) *reinterpret_cast<u32x4*>(keys + L::kTile + i * kStep + (mine + my_row) * L::kRow + my_piece * 16) = Vr[i];
     }
     const Where next = find(t0 + kTurn, ahead);
     ahead = look_up(t0 + 2 * kTurn);
-    load_rows(kb, next, K);  // behind the last tile one that is there: the loads on their way are then the same in number
+    load_rows(kb, next, K);  // behind the last tile, of that: the loads on their way are then the same in number
     if constexpr (RW > 1) {
       load_rows(vb, next, Vr);
       // the tile is whole; the other one is free once every wavefront is past this point in the next turn
@@ -364,15 +371,42 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
       wave_lds_sync();
     }
 
-    f32x4 S[L::kSub];
+    // this wavefront's part of the tile
+    const int first = t0 + half * 16 * kParts;
+    const char* my_keys = keys + half * 16 * kParts * L::kRow;
+    bool odd = false;
+    if constexpr (RW > 1) {
+      int found = 0;
 #pragma unroll
-    for (int u = 0; u < L::kSub; ++u) S[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int w = 0; w < NW; ++w) found |= sm.found[turn ^ 1][w];
+      found = __builtin_amdgcn_readfirstlane(found);
+      odd = (found & 1) != 0;
+      gap = found >= 2;
+    }
+    f32x4 S[kParts];
 #pragma unroll
-    for (int c = 0; c < L::kQ; ++c) {
-      const u32x4 q = kQueries ? sm.q[kQueries ? c : 0][kQueries ? lane : 0] : Q[c];
+    for (int u = 0; u < kParts; ++u) S[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // Pieces of the keys in runs, one read while the products take the one before, where there are registers for them (fp32
+    // and 16-bit heads of 256, and a wavefront's own values, leave none: the order is the compiler's).
+    constexpr bool kOrder = RW > 1 && L::kOut <= 8;
+    constexpr int kMost = kOrder ? 8 : kParts, kRun = L::kQ * kParts < kMost ? L::kQ * kParts : kMost, kRuns = L::kQ * kParts / kRun;
+    u32x4 piece[2][kRun];
+    auto read_run = [&](int n) {
 #pragma unroll
-      for (int u = 0; u < L::kSub; ++u) {
-        const u32x4 k = *reinterpret_cast<const u32x4*>(keys + 16 * u * L::kRow + (read ^ (c << 6)));
+      for (int i = 0; i < kRun; ++i) {
+        const int c = (n * kRun + i) / kParts, u = (n * kRun + i) % kParts;
+        piece[n % 2][i] = *reinterpret_cast<const u32x4*>(my_keys + 16 * u * L::kRow + (read ^ (c << 6)));
+      }
+    };
+    read_run(0);
+#pragma unroll
+    for (int n = 0; n < kRuns; ++n) {
+      if (n + 1 < kRuns) read_run(n + 1);
+      if constexpr (kOrder) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const int c = (n * kRun + i) / kParts, u = (n * kRun + i) % kParts;
+        const u32x4 q = kQueries ? sm.q[kQueries ? c : 0][kQueries ? lane : 0] : Q[c], k = piece[n % 2][i];
         if constexpr (DT == 0) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -381,24 +415,26 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
           S[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k), __builtin_bit_cast(bf16x8, q), S[u], 0, 0, 0);
         }
       }
+      if constexpr (kOrder) __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (RW == 1) wave_lds_sync();  // the next tile's keys go to the same place
 
     // some row does not see some position of the tile
-    bool edge = t0 < sp.k0 || t0 + L::kKeys > sp.first + 1 || (A.window > 0 && t0 <= last_pos - A.window);
+    if (gap || t0 < sp.k0 || t0 + L::kKeys > sp.first + 1 || (A.window > 0 && t0 <= last_pos - A.window)) {
 #pragma unroll
-    for (int u = 0; u < L::kSub; ++u) edge = edge || !here.there[u];
-    if (edge) {
+      for (int u = 0; u < kParts; ++u) {
+        const bool there = !gap || static_cast<uint32_t>(page_of(first + 16 * u)) < A.pages;
 #pragma unroll
-      for (int i = 0; i < 4 * L::kSub; ++i) {
-        const int key = t0 + 16 * (i / 4) + 4 * g + i % 4;
-        const bool seen = here.there[i / 4] && key <= pos && (A.window <= 0 || key > pos - A.window);
-        S[i / 4][i % 4] = seen ? S[i / 4][i % 4] : kNegInf;
+        for (int i = 0; i < 4; ++i) {
+          const int key = first + 16 * u + 4 * g + i;
+          const bool seen = there && key <= pos && (A.window <= 0 || key > pos - A.window);
+          S[u][i] = seen ? S[u][i] : kNegInf;
+        }
       }
     }
     float top = kNegInf;
 #pragma unroll
-    for (int i = 0; i < 4 * L::kSub; ++i) top = fmaxf(top, S[i / 4][i % 4]);
+    for (int i = 0; i < 4 * kParts; ++i) top = fmaxf(top, S[i / 4][i % 4]);
     top *= A.scale2;
     if (__any(top > m + 8.f)) {
       const float now = fmaxf(m, max4(top));
@@ -410,35 +446,12 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
       for (int j = 0; j < L::kOut; ++j) O[j] *= f;
     }
     const float sub = m == kNegInf ? 0.f : m;
-    float P[4 * L::kSub];
+    float P[4 * kParts];
 #pragma unroll
-    for (int i = 0; i < 4 * L::kSub; ++i) {
+    for (int i = 0; i < 4 * kParts; ++i) {
       P[i] = exp2_(fmaf(S[i / 4][i % 4], A.scale2, -sub));
       l += P[i];
     }
-    u32x4 hi, lo;
-    if constexpr (DT != 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        hi[i] = pack2<1>(P[2 * i], P[2 * i + 1]);
-        lo[i] = pack2<1>(P[2 * i] - lo16<1>(hi[i]), P[2 * i + 1] - hi16<1>(hi[i]));
-      }
-    }
-    auto product = [&](const uint32_t (&v)[4 * L::kSub][L::kWords], int j, f32x4 z) {
-      if constexpr (DT == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(v[i][j]), P[i], z, 0, 0, 0);
-      } else {
-        u32x4 a;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          a[i] = __builtin_amdgcn_perm(v[2 * i + 1][j / 2], v[2 * i][j / 2], j % 2 == 0 ? 0x05040100u : 0x07060302u);
-        z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, hi), z, 0, 0, 0);
-        z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, lo), z, 0, 0, 0);
-      }
-      return z;
-    };
-    bool odd = false;
     if constexpr (RW == 1) {
       if (outside) {
 #pragma unroll
@@ -459,67 +472,94 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
 #pragma unroll
           for (int e = 0; e < L::kWords; ++e) most = largest<DT>(most, V[c][i][e]);
       odd = __any(not_finite<DT>(most));
-    } else {
-      int any = 0;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) any |= sm.odd[turn ^ 1][w];
-      odd = __builtin_amdgcn_readfirstlane(any) != 0;
     }
     // Neither does a second piece of 0, or the weight of a row that does not see them, keep out those that
     // are left: they are added one by one, and the products get 0 in their place.
     float* weights = RW == 1 ? reinterpret_cast<float*>(keys) : sm.weights[RW == 1 ? 0 : wave];  // [key][row]
-    if (__builtin_expect(odd, 0)) {
-      wave_lds_sync();
+    auto values = [&](auto is_odd) {
 #pragma unroll
-      for (int i = 0; i < 4 * L::kSub; ++i) weights[(16 * (i / 4) + 4 * g + i % 4) * 16 + l16] = P[i];
-      wave_lds_sync();
-    }
+      for (int p0 = 0; p0 < kParts; p0 += L::kGroup) {
+        constexpr int N = 4 * L::kGroup;  // a lane's weights of a product
+        const float(&W)[N] = *reinterpret_cast<const float(*)[N]>(P + 4 * p0);
+        u32x4 hi, lo;
+        if constexpr (DT != 0) {
 #pragma unroll
-    for (int c = 0; c < L::VC; ++c) {
-      uint32_t v[4 * L::kSub][L::kWords];
-#pragma unroll
-      for (int i = 0; i < 4 * L::kSub; ++i)
-#pragma unroll
-        for (int e = 0; e < L::kWords; ++e) {
-          if constexpr (RW == 1)
-            v[i][e] = V[c][i][e];
-          else
-            v[i][e] = reinterpret_cast<const uint32_t*>(keys + L::kTile + (16 * (i / 4) + 4 * g + i % 4) * L::kRow +
-                                                        (c * 16 + l16) * L::VE * L::kBytes)[e];
-        }
-      if (__builtin_expect(odd, 0)) {
-#pragma unroll
-        for (int i = 0; i < 4 * L::kSub; ++i)
-#pragma unroll
-          for (int e = 0; e < L::kWords; ++e) v[i][e] = finite_only<DT>(v[i][e]);
-      }
-#pragma unroll
-      for (int j = 0; j < L::VE; ++j) O[c * L::VE + j] = product(v, j, O[c * L::VE + j]);
-    }
-    if (__builtin_expect(odd, 0)) {
-#pragma unroll 1
-      for (int k = 0; k < L::kKeys; ++k) {
-        const int key = t0 + k, last = L::kSub - 1;  // no run-time index into here: it would leave the registers
-        const bool page = k < 16 ? here.there[0] : here.there[last];
-        const int64_t at = k < 16 ? here.at[0] : here.at[last];
-        const bool seen = page && key <= pos && (A.window <= 0 || key > pos - A.window);
-        if (!seen) continue;
-        const float p = weights[k * 16 + l16];
-        const char* base = vb + at + k % 16 * ts;
-#pragma unroll
-        for (int c = 0; c < L::VC; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {  // this lane's values of the row: 4 runs of VE
-            const T* v = reinterpret_cast<const T*>(base) + c * 16 * L::VE + (4 * g + e) * L::VE;
-#pragma unroll
-            for (int j = 0; j < L::VE; ++j) {
-              const float x = to_f32<DT>(v[j]);
-              if (!(fabsf(x) < __builtin_inff())) O[c * L::VE + j][e] += p * x;
-            }
-            __builtin_amdgcn_sched_barrier(0);
+          for (int i = 0; i < 4; ++i) {
+            hi[i] = pack2<1>(W[2 * i], W[2 * i + 1]);
+            lo[i] = pack2<1>(W[2 * i] - lo16<1>(hi[i]), W[2 * i + 1] - hi16<1>(hi[i]));
           }
+        }
+        auto product = [&](const uint32_t (&v)[N][L::kWords], int j, f32x4 z) {
+          if constexpr (DT == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(v[i][j]), W[i], z, 0, 0, 0);
+          } else {
+            u32x4 a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              a[i] = __builtin_amdgcn_perm(v[2 * i + 1][j / 2], v[2 * i][j / 2], j % 2 == 0 ? 0x05040100u : 0x07060302u);
+            z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, hi), z, 0, 0, 0);
+            z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, lo), z, 0, 0, 0);
+          }
+          return z;
+        };
+        if (__builtin_expect(is_odd, 0)) {
+          wave_lds_sync();
+#pragma unroll
+          for (int i = 0; i < N; ++i) weights[(16 * (i / 4) + 4 * g + i % 4) * 16 + l16] = W[i];
+          wave_lds_sync();
+        }
+#pragma unroll
+        for (int c = 0; c < L::VC; ++c) {
+          uint32_t v[N][L::kWords];
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < L::kWords; ++e) {
+              if constexpr (RW == 1)
+                v[i][e] = V[c][i][e];
+              else
+                v[i][e] = reinterpret_cast<const uint32_t*>(my_keys + L::kTile + (16 * (p0 + i / 4) + 4 * g + i % 4) * L::kRow +
+                                                            (c * 16 + l16) * L::VE * L::kBytes)[e];
+            }
+          if (__builtin_expect(is_odd, 0)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+              for (int e = 0; e < L::kWords; ++e) v[i][e] = finite_only<DT>(v[i][e]);
+          }
+#pragma unroll
+          for (int j = 0; j < L::VE; ++j) O[c * L::VE + j] = product(v, j, O[c * L::VE + j]);
+        }
+        if (__builtin_expect(is_odd, 0)) {
+#pragma unroll 1
+          for (int k = 0; k < 16 * L::kGroup; ++k) {
+            const int key = first + 16 * p0 + k;
+            // the page looked up again: a run-time index into here would take it out of the registers
+            const int at = min(key, ((to - 1) & ~15) + (key & 15)), number = table[at >> C.page_shift];
+            const bool seen = static_cast<uint32_t>(number) < A.pages && key <= pos && (A.window <= 0 || key > pos - A.window);
+            if (!seen) continue;
+            const float p = weights[k * 16 + l16];
+            const char* base = vb + static_cast<int64_t>(number) * page_stride + (at & in_page) * ts;
+#pragma unroll
+            for (int c = 0; c < L::VC; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {  // this lane's values of the row: 4 runs of VE
+                const T* v = reinterpret_cast<const T*>(base) + c * 16 * L::VE + (4 * g + e) * L::VE;
+#pragma unroll
+                for (int j = 0; j < L::VE; ++j) {
+                  const float x = to_f32<DT>(v[j]);
+                  if (!(fabsf(x) < __builtin_inff())) O[c * L::VE + j][e] += p * x;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+              }
+          }
+        }
       }
-    }
+    };
+    if constexpr (!kOrder) values(odd);
+    else if (__builtin_expect(odd, 0)) values(std::true_type{});
+    else values(std::false_type{});
     here = next;
   }
 
@@ -533,7 +573,7 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
     sm.stat[wave][l16][1] = l;
   }
   const int tid = threadIdx.x & 255, orow = tid & 15, om = tid >> 4;  // the row of each 16 and the 16th of its values that this thread writes
-  const int half = threadIdx.x >> 8;                                  // NW = 8: which of the accumulators
+  const int part_of = threadIdx.x >> 8;                               // NW = 8: which of the accumulators
 #pragma unroll
   for (int j0 = 0; j0 < L::kOut; j0 += GT) {
     if (!kOwn || j0 > 0) __syncthreads();  // the last tile, or what was joined before, has been read
@@ -546,16 +586,16 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
       if (out >= rows) continue;
       float top = kNegInf, sum = 0.f, f[KW];
 #pragma unroll
-      for (int k = 0; k < KW; ++k) top = fmaxf(top, sm.stat[RW > 1 ? w : k][orow][0]);
+      for (int k = 0; k < KW; ++k) top = fmaxf(top, sm.stat[w + RW * k][orow][0]);
 #pragma unroll
       for (int k = 0; k < KW; ++k) {
-        const float mw = sm.stat[RW > 1 ? w : k][orow][0];
+        const float mw = sm.stat[w + RW * k][orow][0];
         f[k] = mw == kNegInf ? 1.f : exp2_(mw - top);  // without a weight: zeros, or NaN
-        sum += sm.stat[RW > 1 ? w : k][orow][1] * f[k];
+        sum += sm.stat[w + RW * k][orow][1] * f[k];
       }
       const int ot = token_of(A, out), head = kh * share + out - ot * share;
       const int64_t line = (sp.lo + ot) * C.heads + head;
-      if (om == 0 && half == 0 && j0 == 0) {
+      if (om == 0 && part_of == 0 && j0 == 0) {
         if (part != nullptr) {
           part_stat[2 * (out - block0)] = top;
           part_stat[2 * (out - block0) + 1] = sum;
@@ -566,15 +606,15 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
       constexpr int kRun = L::VE, kRuns = GT / kRun;  // neighbouring values of a thread
 #pragma unroll
       for (int c = 0; c < kRuns; ++c) {
-        if (NW > kWaves && c % 2 != half && kRuns > 1) continue;
-        if (NW > kWaves && kRuns == 1 && half != 0) continue;
+        if (NW > kWaves && c % 2 != part_of && kRuns > 1) continue;
+        if (NW > kWaves && kRuns == 1 && part_of != 0) continue;
         float y[kRun];
 #pragma unroll
         for (int j = 0; j < kRun; ++j) {
           y[j] = 0.f;
 #pragma unroll
           for (int k = 0; k < KW; ++k)
-            y[j] = fmaf(reinterpret_cast<const float*>(&red[RW > 1 ? w : k][c * kRun + j][(om >> 2) * 16 + orow])[om & 3], f[k], y[j]);
+            y[j] = fmaf(reinterpret_cast<const float*>(&red[w + RW * k][c * kRun + j][(om >> 2) * 16 + orow])[om & 3], f[k], y[j]);
         }
         const int v = (j0 / kRun + c) * 16 * kRun + om * kRun;
         if (part != nullptr) {
@@ -608,7 +648,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void k_attend_whole(const AttendArgs 
 template <int DT, int D, int RW>
 __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend(const AttendArgs A) {
   __shared__ Shared<DT, D, RW, kWaves> sm;
-  constexpr int kStep = Tile<DT, D>::kKeys * kWaves / RW;
+  constexpr int kStep = Tile<DT, D, RW>::kKeys * (RW == 1 ? kWaves : 1);
   const CacheArgs& C = A.c;
   // neighbouring heads, whose keys lie side by side, run at the same time
   const int kh = static_cast<int>(blockIdx.x % C.key_heads), me = static_cast<int>(blockIdx.x / C.key_heads);
@@ -682,12 +722,11 @@ __global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_atten
   const unsigned rest = item / C.heads;
   const int token = static_cast<int>(rest % A.max_tokens), b = static_cast<int>(rest / A.max_tokens);
   if (b >= C.batch) return;
-  const Span sp = span_of(A, b);
-  if (token >= sp.n) return;
   const int kh = head / A.share, row = token * A.share + head - kh * A.share, rb = row / A.block_rows, in_block = row - rb * A.block_rows;
   const int32_t* note = A.notes + (static_cast<int64_t>(b) * A.row_blocks + rb) * 2;
-  const int first = note[0], parts = note[1] - first + 1;
-  if (parts == 1) return;
+  const int first = note[0], parts = note[1] - first + 1;  // loaded beside the offsets; of a request without this row nothing
+  const Span sp = span_of(A, b);
+  if (token >= sp.n || parts == 1) return;
   // part 0 in the second place of its workgroup, the others in the first of theirs
   auto place = [&](int s) { return ((static_cast<int64_t>(first + s) * C.key_heads + kh) * 2 + (s == 0 ? 1 : 0)) * A.block_rows + in_block; };
   float top = kNegInf, sum = 0.f, y[N] = {};
@@ -697,6 +736,10 @@ __global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_atten
     const int s = s0 + lane;
     const float* stat = A.stat + place(s) * 2;
     const float ms = s < s1 ? stat[0] : kNegInf, ls = s < s1 ? stat[1] : 0.f;
+    const int n = min(s1 - s0, kWave);
+    vec begin[4];  // the first four parts are loaded beside these
+#pragma unroll
+    for (int i = 0; i < 4; ++i) begin[i] = *reinterpret_cast<const vec*>(A.part + place(s0 + min(i, n - 1)) * D + lane * N);
     float now = ms;
 #pragma unroll
     for (int d = 1; d < 16; d *= 2) now = fmaxf(now, __shfl_xor(now, d, kWave));
@@ -707,11 +750,10 @@ __global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_atten
     sum = sum * old + wave_sum(ls * f);
 #pragma unroll
     for (int e = 0; e < N; ++e) y[e] *= old;
-    const int n = min(s1 - s0, kWave);
     for (int i0 = 0; i0 < n; i0 += 4) {  // four at a time, the last again where there are fewer
       vec x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const vec*>(A.part + place(s0 + min(i0 + i, n - 1)) * D + lane * N);
+      for (int i = 0; i < 4; ++i) x[i] = i0 == 0 ? begin[i] : *reinterpret_cast<const vec*>(A.part + place(s0 + min(i0 + i, n - 1)) * D + lane * N);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float fi = i0 + i < n ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), min(i0 + i, n - 1))) : 0.f;
@@ -754,19 +796,22 @@ namespace {
 
 template <int DT, int D>
 hipError_t attend(const AttendArgs& a, hipStream_t s) {
-  constexpr bool kWide = Tile<DT, D>::kRow > 512;  // as in plan_attend
+  constexpr bool kWide = Tile<DT, D, 1>::kRow > 512;                            // as in plan_attend:
+  constexpr int kTwo = Tile<DT, D, 2>::kSub >= 2 * Tile<DT, D, 2>::kGroup ? 2 : kWaves;  // row blocks of up to 32 rows
   const int64_t heads = a.c.key_heads;
   const dim3 threads(kWaves * kWave);
   if constexpr (!kWide) {
     if (a.groups == 0) {
       const dim3 grid(static_cast<unsigned>(a.c.batch * heads * a.row_blocks));
       if (a.row_waves == 1) k_attend_whole<DT, D, 1, kMany><<<grid, dim3(kMany * kWave), 0, s>>>(a);
+      else if (a.row_waves == 2) k_attend_whole<DT, D, kTwo, kWaves><<<grid, threads, 0, s>>>(a);
       else k_attend_whole<DT, D, kWaves, kWaves><<<grid, threads, 0, s>>>(a);
       return hipGetLastError();
     }
   }
   const dim3 grid(static_cast<unsigned>(a.groups * heads));
-  if (kWide || a.row_waves > 1) k_attend<DT, D, kWaves><<<grid, threads, 0, s>>>(a);
+  if (kWide || a.row_waves == kWaves) k_attend<DT, D, kWaves><<<grid, threads, 0, s>>>(a);
+  else if (a.row_waves == 2) k_attend<DT, D, kTwo><<<grid, threads, 0, s>>>(a);
   else k_attend<DT, D, kWide ? kWaves : 1><<<grid, threads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -795,10 +840,11 @@ bool plan_attend(int32_t io_dtype, AttendArgs& a) {
   // 97 from 121. Not fp32 of 256 values, which a wavefront has no registers for: 8 requests of 20000 keys 75 from 96
   // with shared tiles; nor are those ever faster in one launch (120 keys: 13 us from 17).
   const bool wide = row_bytes > 512;
-  a.row_waves = rows <= 16 && !wide ? 1 : kWaves;
+  const int64_t shared = kShared / row_bytes;  // keys of a tile that wavefronts share
+  a.row_waves = rows <= 16 && !wide ? 1 : rows <= 32 && shared >= 2 * tile ? 2 : kWaves;
   a.block_rows = static_cast<int32_t>(std::min(rows, int64_t{16} * a.row_waves));
   a.row_blocks = static_cast<int32_t>((rows + a.block_rows - 1) / a.block_rows);
-  const int64_t step = a.row_waves == 1 ? tile * kWaves : tile;  // keys of one turn of a workgroup
+  const int64_t step = a.row_waves == 1 ? tile * kWaves : shared;  // keys of one turn of a workgroup
   int64_t span = a.capacity;
   if (a.window > 0) span = std::min(span, static_cast<int64_t>(a.window) + a.max_tokens - 1 + 31);
   const int64_t turns = static_cast<int64_t>(a.c.batch) * a.row_blocks * ((span + step - 1) / step);  // at most, of a key head
