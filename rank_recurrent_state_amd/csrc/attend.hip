@@ -835,10 +835,12 @@ hipError_t pick(const AttendArgs& a, hipStream_t s) {
 bool plan_attend(int32_t io_dtype, AttendArgs& a) {
   const int64_t rows = static_cast<int64_t>(a.max_tokens) * a.share, tile = io_dtype == SEED_BF16 ? 32 : 16;
   const int64_t row_bytes = static_cast<int64_t>(a.c.dim) * (io_dtype == SEED_BF16 ? 2 : 4);
-  // Up to 16 rows are one matrix tile's, and the wavefronts take keys of their own: against rows over wavefronts,
-  // 16 requests of 4096 keys of 128 values 31 us from 34, 64 of 3000 keys of 64 values 23 from 33, 32 of 5000 in fp32
-  // 97 from 121. Not fp32 of 256 values, which a wavefront has no registers for: 8 requests of 20000 keys 75 from 96
-  // with shared tiles; nor are those ever faster in one launch (120 keys: 13 us from 17).
+  // Up to 16 rows are one matrix tile's, and the wavefronts take keys of their own: against shared tiles, 16 requests
+  // of 4096 keys of 128 values 31 us from 34, 64 of 3000 keys of 64 values 23 from 33, 32 of 5000 in fp32 97 from 121. Not
+  // fp32 of 256 values, which a wavefront has no registers for: 8 requests of 20000 keys 75 from 96 with shared
+  // tiles; nor are those faster in one launch (120 keys: 13 us from 17). Up to 32 rows: two wavefronts for each half of
+  // a tile that has two products' keys (48 requests, 32 rows: fp32 240 from 353, 64 values 136 from 177; 128 values
+  // the same within 4 %).
   const bool wide = row_bytes > 512;
   const int64_t shared = kShared / row_bytes;  // keys of a tile that wavefronts share
   a.row_waves = rows <= 16 && !wide ? 1 : rows <= 32 && shared >= 2 * tile ? 2 : kWaves;
@@ -850,12 +852,15 @@ bool plan_attend(int32_t io_dtype, AttendArgs& a) {
   const int64_t turns = static_cast<int64_t>(a.c.batch) * a.row_blocks * ((span + step - 1) / step);  // at most, of a key head
   if (turns >= int64_t{1} << 30) return false;
   // Short spans in one launch, a workgroup each. One request of 300 keys: 7.4 us from 11.4 with shares and a join;
-  // 64 requests of 1000 keys: 30 both; of 2000: 56 from 49 the other way. Rows over wavefronts take the keys one
-  // tile after another, so that where units leave compute units idle only a few are as fast: 8 requests of 6
-  // tokens over 256 keys 13 us, cut 11 (and 4 us of host time more), over 512 keys 21 and 13; but 64 of 512 keys
-  // 24 from 36, of 1000 39 from 44, of 2000 85 and 61.
-  const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * a.row_blocks;
-  const int64_t few = wide ? 0 : a.row_waves == 1 ? std::min(4 * tile * kMany, (int64_t{256} << 10) / row_bytes) : (units >= 512 ? 32 : 8) * step;
+  // 64 requests of 1000 keys: 30 both; of 2000: 56 from 49 the other way. Wavefronts that share a tile take the keys one tile
+  // after another: few are as fast where the units leave compute units idle, and more the more units there are, whose
+  // requests the shares cut and join. 6 tokens of one request, 8 key heads: 250 keys (4 turns) 10.3 us, cut 12.1, 500 keys
+  // 15.6 and 12.4; of 64 requests: 1000 keys 31, cut 39, 2000 keys (31 turns) 64 and 60; of 256: 2000 keys 175, cut
+  // 198. fp32, whose products take longer: of 64 requests 500 keys (16 turns) 47, cut 52, 1000 keys 77 and 71.
+  const int64_t units = static_cast<int64_t>(a.c.batch) * a.c.key_heads * a.row_blocks, per_turn = io_dtype == SEED_BF16 ? 16 : 32;
+  const int64_t few = wide               ? 0
+                      : a.row_waves == 1 ? std::min(4 * tile * kMany, (int64_t{256} << 10) / row_bytes)
+                                         : std::min(std::max(units / per_turn, int64_t{4}), int64_t{64}) * step;
   a.groups = 0;
   if (span <= few) return true;
   a.groups = static_cast<int32_t>(std::max(std::min((kGroups + a.c.key_heads - 1) / a.c.key_heads, turns), int64_t{1}));
