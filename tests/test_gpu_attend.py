@@ -478,6 +478,113 @@ def test_graph_replays():
             assert torch.equal(o, want) and torch.equal(lse, wl) and torch.equal(qo, wq)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("share,most", [(5, 3), (7, 4), (6, 8), (11, 7)])
+@pytest.mark.parametrize("lengths", [[97, 30, 100], [1999, 33, 700]])
+@pytest.mark.parametrize("window", [0, 45])
+def test_row_counts(dtype, dim, share, most, lengths, window):
+    """Up to 16, 32, 64 and more rows of a key head, over caches that stay whole and that are cut: a page that is not
+    there, NaN wherever no row looks, and an infinity that only its own column shows."""
+    rrs, torch = _rrs()
+    new, heads = [most, 1, most - 1], 2 * share
+    cache = _cache(rrs, torch, lengths, 2, dim, 16, dtype, dim + share)
+    cache.table[2, 1] = -1
+    cache.table[0, (lengths[0] - most - 20) // 16] = 1 << 20
+    clean = rrs.Cache(cache.k.clone(), cache.v.clone(), cache.table)
+    keep = torch.zeros(cache.k.shape[:2], dtype=torch.bool, device="cuda")
+    for b, n in enumerate(lengths):
+        j = torch.arange(max(0, n - new[b] + 1 - window) if window else 0, n, device="cuda")
+        number = cache.table[b].long()[j // 16]
+        there = (number >= 0) & (number < len(cache.k))
+        keep[number[there], j[there] % 16] = True
+    cache.k[~keep] = float("nan")
+    cache.v[~keep] = float("nan")
+    o, lse = _check(rrs, torch, cache, dtype, new, lengths, heads, lead=1, window=window)
+    o2, lse2 = _check(rrs, torch, clean, dtype, new, lengths, heads, lead=1, window=window)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    # the last but one position of the first request, key head 1: its last two tokens' rows see it
+    at = lengths[0] - 2
+    cache.v[int(cache.table[0, at // 16]), at % 16, 1, dim - 3] = float("inf")
+    q = torch.randn(1 + sum(new) + 2, heads, dim, generator=_gen(torch, 1), device="cuda").to(cache.k.dtype)
+    got = torch.full_like(q, 7.0)
+    rrs.seed_decode_attend(cache, _i32(torch, lengths), q, got, offsets=_offsets(torch, new, 1), max_tokens=most, window=window)
+    rows = slice(1 + most - 2, 1 + most)
+    assert (got[rows, share:, dim - 3] == float("inf")).all()
+    got[rows, share:, dim - 3] = o[rows, share:, dim - 3]
+    assert torch.equal(got, o)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("share,most", [(4, 6), (8, 6)])
+def test_large_scores_of_drafts(dtype, share, most):
+    """A maximum that grows along the cache, and a falling one, over wavefronts that share tiles."""
+    rrs, torch = _rrs()
+    lengths = [1500, 1500]
+    for dim in (64, 128, 256):
+        cache = _cache(rrs, torch, lengths, 1, dim, 16, dtype, 6)
+        for b, ramp in enumerate((torch.linspace(-3, 3, 1500), torch.linspace(3, -3, 1500))):
+            j = torch.arange(1500, device="cuda")
+            number = cache.table[b].long()[j // 16]
+            cache.k[number, j % 16, 0] = (cache.k[number, j % 16, 0].float() * 0.1 + ramp.cuda()[:, None]).to(cache.k.dtype)
+        q = torch.ones(2 * most + 2, share, dim, device="cuda").to(cache.k.dtype)
+        _check(rrs, torch, cache, dtype, [most, most], lengths, share, scale=0.25, q=q)
+        _check(rrs, torch, cache, dtype, [most, most], lengths, share, scale=-0.25, q=q)
+
+
+def test_two_streams_and_graphs_of_drafts():
+    """Two batches' drafts at once on two streams, each with a workspace of its own, and both captured and replayed over
+    growing lengths: the bits of the calls one by one."""
+    rrs, torch = _rrs()
+    new, heads, dim = [6, 0, 3, 5], 16, 128
+    off, most = _offsets(torch, new), 6
+    sets = []
+    for i, lengths in enumerate(([5000, 40, 3, 9000], [64, 7000, 2100, 300])):
+        cache = _cache(rrs, torch, [n + 100 for n in lengths], 2, dim, 16, "bf16", 20 + i)
+        q = torch.randn(sum(new), heads, dim, generator=_gen(torch, i), device="cuda").bfloat16()
+        need = rrs.seed_attend_workspace_bytes(cache, sum(new), heads, max_tokens=most, ragged=True)
+        sets.append(dict(cache=cache, lengths=_i32(torch, lengths), q=q, ws=torch.empty(need, dtype=torch.uint8, device="cuda"),
+                         o=torch.empty_like(q), lse=torch.empty(sum(new), heads, device="cuda"), stream=torch.cuda.Stream()))
+
+    def call(s, **kw):
+        rrs.seed_decode_attend(s["cache"], s["lengths"], s["q"], s["o"], offsets=off, max_tokens=most, lse=s["lse"], **kw)
+
+    def results():
+        torch.cuda.synchronize()
+        return [(s["o"].clone(), s["lse"].clone()) for s in sets]
+
+    graphs = []
+    for s in sets:
+        call(s)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s["stream"]):
+            call(s, ws=s["ws"])
+        graphs.append(g)
+    for turn in range(5):
+        for s in sets:
+            s["lengths"] += 7
+            s["q"].normal_()
+            call(s)
+        want = results()
+        for s in sets:
+            s["o"].fill_(3.0)
+            s["stream"].wait_stream(torch.cuda.current_stream())
+        for _ in range(3):
+            for s in sets:
+                call(s, ws=s["ws"], stream=s["stream"])
+        got = results()
+        for s in sets:
+            s["o"].fill_(3.0)
+        torch.cuda.synchronize()
+        for s, g in zip(sets, graphs):
+            with torch.cuda.stream(s["stream"]):
+                g.replay()
+        again = results()
+        for a, b, c in zip(want, got, again):
+            assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(a, b, c))
+
+
 def test_parts_of_a_context_join_by_lse():
     """Two halves of a context, attended apart and joined by their lse, are the whole."""
     rrs, torch = _rrs()
