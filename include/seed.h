@@ -548,7 +548,8 @@ typedef struct seed_rotary_scaling {
   double low, high;  /* 0 < low < high (PARTS and INDEX; ignored by the others) */
 } seed_rotary_scaling;
 
-/* Fills turns[0 .. dim / 2 - 1] in HOST memory (the caller copies it to the device once). Host-only, pure. */
+/* Fills turns[0 .. dim / 2 - 1] in HOST memory (the caller copies it to the device once); SEED_ERR_ARG where one is
+ * not finite. Host-only, pure. */
 int seed_rotary_turns(const seed_rotary_scaling *scaling, int32_t dim, double *turns);
 
 /*
@@ -565,7 +566,7 @@ int seed_rotate_rows(const seed_rows *rows, const seed_rotary *rotary, const voi
  * head h of a slot is `dim` contiguous values at k (or v) + page_stride number + token_stride slot + head_stride h.
  * Pages are [page][key_heads][dim] (token_stride >= key_heads head_stride) or [key_heads][page][dim] (head_stride >=
  * page token_stride), without overlaps inside a page or between pages (else SEED_ERR_ARG), token_stride at most 2^24
- * (else SEED_ERR_UNSUPPORTED); k and v have the same strides and may lie side by side in one buffer.
+ * elements (else SEED_ERR_UNSUPPORTED); k and v have the same strides and may lie side by side in one buffer.
  * table entries are read on the device where a position needs them, and not checked on the host: one outside
  * 0 .. pages - 1 is a page that is not there. A page may be listed by several requests (a shared
  * prefix); only pages that receive new rows must belong to one.
@@ -592,7 +593,7 @@ typedef struct seed_tokens {
   int64_t tokens;          /* rows of the row buffers                                            */
   const int32_t *offsets;  /* [batch + 1], device memory, or NULL                                */
   const int32_t *lengths;  /* [batch], device memory                                             */
-  int32_t heads;           /* heads of the queries: a multiple of key_heads                      */
+  int32_t heads;           /* heads of the queries: a multiple of key_heads (attention: at most 2^14 times) */
   int64_t q_stride, k_stride, v_stride, o_stride;  /* elements between rows; of absent buffers ignored */
 } seed_tokens;
 
@@ -609,14 +610,14 @@ int seed_cache_append(const seed_cache *cache, const seed_tokens *tokens, const 
 
 /* Which keys a call's rows see, and the limits that set its launch. */
 typedef struct seed_attend {
-  int32_t max_tokens;  /* most new tokens of a request, 1 .. 32; a request's rows behind are not written */
+  int32_t max_tokens;  /* most new tokens of a request, 1 .. 32 (more: SEED_ERR_UNSUPPORTED); a request's rows behind are not written */
   int32_t max_length;  /* most tokens of a request: larger lengths are taken as this one; at most page * width */
   int32_t window;      /* > 0: a row sees its own position and the window - 1 before it; 0: all */
   float scale;         /* of the products q . k; finite and not 0                                */
 } seed_attend;
 
-/* Workspace bytes of seed_decode_attend (0: none needed, or invalid arguments). Depends on the sizes
- * only. Host-only, pure. */
+/* Workspace bytes of seed_decode_attend (0: none needed, or invalid arguments): at most 512 row blocks of partial
+ * results per key head's share, independent of the lengths. Host-only, pure. */
 size_t seed_attend_workspace_bytes(const seed_cache *cache, const seed_tokens *tokens, const seed_attend *attend);
 
 /*
@@ -630,9 +631,10 @@ size_t seed_attend_workspace_bytes(const seed_cache *cache, const seed_tokens *t
  *   lse    float [tokens][heads], written, or NULL.
  *   ws     workspace of seed_attend_workspace_bytes bytes, 16-byte aligned (NULL when that is 0); it must
  *          not be shared by calls that may run at the same time.
- * Long caches of few requests are split over their length and joined (by the sizes: max_length, not lengths, sets
- * the cut, so a max_length close to the longest request's is faster than a far one). Weights and sums are fp32;
- * bf16 weights enter the products in two pieces. The same call gives the same bits.
+ * Short caches (by max_length and the other sizes) are one launch; the keys of longer ones are cut into equal shares
+ * by the requests' lengths, on the device, and joined by a second launch. max_length may be far above the lengths;
+ * close to short ones it saves the second launch and the workspace. Weights and sums are fp32; bf16 weights enter the
+ * products in two pieces. The same call gives the same bits, on any stream and in a replayed graph too.
  */
 int seed_decode_attend(const seed_cache *cache, const seed_tokens *tokens, const seed_attend *attend, const void *q,
                        void *o, float *lse, void *ws, size_t ws_bytes, void *stream);

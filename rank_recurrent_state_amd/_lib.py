@@ -916,7 +916,8 @@ def seed_decode_attend(cache: Cache, lengths, q, o, offsets=None, max_tokens: in
                        scale: float | None = None, window: int = 0, lse=None, ws=None, stream=None) -> None:
     """Attention of every request's new tokens, q [tokens, heads, dim] (rows may be strided), over its cache,
     which holds them already, into o. lengths, offsets: as for seed_cache_append; max_tokens: the most new tokens
-    of a request; max_length: the most tokens of a request (None: what the table holds); scale: None for
+    of a request; max_length: the most tokens of a request (None: what the table holds; where all requests are
+    short, one close to them saves a launch); scale: None for
     1 / sqrt(dim); window: positions a row sees, 0 for all; lse: float [tokens, heads] or None. ws: a workspace
     of seed_attend_workspace_bytes bytes; without one, one is taken from torch's allocator when needed."""
     torch, _ = _io()
@@ -942,7 +943,8 @@ def seed_decode_attend(cache: Cache, lengths, q, o, offsets=None, max_tokens: in
         if need is None:
             if len(cache.need) >= 1024:  # a serving loop's ever new sizes
                 cache.need.clear()
-            need = cache.need[key] = LIB.seed_attend_workspace_bytes(cache.ref, new, how)
+            sizes = ctypes.byref(seed_attend(max_tokens, max_length, window, 1.0))  # the key's only: not a scale that is refused
+            need = cache.need[key] = LIB.seed_attend_workspace_bytes(cache.ref, new, sizes)
     wp, size, ws = a.workspace(need, ws, stream)
     a.launch("seed_decode_attend", stream, cache.ref, new, how, qp, op, lp, wp, size)
 

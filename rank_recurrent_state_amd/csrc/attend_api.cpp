@@ -185,6 +185,7 @@ int seed_rotary_turns(const seed_rotary_scaling* s, int32_t dim, double* turns) 
       keep = fmin(fmax(keep, 0.0), 1.0);
       t *= keep + (1.0 - keep) / s->factor;
     }
+    if (!isfinite(t)) return SEED_ERR_ARG;  // a base or factor next to 0
     turns[i] = t;
   }
   return SEED_OK;

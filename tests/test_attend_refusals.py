@@ -60,6 +60,8 @@ def test_turns_refusals():
         assert call(**bad) == r.SEED_ERR_ARG, bad
     assert call(factor=0.0, length=-1.0, low=9.0, high=1.0) == r.SEED_OK  # ignored by a plain table
     assert call(kind=1, length=-1.0, low=9.0, high=1.0) == r.SEED_OK
+    # turns beyond fp64
+    assert call(kind=1, factor=5e-324) == r.SEED_ERR_ARG and call(kind=2, factor=1e-300, dim=4) == r.SEED_ERR_ARG
 
 
 def _rotary(r, dim=64, interleaved=0, amplitude=1.0, turns=5 * FAR):

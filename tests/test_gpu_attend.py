@@ -412,6 +412,18 @@ def test_limits_of_the_call():
         assert torch.isfinite(o.float()).all()
 
 
+def test_a_refused_call_leaves_no_trace():
+    """A scale of 0 is refused; the same call with another one runs."""
+    rrs, torch = _rrs()
+    cache = _cache(rrs, torch, [9000], 2, 128, 16, "bf16", 2)
+    q = torch.randn(1, 8, 128, device="cuda").bfloat16()
+    o = torch.full_like(q, 7.0)
+    with pytest.raises(rrs.SeedError):
+        rrs.seed_decode_attend(cache, _i32(torch, [9000]), q, o, scale=0.0)
+    assert (o == 7.0).all()
+    _check(rrs, torch, cache, "bf16", [1], [9000], 8, ragged=False, q=q)
+
+
 def test_strided_rows_and_workspace():
     """q and o as column ranges of wider rows, a workspace of the caller's, another stream: the same bits."""
     rrs, torch = _rrs()
