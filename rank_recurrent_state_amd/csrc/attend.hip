@@ -11,12 +11,13 @@
 //                 16-bit values are paired by key with byte permutes.
 // Keys are loaded as whole rows and pass through LDS to where the product takes them. Up to 16 rows: every wavefront
 // has keys of its own, and its values go straight to registers; the wavefronts are joined at the end. More: 4
-// wavefronts have 16 rows each and share two tiles of keys and values in LDS, each loading a quarter of the next.
-// The keys of all requests are cut into equal shares for two workgroups per compute unit, whose partial results
-// a second launch joins; short ones stay whole and need no second launch.
+// wavefronts share tiles of 16 KB of keys and as many of values, each loading a quarter of the next, for 4 row blocks or
+// for 2 by halves of the tile. The keys of all requests are cut into equal shares for two workgroups per compute
+// unit, whose partial results a second launch joins; short ones stay whole and need no second launch.
 // Measured: 64 requests of up to 16384 tokens, 8 key heads of 128, 1.75 GB: 286 us, 6.1 TB/s (the kernel alone 6.2; a
-// kernel that only reads such pages 6.5 - 6.7); one request of 131072 tokens 92 us, 5.9 TB/s; 6 tokens of 48 requests
-// (48 rows of a key head of 256), 298 MB: 73 us, 4.1 TB/s, where partial results and their join take the rest.
+// kernel that only reads such pages 6.5 - 6.7); one request of 131072 tokens 92 us, 5.8 TB/s; 6 tokens of 48 requests
+// (48 rows of a key head of 256), 298 MB: 72 us, 4.2 TB/s, of which the join takes 8 and the first tiles' way 6; the loop
+// between reads 7.
 // bf16 weights enter as two pieces (p and p - bf16(p)), so that o is off by its own rounding only: with one
 // piece the weights' rounding, 2^-9 each, is as large as o's. The products are far from the matrix unit's rate.
 // m is only moved when a score passes it by 8 (weights up to 2^8): most tiles then need no exchange between

@@ -8,6 +8,9 @@
 // segment that holds the draw is read again and its tokens are walked. Every wavefront finds the request's first
 // refused row by itself, from a few gathered values, and no step needs more than one wavefront: a row that one
 // workgroup reads as fast as a second launch takes is summed and walked by it, larger ones in two launches.
+// Measured: 128 requests, 150001 tokens, fp32, 154 MB: 25 us, 6.2 TB/s; 200 requests, 65536 tokens, bf16, no drafts'
+// probabilities, 26 MB: 14 us, of which the sums take 10: four loads one after another lead to a row, and the rows
+// are short. Two segments a wavefront at once: the same or up to 1 us more.
 #include "attend.hpp"
 #include "common.hpp"
 
@@ -19,8 +22,9 @@ constexpr int kRun = 16;                  // tokens of a lane
 constexpr int kSegment = kWave * kRun;    // and of a segment
 constexpr int kWaves = 4;                 // of a workgroup that sums
 constexpr int kMany = 16;                 // of one that does a request alone
-constexpr int kMost = 32;                 // segments of such a request
-constexpr int kPair = 2;                  // segments that a wavefront loads at once
+// Segments of such a request. One request of 16384 fp32 tokens: 7.1 us, in two launches 8.2; of 32768: 8.4 and 8.6; of
+// 65536: 11 and 8. 64 of 16384: 8 and 10; of 32768: 12 and 10; 200 of 32768: 13 and 14.
+constexpr int kMost = 32;
 
 // 16 bytes at any address that holds a value: rows of an odd length start anywhere.
 template <int DT> struct Any16;
@@ -158,19 +162,15 @@ __device__ __forceinline__ double sum_before(double v, double& total) {
   return lane == 0 ? 0.0 : above;
 }
 
-// Sums of K neighbouring segments' weights.
-template <int DT, int K>
-__device__ __forceinline__ void sum_segments(const Weights<DT>& W, int seg, int vocab, double (&s)[K]) {
+// Sum of a segment's weights.
+template <int DT>
+__device__ __forceinline__ double sum_segment(const Weights<DT>& W, int seg, int vocab) {
   constexpr int N = Weights<DT>::N;
-  double w[K * kRun];
-  W.template load<K * kRun / N>(seg * kSegment + (static_cast<int>(threadIdx.x) & 63) * N, kWave * N, vocab, (seg + K) * kSegment <= vocab, w);
+  double w[kRun], s = 0.0;
+  W.template load<kRun / N>(seg * kSegment + (static_cast<int>(threadIdx.x) & 63) * N, kWave * N, vocab, (seg + 1) * kSegment <= vocab, w);
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    s[k] = 0.0;
-#pragma unroll
-    for (int e = 0; e < kRun; ++e) s[k] += w[k * kRun + e];
-    s[k] = wave_sum64(s[k]);
-  }
+  for (int e = 0; e < kRun; ++e) s += w[e];
+  return wave_sum64(s);
 }
 
 // The token of segment seg that passes target, base the sum of the segments before; where none does (passes: whether
@@ -200,20 +200,20 @@ __device__ __forceinline__ int walk(const Weights<DT>& W, int seg, int vocab, do
 template <int DT>
 __device__ __noinline__ int pick_plain(const stor_t<DT>* p, int segments, int vocab, double draw) {
   const Weights<DT> W{p, nullptr, -1};
-  double total = 0.0, s[1];
+  double total = 0.0;
   int last = -1;
   for (int i = 0; i < segments; ++i) {
-    sum_segments<DT, 1>(W, i, vocab, s);
-    total += s[0];
-    if (s[0] > 0.0) last = i;
+    const double s = sum_segment<DT>(W, i, vocab);
+    total += s;
+    if (s > 0.0) last = i;
   }
   if (last < 0) return -1;
   const double target = draw * total;
   double c = 0.0;
   for (int i = 0; i < segments; ++i) {
-    sum_segments<DT, 1>(W, i, vocab, s);
-    if (s[0] > 0.0 && c + s[0] > target) return walk<DT>(W, i, vocab, c, target, true);
-    c += s[0];
+    const double s = sum_segment<DT>(W, i, vocab);
+    if (s > 0.0 && c + s > target) return walk<DT>(W, i, vocab, c, target, true);
+    c += s;
   }
   return walk<DT>(W, last, vocab, c, target, false);
 }
@@ -254,22 +254,19 @@ __device__ __forceinline__ void finish(const VerifyArgs& A, int b, int64_t lo, i
 
 }  // namespace
 
-// A wavefront per kPair segments.
+// A wavefront per segment.
 template <int DT>
 __global__ __launch_bounds__(kWaves* kWave) void k_verify_sums(const VerifyArgs A) {
-  const int groups = (A.segments + kWaves * kPair - 1) / (kWaves * kPair);
+  const int groups = (A.segments + kWaves - 1) / kWaves;
   const int b = static_cast<int>(blockIdx.x / groups);
-  const int seg = (static_cast<int>(blockIdx.x % groups) * kWaves + static_cast<int>(threadIdx.x >> 6)) * kPair;
+  const int seg = static_cast<int>(blockIdx.x % groups) * kWaves + static_cast<int>(threadIdx.x >> 6);
   int64_t lo, hi;
   sequence_rows(A.offsets, b, A.rows, lo, hi);
   if (lo >= hi || seg >= A.segments) return;
   const int64_t row = first_refused<DT>(A, lo, hi);
-  double s[kPair];
-  sum_segments<DT, kPair>(weights_at<DT>(A, row, hi), seg, A.vocab, s);
+  const double sum = sum_segment<DT>(weights_at<DT>(A, row, hi), seg, A.vocab);
   if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-    for (int k = 0; k < kPair; ++k)
-      if (seg + k < A.segments) A.sums[static_cast<int64_t>(b) * A.segments + seg + k] = s[k];
+    A.sums[static_cast<int64_t>(b) * A.segments + seg] = sum;
     if (seg == 0) A.kept[b] = static_cast<int32_t>(row - lo);
   }
 }
@@ -294,7 +291,7 @@ __global__ __launch_bounds__(kWave) void k_verify_pick(const VerifyArgs A) {
 // A workgroup per request, the sums in LDS.
 template <int DT>
 __global__ __launch_bounds__(kMany* kWave) void k_verify_whole(const VerifyArgs A) {
-  __shared__ double sums[kMost + kPair];
+  __shared__ double sums[kMost];
   const int b = blockIdx.x, wave = threadIdx.x >> 6;
   const double draw = A.draws[b];
   int64_t lo, hi;
@@ -305,13 +302,9 @@ __global__ __launch_bounds__(kMany* kWave) void k_verify_whole(const VerifyArgs 
   }
   const int64_t row = first_refused<DT>(A, lo, hi);
   const Weights<DT> W = weights_at<DT>(A, row, hi);
-  for (int seg = wave * kPair; seg < A.segments; seg += kMany * kPair) {
-    double s[kPair];
-    sum_segments<DT, kPair>(W, seg, A.vocab, s);
-    if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-      for (int k = 0; k < kPair; ++k) sums[seg + k] = s[k];
-    }
+  for (int seg = wave; seg < A.segments; seg += kMany) {
+    const double sum = sum_segment<DT>(W, seg, A.vocab);
+    if ((threadIdx.x & 63) == 0) sums[seg] = sum;
   }
   __syncthreads();
   if (wave != 0) return;
@@ -326,7 +319,7 @@ hipError_t verify(const VerifyArgs& a, hipStream_t s) {
     k_verify_whole<DT><<<dim3(static_cast<unsigned>(a.batch)), dim3(kMany * kWave), 0, s>>>(a);
     return hipGetLastError();
   }
-  const int64_t groups = (a.segments + kWaves * kPair - 1) / (kWaves * kPair);
+  const int64_t groups = (a.segments + kWaves - 1) / kWaves;
   k_verify_sums<DT><<<dim3(static_cast<unsigned>(a.batch * groups)), dim3(kWaves * kWave), 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
