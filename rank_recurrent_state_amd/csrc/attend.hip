@@ -658,31 +658,47 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend(const AttendArgs A
     const Span sp = span_of(A, min(i, C.batch - 1));
     return i < C.batch ? sp.turns(kStep) * ((sp.n * A.share + 16 * RW - 1) / (16 * RW)) : 0;
   };
-  // every wavefront for itself: the sum of all turns, then the request in which this share begins
-  int total = 0, here = 0;
-  int mine = turns(lane), run = scan(mine, lane, here);
-  total = here;
-  for (int i = kWave; i < C.batch; i += kWave) {
-    int more;
-    scan(turns(i + lane), lane, more);
-    total += more;
-  }
-  const int share = share_of(total, A.groups), w0 = me * share, w1 = min(w0 + share, total);
-  if (w0 >= total) return;
-  int b = 0, begin = 0;  // request, and its first turn
-  for (;;) {
-    const uint64_t past = __ballot(begin + run > w0);
-    if (past != 0) {
-      const int at = __builtin_ctzll(past);
-      begin += __builtin_amdgcn_readlane(run - mine, at);
-      b += at;
-      break;
+  // every wavefront for itself: the sum of all turns, then the request in which this share begins. The lengths of up to
+  // 256 requests are loaded at once (64 at a time: up to 2 us more for 256 requests; at once for one: 1 us more).
+  int share = 0, w0 = 0, w1 = 0, b = -1, begin = 0;  // request, and its first turn
+  auto find_share = [&](auto at_once) {
+    constexpr int kAt = decltype(at_once)::value;
+    int mine[kAt], run[kAt], sums[kAt], loaded = 0, total = 0;
+    auto read = [&](int first) {
+      loaded = first;
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) mine[j] = turns(first + j * kWave + lane);
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) run[j] = scan(mine[j], lane, sums[j]);
+    };
+    for (int i = 0; i < C.batch; i += kAt * kWave) {
+      read(i);
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) total += sums[j];
     }
-    begin += here;
-    b += kWave;
-    mine = turns(b + lane);
-    run = scan(mine, lane, here);
-  }
+    share = share_of(total, A.groups);
+    w0 = me * share;
+    w1 = min(w0 + share, total);
+    if (w0 >= total) return;
+    if (loaded != 0) read(0);
+    for (;;) {
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        const uint64_t past = __ballot(begin + run[j] > w0);
+        if (b < 0 && past != 0) {
+          const int at = __builtin_ctzll(past);
+          begin += __builtin_amdgcn_readlane(run[j] - mine[j], at);
+          b = loaded + j * kWave + at;
+        }
+        if (b < 0) begin += sums[j];
+      }
+      if (b >= 0) break;
+      read(loaded + kAt * kWave);
+    }
+  };
+  if (C.batch <= kWave) find_share(std::integral_constant<int, 1>{});
+  else find_share(std::integral_constant<int, 4>{});
+  if (w0 >= w1) return;
   Span sp = span_of(A, b);
   for (int w = w0; w < w1;) {
     const int each = sp.turns(kStep), blocks = (sp.n * A.share + 16 * RW - 1) / (16 * RW);
@@ -707,90 +723,92 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend(const AttendArgs A
   }
 }
 
-// Joins the parts of the rows that more than one workgroup has: WR wavefronts per row and head, a lane D / 64 of
-// its values.
+// Joins the parts of the rows that more than one workgroup has: a workgroup per request, row block, key head and
+// `each` rows (WR > 1: one), WR wavefronts per row, a lane D / 64 of its values.
 template <int DT, int D, int WR>
-__global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_attend_join(const AttendArgs A) {
+__global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_attend_join(const AttendArgs A, int each) {
   using T = stor_t<DT>;
-  constexpr int N = D / kWave, kRows = WR == 1 ? kWaves : 1;
+  constexpr int N = D / kWave;
   using vec = __attribute__((ext_vector_type(N))) float;
   __shared__ float acc[WR][D];
   __shared__ float stats[WR][2];
   const CacheArgs& C = A.c;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const unsigned item = blockIdx.x * kRows + (WR == 1 ? wave : 0);
-  const int head = static_cast<int>(item % C.heads);
-  const unsigned rest = item / C.heads;
-  const int token = static_cast<int>(rest % A.max_tokens), b = static_cast<int>(rest / A.max_tokens);
-  if (b >= C.batch) return;
-  const int kh = head / A.share, row = token * A.share + head - kh * A.share, rb = row / A.block_rows, in_block = row - rb * A.block_rows;
-  const int32_t* note = A.notes + (static_cast<int64_t>(b) * A.row_blocks + rb) * 2;
-  const int first = note[0], parts = note[1] - first + 1;  // loaded beside the offsets; of a request without this row nothing
+  const int chunks = (A.block_rows + each - 1) / each;
+  const int chunk = static_cast<int>(blockIdx.x % chunks);
+  const unsigned rest = blockIdx.x / chunks, block = rest / C.key_heads;
+  const int kh = static_cast<int>(rest % C.key_heads), b = static_cast<int>(block / A.row_blocks), rb = static_cast<int>(block % A.row_blocks);
+  const int32_t* note = A.notes + static_cast<int64_t>(block) * 2;
+  const int first = note[0], parts = note[1] - first + 1;  // loaded beside the offsets; of a request without these rows nothing
   const Span sp = span_of(A, b);
-  if (token >= sp.n || parts == 1) return;
-  // part 0 in the second place of its workgroup, the others in the first of theirs
-  auto place = [&](int s) { return ((static_cast<int64_t>(first + s) * C.key_heads + kh) * 2 + (s == 0 ? 1 : 0)) * A.block_rows + in_block; };
-  float top = kNegInf, sum = 0.f, y[N] = {};
-  // up to 64 parts at a time, a lane's maximum and sum each; several wavefronts take a run of parts each
-  const int per = WR == 1 ? parts : (parts + WR - 1) / WR, s1 = WR == 1 ? parts : min((wave + 1) * per, parts);
-  for (int s0 = WR == 1 ? 0 : wave * per; s0 < s1; s0 += kWave) {
-    const int s = s0 + lane;
-    const float* stat = A.stat + place(s) * 2;
-    const float ms = s < s1 ? stat[0] : kNegInf, ls = s < s1 ? stat[1] : 0.f;
-    const int n = min(s1 - s0, kWave);
-    vec begin[4];  // the first four parts are loaded beside these
+  const int rows = min(sp.n * A.share - rb * A.block_rows, A.block_rows), end = min((chunk + 1) * each, rows);
+  if (rows <= 0 || parts == 1) return;
+  for (int in_block = chunk * each + (WR == 1 ? wave : 0); in_block < end; in_block += WR == 1 ? kWaves : 1) {
+    const int row = rb * A.block_rows + in_block, token = token_of(A, row), head = kh * A.share + row - token * A.share;
+    // part 0 in the second place of its workgroup, the others in the first of theirs
+    auto place = [&](int s) { return ((static_cast<int64_t>(first + s) * C.key_heads + kh) * 2 + (s == 0 ? 1 : 0)) * A.block_rows + in_block; };
+    float top = kNegInf, sum = 0.f, y[N] = {};
+    // up to 64 parts at a time, a lane's maximum and sum each; several wavefronts take a run of parts each
+    const int per = WR == 1 ? parts : (parts + WR - 1) / WR, s1 = WR == 1 ? parts : min((wave + 1) * per, parts);
+    for (int s0 = WR == 1 ? 0 : wave * per; s0 < s1; s0 += kWave) {
+      const int s = s0 + lane;
+      const float* stat = A.stat + place(s) * 2;
+      const float ms = s < s1 ? stat[0] : kNegInf, ls = s < s1 ? stat[1] : 0.f;
+      const int n = min(s1 - s0, kWave);
+      vec begin[4];  // the first four parts are loaded beside these
 #pragma unroll
-    for (int i = 0; i < 4; ++i) begin[i] = *reinterpret_cast<const vec*>(A.part + place(s0 + min(i, n - 1)) * D + lane * N);
-    float now = ms;
+      for (int i = 0; i < 4; ++i) begin[i] = *reinterpret_cast<const vec*>(A.part + place(s0 + min(i, n - 1)) * D + lane * N);
+      float now = ms;
 #pragma unroll
-    for (int d = 1; d < 16; d *= 2) now = fmaxf(now, __shfl_xor(now, d, kWave));
-    now = fmaxf(top, max4(now));
-    const float old = now == kNegInf ? 1.f : exp2_(top - now);
-    top = now;
-    const float f = ms == kNegInf ? 1.f : exp2_(ms - now);  // a part without a weight holds zeros, or NaN
-    sum = sum * old + wave_sum(ls * f);
+      for (int d = 1; d < 16; d *= 2) now = fmaxf(now, __shfl_xor(now, d, kWave));
+      now = fmaxf(top, max4(now));
+      const float old = now == kNegInf ? 1.f : exp2_(top - now);
+      top = now;
+      const float f = ms == kNegInf ? 1.f : exp2_(ms - now);  // a part without a weight holds zeros, or NaN
+      sum = sum * old + wave_sum(ls * f);
 #pragma unroll
-    for (int e = 0; e < N; ++e) y[e] *= old;
-    for (int i0 = 0; i0 < n; i0 += 4) {  // four at a time, the last again where there are fewer
-      vec x[4];
+      for (int e = 0; e < N; ++e) y[e] *= old;
+      for (int i0 = 0; i0 < n; i0 += 4) {  // four at a time, the last again where there are fewer
+        vec x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = i0 == 0 ? begin[i] : *reinterpret_cast<const vec*>(A.part + place(s0 + min(i0 + i, n - 1)) * D + lane * N);
+        for (int i = 0; i < 4; ++i) x[i] = i0 == 0 ? begin[i] : *reinterpret_cast<const vec*>(A.part + place(s0 + min(i0 + i, n - 1)) * D + lane * N);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float fi = i0 + i < n ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), min(i0 + i, n - 1))) : 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const float fi = i0 + i < n ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), min(i0 + i, n - 1))) : 0.f;
 #pragma unroll
-        for (int e = 0; e < N; ++e) y[e] = i0 + i < n ? fmaf(x[i][e], fi, y[e]) : y[e];
+          for (int e = 0; e < N; ++e) y[e] = i0 + i < n ? fmaf(x[i][e], fi, y[e]) : y[e];
+        }
       }
     }
-  }
-  if constexpr (WR > 1) {
+    if constexpr (WR > 1) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[wave][lane * N + e] = y[e];
-    if (lane == 0) {
-      stats[wave][0] = top;
-      stats[wave][1] = sum;
+      for (int e = 0; e < N; ++e) acc[wave][lane * N + e] = y[e];
+      if (lane == 0) {
+        stats[wave][0] = top;
+        stats[wave][1] = sum;
+      }
+      __syncthreads();
+      if (wave != 0) return;  // one row
+      float most = kNegInf;
+#pragma unroll
+      for (int w = 0; w < WR; ++w) most = fmaxf(most, stats[w][0]);
+      sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) y[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < WR; ++w) {
+        const float f = stats[w][0] == kNegInf ? 1.f : exp2_(stats[w][0] - most);
+        sum += stats[w][1] * f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) y[e] = fmaf(acc[w][lane * N + e], f, y[e]);
+      }
+      top = most;
     }
-    __syncthreads();
-    if (wave != 0) return;
-    float most = kNegInf;
 #pragma unroll
-    for (int w = 0; w < WR; ++w) most = fmaxf(most, stats[w][0]);
-    sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < N; ++e) y[e] = 0.f;
-#pragma unroll
-    for (int w = 0; w < WR; ++w) {
-      const float f = stats[w][0] == kNegInf ? 1.f : exp2_(stats[w][0] - most);
-      sum += stats[w][1] * f;
-#pragma unroll
-      for (int e = 0; e < N; ++e) y[e] = fmaf(acc[w][lane * N + e], f, y[e]);
-    }
-    top = most;
+    for (int e = 0; e < N; ++e) y[e] = sum == 0.f ? 0.f : y[e] / sum;
+    store_f32<DT, N>(static_cast<T*>(A.o) + (sp.lo + token) * A.o_stride + static_cast<int64_t>(head) * D + lane * N, y);
+    if (lane == 0 && A.lse != nullptr) A.lse[(sp.lo + token) * C.heads + head] = natural_log_sum(top, sum);
   }
-#pragma unroll
-  for (int e = 0; e < N; ++e) y[e] = sum == 0.f ? 0.f : y[e] / sum;
-  store_f32<DT, N>(static_cast<T*>(A.o) + (sp.lo + token) * A.o_stride + static_cast<int64_t>(head) * D + lane * N, y);
-  if (lane == 0 && A.lse != nullptr) A.lse[(sp.lo + token) * C.heads + head] = natural_log_sum(top, sum);
 }
 
 namespace {
@@ -817,12 +835,15 @@ hipError_t attend(const AttendArgs& a, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // Few rows: 8 wavefronts each (one request of 100000 keys, 32 rows: 73 us from 76 with one), many: one (64 requests,
-  // 2048 rows: 146 us from 150; 512 rows are the same).
-  const int64_t items = static_cast<int64_t>(a.c.batch) * a.max_tokens * a.c.heads;
-  if (items > 512)
-    k_attend_join<DT, D, 1><<<dim3(static_cast<unsigned>((items + kWaves - 1) / kWaves)), threads, 0, s>>>(a);
-  else
-    k_attend_join<DT, D, 8><<<dim3(static_cast<unsigned>(items)), dim3(8 * kWave), 0, s>>>(a);
+  // 2048 rows: 146 us from 150; 512 rows are the same), and more rows a workgroup where there are more than 2048 workgroups
+  // of 4, most of whose rows then have one part (256 requests of 6 tokens, 120 keys: 52 us from 57).
+  const int64_t blocks = static_cast<int64_t>(a.c.batch) * a.row_blocks * heads, items = blocks * a.block_rows;
+  if (items > 512) {
+    const int each = static_cast<int>(std::max((items / 2048 + kWaves - 1) / kWaves, int64_t{1})) * kWaves;
+    k_attend_join<DT, D, 1><<<dim3(static_cast<unsigned>(blocks * ((a.block_rows + each - 1) / each))), threads, 0, s>>>(a, each);
+  } else {
+    k_attend_join<DT, D, 8><<<dim3(static_cast<unsigned>(items)), dim3(8 * kWave), 0, s>>>(a, 1);
+  }
   return hipGetLastError();
 }
 
