@@ -412,6 +412,29 @@ def test_limits_of_the_call():
         assert torch.isfinite(o.float()).all()
 
 
+@pytest.mark.parametrize("batch", [65, 256, 300, 600])
+@pytest.mark.parametrize("most", [1, 6])
+def test_many_requests(batch, most):
+    """Shares that begin in any request: most short or empty, a few long, some without new rows."""
+    rrs, torch = _rrs()
+    r = np.random.default_rng(batch + most)
+    new = [int(x) for x in r.integers(0, most + 1, batch)]
+    new[0] = most
+    lengths = [n + int(x) for n, x in zip(new, r.integers(0, 40, batch))]
+    for b in (1, batch // 2, batch - 1):
+        lengths[b] = 2000 + b
+    cache = _cache(rrs, torch, lengths, 2, 64, 16, "bf16", batch)
+    cache = rrs.Cache(cache.k, cache.v, torch.nn.functional.pad(cache.table, (0, 1024 - cache.table.shape[1]), value=-1))  # a far limit
+    assert rrs.seed_attend_workspace_bytes(cache, sum(new), 6, max_tokens=most, ragged=True) > 0
+    _check(rrs, torch, cache, "bf16", new, lengths, 6, lead=1)
+    for b in range(batch):  # only the last one has rows, and only the first
+        if b != batch - 1:
+            new[b] = 0
+    _check(rrs, torch, cache, "bf16", new[:-1] + [most], lengths, 6)
+    _check(rrs, torch, cache, "bf16", [most] + [0] * (batch - 1), [max(lengths[0], most)] + lengths[1:], 6)
+    _check(rrs, torch, cache, "bf16", [0] * batch, lengths, 6)
+
+
 def test_a_refused_call_leaves_no_trace():
     """A scale of 0 is refused; the same call with another one runs."""
     rrs, torch = _rrs()
