@@ -755,9 +755,13 @@ __global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_atten
       const float* stat = A.stat + place(s) * 2;
       const float ms = s < s1 ? stat[0] : kNegInf, ls = s < s1 ? stat[1] : 0.f;
       const int n = min(s1 - s0, kWave);
-      vec begin[4];  // the first four parts are loaded beside these
+      // The first 4 parts are loaded beside these, the others 16 or 4 at a time, the last one again where there are fewer.
+      // Always 4: 397 parts 11.5 us from 9.2; always 16: 6 parts 9.0 from 8.3.
+      constexpr int kFirst = 4, kMore = 16;
+      auto part = [&](int i) { return *reinterpret_cast<const vec*>(A.part + place(s0 + min(i, n - 1)) * D + lane * N); };
+      vec x[kMore];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) begin[i] = *reinterpret_cast<const vec*>(A.part + place(s0 + min(i, n - 1)) * D + lane * N);
+      for (int i = 0; i < kFirst; ++i) x[i] = part(i);
       float now = ms;
 #pragma unroll
       for (int d = 1; d < 16; d *= 2) now = fmaxf(now, __shfl_xor(now, d, kWave));
@@ -768,16 +772,25 @@ __global__ __launch_bounds__(WR == 1 ? kWaves * kWave : WR * kWave) void k_atten
       sum = sum * old + wave_sum(ls * f);
 #pragma unroll
       for (int e = 0; e < N; ++e) y[e] *= old;
-      for (int i0 = 0; i0 < n; i0 += 4) {  // four at a time, the last again where there are fewer
-        vec x[4];
+      auto add = [&](int i, const vec& xi) {
+        const float fi = i < n ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), min(i, n - 1))) : 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = i0 == 0 ? begin[i] : *reinterpret_cast<const vec*>(A.part + place(s0 + min(i0 + i, n - 1)) * D + lane * N);
+        for (int e = 0; e < N; ++e) y[e] = i < n ? fmaf(xi[e], fi, y[e]) : y[e];
+      };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float fi = i0 + i < n ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), min(i0 + i, n - 1))) : 0.f;
+      for (int i = 0; i < kFirst; ++i) add(i, x[i]);
+      int i0 = kFirst;
+      for (; i0 + kMore / 2 < n; i0 += kMore) {
 #pragma unroll
-          for (int e = 0; e < N; ++e) y[e] = i0 + i < n ? fmaf(x[i][e], fi, y[e]) : y[e];
-        }
+        for (int i = 0; i < kMore; ++i) x[i] = part(i0 + i);
+#pragma unroll
+        for (int i = 0; i < kMore; ++i) add(i0 + i, x[i]);
+      }
+      for (; i0 < n; i0 += kFirst) {
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i) x[i] = part(i0 + i);
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i) add(i0 + i, x[i]);
       }
     }
     if constexpr (WR > 1) {
@@ -822,7 +835,8 @@ hipError_t attend(const AttendArgs& a, hipStream_t s) {
   if constexpr (!kWide) {
     if (a.groups == 0) {
       const dim3 grid(static_cast<unsigned>(a.c.batch * heads * a.row_blocks));
-      if (a.row_waves == 1) k_attend_whole<DT, D, 1, kMany><<<grid, dim3(kMany * kWave), 0, s>>>(a);
+      if (a.row_waves == 1 && a.few) k_attend_whole<DT, D, 1, kWaves><<<grid, threads, 0, s>>>(a);
+      else if (a.row_waves == 1) k_attend_whole<DT, D, 1, kMany><<<grid, dim3(kMany * kWave), 0, s>>>(a);
       else if (a.row_waves == 2) k_attend_whole<DT, D, kTwo, kWaves><<<grid, threads, 0, s>>>(a);
       else k_attend_whole<DT, D, kWaves, kWaves><<<grid, threads, 0, s>>>(a);
       return hipGetLastError();
@@ -873,7 +887,8 @@ bool plan_attend(int32_t io_dtype, AttendArgs& a) {
   if (a.window > 0) span = std::min(span, static_cast<int64_t>(a.window) + a.max_tokens - 1 + 31);
   const int64_t turns = static_cast<int64_t>(a.c.batch) * a.row_blocks * ((span + step - 1) / step);  // at most, of a key head
   if (turns >= int64_t{1} << 30) return false;
-  // Short spans in one launch, a workgroup each. One request of 300 keys: 7.4 us from 11.4 with shares and a join;
+  // Short spans in one launch, a workgroup each, of 4 wavefronts where those hold them in one turn (256 requests of 100
+  // keys 20 us, of 8 wavefronts 34; one request the same). One request of 300 keys: 7.4 us from 11.4 with shares and a join;
   // 64 requests of 1000 keys: 30 both; of 2000: 56 from 49 the other way. Wavefronts that share a tile take the keys one tile
   // after another: few are as fast where the units leave compute units idle, and more the more units there are, whose
   // requests the shares cut and join. 6 tokens of one request, 8 key heads: 250 keys (4 turns) 10.3 us, cut 12.1, 500 keys
@@ -884,6 +899,7 @@ bool plan_attend(int32_t io_dtype, AttendArgs& a) {
                       : a.row_waves == 1 ? std::min(4 * tile * kMany, (int64_t{256} << 10) / row_bytes)
                                          : std::min(std::max(units / per_turn, int64_t{4}), int64_t{64}) * step;
   a.groups = 0;
+  a.few = span <= kWaves * tile;  // one turn of 4 wavefronts
   if (span <= few) return true;
   a.groups = static_cast<int32_t>(std::max(std::min((kGroups + a.c.key_heads - 1) / a.c.key_heads, turns), int64_t{1}));
   return true;
