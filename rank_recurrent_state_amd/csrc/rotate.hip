@@ -3,8 +3,9 @@
 //
 // What bounds it: every value is read once and written once, so HBM. A workgroup takes a token: a thread forms the
 // sine and cosine of an angle (fp64: a position of 10^6 times a frequency of 1 loses 0.06 in fp32) and leaves
-// them in LDS, and all run over the token's heads as they lie, twice 16 bytes each a time. Heads, rotated parts or
-// addresses that do not divide so go value by value.
+// them in LDS, and all run over the token's heads as they lie, twice 16 bytes each a time. Where turned parts do
+// not divide so, 16 bytes, with the other values of their pairs in LDS; heads or addresses that do not divide go value by
+// value.
 // Measured: 32768 rows x 40 heads of 128, 671 MB: 108 us, 6.2 TB/s; 32768 prompt tokens, 16 + 2 x 4 heads of 256, into
 // pages, 805 MB: 135 us, 6.0 TB/s (a large copy by torch: 5.1). A token's call: 3 us, 7 with the call's host time.
 #include "attend.hpp"
@@ -32,6 +33,8 @@ __device__ __forceinline__ float2 turn_of(double turns, int64_t position, float 
     return make_float2(amplitude * cs, amplitude * sn);
   }
 }
+
+constexpr int kMostPairs = 2048;  // angles of a token
 
 // 16 bytes as VEC floats, and back.
 template <int DT, int VEC>
@@ -114,6 +117,78 @@ struct Item {
   }
 };
 
+// 16 bytes of a head as they lie, for turned parts that do not divide into halves of 16 bytes: the other values of their
+// pairs are read from LDS, where all threads of a turn leave theirs.
+template <int DT>
+struct AnyItem {
+  static constexpr int VEC = DT == 0 ? 4 : 8;
+  using T = stor_t<DT>;
+  u32x4 x;
+  T* y = nullptr;  // nullptr: no item
+  int at, rot;
+  __device__ __forceinline__ void load(const T* from, T* to, int item, int, int turned) {
+    at = item * VEC;
+    rot = turned;
+    y = to;
+    x = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + at));
+  }
+  __device__ __forceinline__ void finish(const float2* cs, const u32x4* left, int interleaved) {
+    if (y == nullptr) return;
+    if (at < rot) {
+      const T* head = reinterpret_cast<const T*>(left + threadIdx.x) - at;
+      const int half = rot / 2;
+      float v[VEC];
+      unpack<DT, VEC>(x, v);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int j = min(at + e, rot - 1);
+        const bool first = interleaved ? (j & 1) == 0 : j < half;
+        const int other = interleaved ? j ^ 1 : (first ? j + half : j - half), pair = interleaved ? j >> 1 : min(j, other);
+        const float o = to_f32<DT>(head[other]);
+        const float2 c = cs[pair];
+        v[e] = v[e] * c.x + (first ? -o : o) * c.y;
+      }
+      const u32x4 turned = pack<DT, VEC>(v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = at + e * (VEC / 4) < rot ? turned[e] : x[e];
+    }
+    __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(y + at));
+    y = nullptr;
+  }
+};
+
+// All items of a token: n of them, taken by turns of the workgroup's threads (ANY: of whole heads, the next turn's on
+// their way); the first are while angles() forms the angles.
+template <int DT, bool ANY, typename Fetch, typename Angles>
+__device__ __forceinline__ void turn_token(int n, int items, int interleaved, const float2* cs, Fetch fetch, Angles angles) {
+  __shared__ u32x4 left[ANY ? 2 : 1][ANY ? kThreads : 1];
+  const int tid = threadIdx.x;
+  if constexpr (ANY) {
+    const int turn = kThreads / items * items;
+    AnyItem<DT> it;
+    if (tid < turn && tid < n) fetch(it, tid);
+    angles();
+    for (int i0 = 0, buffer = 0; i0 < n; i0 += turn, buffer ^= 1) {
+      if (it.y != nullptr) left[buffer][tid] = it.x;
+      __syncthreads();  // what the turn before the last one left has been read
+      AnyItem<DT> next;
+      if (tid < turn && i0 + turn + tid < n) fetch(next, i0 + turn + tid);
+      it.finish(cs, left[buffer], interleaved);
+      it = next;
+    }
+  } else {
+    Item<DT> it;
+    if (tid < n) fetch(it, tid);
+    angles();
+    __syncthreads();
+    it.finish(cs, interleaved);
+    for (int i = tid + kThreads; i < n; i += kThreads) {
+      fetch(it, i);
+      it.finish(cs, interleaved);
+    }
+  }
+}
+
 // Where a new token goes: its request's position, and the place of it in the cache (-1: not there).
 struct Place {
   int64_t position, slot;
@@ -147,14 +222,11 @@ __device__ __forceinline__ int request_of(const CacheArgs& C, int64_t row, int b
   return b;
 }
 
-constexpr int kMostPairs = 2048;  // angles of a token
-
 }  // namespace
 
-// A workgroup per token and heads_each of its heads (blockIdx.y), `items` items each. The first items are on their way
-// while the angles are formed. One token: with several, whose sines are formed together, 32768 rows x 40
-// heads take 112 us (two) to 132 (sixteen) in the place of 106.
-template <int DT>
+// A workgroup per token and heads_each of its heads (blockIdx.y), `items` items each. One token: with several, whose
+// sines are formed together, 32768 rows x 40 heads take 112 us (two) to 132 (sixteen) in the place of 106.
+template <int DT, bool ANY>
 __global__ __launch_bounds__(kThreads) void k_rotate_rows(const RotateArgs A, int heads_each, int items, uint32_t per_item) {
   using T = stor_t<DT>;
   __shared__ float2 cs[kMostPairs];
@@ -162,25 +234,21 @@ __global__ __launch_bounds__(kThreads) void k_rotate_rows(const RotateArgs A, in
   const int h0 = static_cast<int>(blockIdx.y) * heads_each, n = min(heads_each, A.heads - h0) * items;
   const T* x = static_cast<const T*>(A.x) + row * A.x_stride + static_cast<int64_t>(h0) * A.dim;
   T* y = static_cast<T*>(A.y) + row * A.y_stride + static_cast<int64_t>(h0) * A.dim;
-  Item<DT> it;
-  auto fetch = [&](int i) {
-    const int h = divide(i, per_item);
-    it.load(x + h * A.dim, y + h * A.dim, i - h * items, A.dim, A.rot);
-  };
-  if (static_cast<int>(threadIdx.x) < n) fetch(threadIdx.x);
-  const int position = A.positions[row];
-  for (int i = threadIdx.x; i < A.rot / 2; i += kThreads) cs[i] = turn_of<DT>(A.turns[i], position, A.amplitude);
-  __syncthreads();
-  it.finish(cs, A.interleaved);
-  for (int i = threadIdx.x + kThreads; i < n; i += kThreads) {
-    fetch(i);
-    it.finish(cs, A.interleaved);
-  }
+  turn_token<DT, ANY>(
+      n, items, A.interleaved, cs,
+      [&](auto& it, int i) {
+        const int h = divide(i, per_item);
+        it.load(x + h * A.dim, y + h * A.dim, i - h * items, A.dim, A.rot);
+      },
+      [&] {
+        const int position = A.positions[row];
+        for (int i = threadIdx.x; i < A.rot / 2; i += kThreads) cs[i] = turn_of<DT>(A.turns[i], position, A.amplitude);
+      });
 }
 
 // The same for the rows of seed_cache_append: of all heads of a token, the queries come first, then the keys, then the
 // values.
-template <int DT>
+template <int DT, bool ANY>
 __global__ __launch_bounds__(kThreads) void k_cache_append(const AppendArgs A, int heads_each, int items, uint32_t per_item) {
   using T = stor_t<DT>;
   __shared__ float2 cs[kMostPairs];
@@ -197,22 +265,18 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const AppendArgs A, i
   T* qo = static_cast<T*>(A.q_out) + row * A.o_stride;
   T* ko = static_cast<T*>(C.k) + p.slot;
   T* vo = static_cast<T*>(C.v) + p.slot;
-  Item<DT> it;
-  auto fetch = [&](int i) {
-    const int part = divide(i, per_item), item = i - part * items, h = h0 + part, kh = h - queries, vh = kh - C.key_heads;
-    if (kh < 0) it.load(q + static_cast<int64_t>(h) * C.dim, qo + static_cast<int64_t>(h) * C.dim, item, C.dim, A.rot);
-    else if (p.slot < 0) return;
-    else if (vh < 0) it.load(k + static_cast<int64_t>(kh) * C.dim, ko + kh * C.head_stride, item, C.dim, A.rot);
-    else it.load(v + static_cast<int64_t>(vh) * C.dim, vo + vh * C.head_stride, item, C.dim, 0);
-  };
-  if (static_cast<int>(threadIdx.x) < n) fetch(threadIdx.x);
-  for (int i = threadIdx.x; i < A.rot / 2; i += kThreads) cs[i] = turn_of<DT>(A.turns[i], p.position, A.amplitude);
-  __syncthreads();
-  it.finish(cs, A.interleaved);
-  for (int i = threadIdx.x + kThreads; i < n; i += kThreads) {
-    fetch(i);
-    it.finish(cs, A.interleaved);
-  }
+  turn_token<DT, ANY>(
+      n, items, A.interleaved, cs,
+      [&](auto& it, int i) {
+        const int part = divide(i, per_item), item = i - part * items, h = h0 + part, kh = h - queries, vh = kh - C.key_heads;
+        if (kh < 0) it.load(q + static_cast<int64_t>(h) * C.dim, qo + static_cast<int64_t>(h) * C.dim, item, C.dim, A.rot);
+        else if (p.slot < 0) return;
+        else if (vh < 0) it.load(k + static_cast<int64_t>(kh) * C.dim, ko + kh * C.head_stride, item, C.dim, A.rot);
+        else it.load(v + static_cast<int64_t>(vh) * C.dim, vo + vh * C.head_stride, item, C.dim, 0);
+      },
+      [&] {
+        for (int i = threadIdx.x; i < A.rot / 2; i += kThreads) cs[i] = turn_of<DT>(A.turns[i], p.position, A.amplitude);
+      });
 }
 
 // Value by value: a thread has one pair of a token, or one value of the rest, for heads part, part + parts, ..
@@ -313,27 +377,35 @@ Cut cut(int64_t rows, int heads, int items) {
   Cut c;
   c.heads_each = heads;
   if (rows < 2048) {  // a turn of the threads each
-    c.heads_each = (kThreads + items - 1) / items;
+    c.heads_each = kThreads / items > 1 ? kThreads / items : 1;
     c.heads_each = c.heads_each < heads ? c.heads_each : heads;
   }
   c.per_item = static_cast<uint32_t>((0xffffffffull + items) / items);
   c.grid = dim3(static_cast<unsigned>(rows), static_cast<unsigned>((heads + c.heads_each - 1) / c.heads_each));
   return c;
 }
-// Whether heads and their rotated part divide into items, and the launch's indexes stay small: 16384 rows x 40 heads 55 us,
-// value by value 81; 1 row the same.
-bool whole(int64_t rows, int64_t heads, int dim, int rot, int vec) {
-  return dim % (2 * vec) == 0 && rot % (2 * vec) == 0 && rot / 2 <= kMostPairs && heads * dim <= 16384 && rows < (1 << 24);
+// How a token's heads go: as pairs of 16 bytes where heads and turned parts divide into two of them, as 16 bytes and what
+// LDS holds of the others where only the heads divide, or value by value; the first two within what the launch counts.
+// 16384 rows x 40 heads of 128 values, bf16: all turned 55 us as pairs, 78 by LDS, 81 value by value; 98 to 124 of them
+// 78 by LDS, 166 to 171 value by value (bound by the vector unit both); fp32 8192 rows 58, 61, 86 and 61, 117. One row
+// takes the same.
+enum class Way { kPairs, kAny, kValues };
+Way way(int64_t rows, int64_t heads, int dim, int rot, int vec, bool aligned) {
+  if (!aligned || dim % vec != 0 || rot / 2 > kMostPairs || rows >= (1 << 24) || heads * dim > (1 << 20)) return Way::kValues;
+  if (dim % (2 * vec) == 0 && rot % (2 * vec) == 0) return heads * (dim / (2 * vec)) * (dim / (2 * vec)) < (int64_t{1} << 32) ? Way::kPairs : Way::kValues;
+  return dim / vec <= kThreads ? Way::kAny : Way::kValues;
 }
 
 template <int DT>
-hipError_t rotate(const RotateArgs& a, bool v, hipStream_t s) {
+hipError_t rotate(const RotateArgs& a, bool aligned, hipStream_t s) {
   constexpr int VEC = DT == 0 ? 4 : 8;
   const bool in_place = a.x == a.y;
-  if (v) {
-    const int items = (in_place ? a.rot : a.dim) / (2 * VEC);
+  const Way w = way(a.rows, a.heads, a.dim, a.rot, VEC, aligned);
+  if (w != Way::kValues) {
+    const int turned = in_place ? a.rot : a.dim, items = w == Way::kPairs ? turned / (2 * VEC) : (turned + VEC - 1) / VEC;
     const Cut c = cut(a.rows, a.heads, items);
-    k_rotate_rows<DT><<<c.grid, dim3(kThreads), 0, s>>>(a, c.heads_each, items, c.per_item);
+    if (w == Way::kPairs) k_rotate_rows<DT, false><<<c.grid, dim3(kThreads), 0, s>>>(a, c.heads_each, items, c.per_item);
+    else k_rotate_rows<DT, true><<<c.grid, dim3(kThreads), 0, s>>>(a, c.heads_each, items, c.per_item);
   } else {
     const int items = in_place ? a.rot / 2 : a.dim - a.rot / 2, parts = parts_of(a.rows * items, a.heads);
     k_rotate_values<DT><<<dim3(loop_blocks((a.rows * parts * items + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(a, items, parts);
@@ -342,13 +414,15 @@ hipError_t rotate(const RotateArgs& a, bool v, hipStream_t s) {
 }
 
 template <int DT>
-hipError_t append(const AppendArgs& a, bool v, hipStream_t s) {
+hipError_t append(const AppendArgs& a, bool aligned, hipStream_t s) {
   constexpr int VEC = DT == 0 ? 4 : 8;
   const int queries = a.q != nullptr ? a.c.heads : 0;
-  if (v) {
-    const int items = a.c.dim / (2 * VEC);
+  const Way w = way(a.c.tokens, queries + 2 * static_cast<int64_t>(a.c.key_heads), a.c.dim, a.rot, VEC, aligned);
+  if (w != Way::kValues) {
+    const int items = a.c.dim / (w == Way::kPairs ? 2 * VEC : VEC);
     const Cut c = cut(a.c.tokens, queries + 2 * a.c.key_heads, items);
-    k_cache_append<DT><<<c.grid, dim3(kThreads), 0, s>>>(a, c.heads_each, items, c.per_item);
+    if (w == Way::kPairs) k_cache_append<DT, false><<<c.grid, dim3(kThreads), 0, s>>>(a, c.heads_each, items, c.per_item);
+    else k_cache_append<DT, true><<<c.grid, dim3(kThreads), 0, s>>>(a, c.heads_each, items, c.per_item);
   } else {
     const int items = a.c.dim - a.rot / 2, parts = parts_of(a.c.tokens * items, queries + a.c.key_heads);
     k_append_values<DT><<<dim3(loop_blocks((a.c.tokens * parts * items + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(a, items, parts);
@@ -360,16 +434,15 @@ hipError_t append(const AppendArgs& a, bool v, hipStream_t s) {
 
 hipError_t launch_rotate_rows(int32_t io_dtype, const RotateArgs& a, hipStream_t s) {
   const int bytes = io_dtype == SEED_BF16 ? 2 : 4;
-  const bool v = whole(a.rows, a.heads, a.dim, a.rot, 16 / bytes) && rows_aligned16(a.x, a.x_stride, bytes) && rows_aligned16(a.y, a.y_stride, bytes);
-  return io_dtype == SEED_BF16 ? rotate<1>(a, v, s) : rotate<0>(a, v, s);
+  const bool aligned = rows_aligned16(a.x, a.x_stride, bytes) && rows_aligned16(a.y, a.y_stride, bytes);
+  return io_dtype == SEED_BF16 ? rotate<1>(a, aligned, s) : rotate<0>(a, aligned, s);
 }
 
 hipError_t launch_cache_append(int32_t io_dtype, const AppendArgs& a, hipStream_t s) {
   const int bytes = io_dtype == SEED_BF16 ? 2 : 4;
-  bool v = whole(a.c.tokens, (a.q != nullptr ? a.c.heads : 0) + 2 * static_cast<int64_t>(a.c.key_heads), a.c.dim, a.rot, 16 / bytes) &&
-           rows_aligned16(a.k, a.k_stride, bytes) && rows_aligned16(a.v, a.v_stride, bytes);
-  if (a.q != nullptr) v = v && rows_aligned16(a.q, a.q_stride, bytes) && rows_aligned16(a.q_out, a.o_stride, bytes);
-  return io_dtype == SEED_BF16 ? append<1>(a, v, s) : append<0>(a, v, s);
+  bool aligned = rows_aligned16(a.k, a.k_stride, bytes) && rows_aligned16(a.v, a.v_stride, bytes);
+  if (a.q != nullptr) aligned = aligned && rows_aligned16(a.q, a.q_stride, bytes) && rows_aligned16(a.q_out, a.o_stride, bytes);
+  return io_dtype == SEED_BF16 ? append<1>(a, aligned, s) : append<0>(a, aligned, s);
 }
 
 }  // namespace seed

@@ -85,6 +85,29 @@ def test_rotate_rows(dtype, interleaved, rows, heads, dim, rot):
     assert torch.equal(wide[:, 8 + heads * dim:], before[:, 8 + heads * dim:])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rows,heads,dim,rot", [(5, 40, 128, 100), (2100, 40, 128, 98), (3, 64, 72, 72), (2050, 64, 72, 36), (7, 80, 256, 158),
+                                                (2049, 72, 256, 64), (2, 3, 2048, 14), (2, 2, 1032, 1030), (1, 1, 16, 2)])
+def test_rotate_parts_of_any_size(dtype, interleaved, rows, heads, dim, rot):
+    """Turned parts that do not divide into 16 bytes, over several turns of a workgroup and many values a token; what lies
+    behind them keeps its bits, in place too."""
+    test_rotate_rows(dtype, interleaved, rows, heads, dim, rot)
+    rrs, torch = _rrs()
+    rotary = rrs.make_rotary(rot, interleaved=interleaved)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    x = torch.randint(-(1 << 15), 1 << 15, (3, heads, dim), generator=_gen(torch, 1), device="cuda", dtype=torch.int32).to(bits)
+    x[..., :rot] = 0
+    x[..., rot:] |= 0x7f81 if dtype == "bf16" else 0x7f800001  # NaN of all kinds
+    before, y = x.clone(), torch.zeros_like(x)
+    at = _i32(torch, [0, 5, -9])
+    rrs.seed_rotate_rows(rotary, x.view(_dt(torch, dtype)), at, y.view(_dt(torch, dtype)))
+    zero = y.view(_dt(torch, dtype))[..., :rot] == 0  # of either sign: 0 c - 0 s
+    assert torch.equal(y[..., rot:], before[..., rot:]) and zero.all()
+    rrs.seed_rotate_rows(rotary, x.view(_dt(torch, dtype)), at, x.view(_dt(torch, dtype)))
+    assert torch.equal(x[..., rot:], before[..., rot:])
+
+
 def test_rotation_keeps_products():
     """Turned queries and keys meet as the difference of their positions says, also far out."""
     rrs, torch = _rrs()
@@ -190,6 +213,14 @@ def test_cache_append(dtype, layout, new, history, heads, kh, dim, page, rot, in
         again, k1, v1 = q[lead:lead + n].clone(), cache.k.clone(), cache.v.clone()
         rrs.seed_cache_append(cache, _i32(torch, lengths), k[lead:lead + n], v[lead:lead + n], rotary=rotary, q=again, q_out=again)
         assert torch.equal(again, out[lead:lead + n]) and torch.equal(cache.k, k1) and torch.equal(cache.v, v1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("new,heads,kh,dim,rot", [([3, 0, 40], 64, 8, 256, 64), ([1, 2, 1], 40, 5, 128, 100), ([2, 2200], 12, 1, 64, 58), ([4], 7, 7, 256, 250)])
+def test_append_parts_of_any_size(dtype, interleaved, new, heads, kh, dim, rot):
+    """Many values a token, and turned parts that do not divide into 16 bytes."""
+    test_cache_append(dtype, "heads", new, [5] * len(new), heads, kh, dim, 16, rot, interleaved)
 
 
 def test_append_places_that_are_not_there():
