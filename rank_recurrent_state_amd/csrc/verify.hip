@@ -8,9 +8,9 @@
 // segment that holds the draw is read again and its tokens are walked. Every wavefront finds the request's first
 // refused row by itself, from a few gathered values, and no step needs more than one wavefront: a row that one
 // workgroup reads as fast as a second launch takes is summed and walked by it, larger ones in two launches.
-// Measured: 128 requests, 150001 tokens, fp32, 154 MB: 25 us, 6.2 TB/s; 200 requests, 65536 tokens, bf16, no drafts'
-// probabilities, 26 MB: 14 us, of which the sums take 10: four loads one after another lead to a row, and the rows
-// are short. Two segments a wavefront at once: the same or up to 1 us more.
+// Measured: 128 requests, 150001 tokens, fp32, 154 MB: 24 us, 6.4 TB/s; 200 requests, 65536 tokens, bf16, no drafts'
+// probabilities, 26 MB: 13 us, of which the sums take 9: four loads one after another lead to a row, and conversions and
+// sums in fp64 take as long as the reads (14 us with the choice of positive weights and of x in fp64 for all). Two segments a wavefront at once: the same or up to 1 us more.
 #include "attend.hpp"
 #include "common.hpp"
 
@@ -72,14 +72,26 @@ struct Weights {
             }
         }
     }
+    if (q != nullptr) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+      for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const double pe = pt[k][e];
-        const double d = q != nullptr ? pe - static_cast<double>(qt[k][e]) : (t0 + k * step + e == x ? 0.0 : pe);
-        w[k * N + e] = fmax(d, 0.0);  // of NaN: 0
+        for (int e = 0; e < N; ++e) w[k * N + e] = fmax(static_cast<double>(pt[k][e]) - static_cast<double>(qt[k][e]), 0.0);  // of NaN: 0
+    } else {
+      bool here = false;  // token x among these
+#pragma unroll
+      for (int k = 0; k < K; ++k) here = here || static_cast<uint32_t>(x - (t0 + k * step)) < N;
+      if (__any(here)) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int e = 0; e < N; ++e) pt[k][e] = t0 + k * step + e == x ? 0.f : pt[k][e];
       }
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < N; ++e) w[k * N + e] = __builtin_amdgcn_fmed3f(pt[k][e], 0.f, __builtin_inff());  // of NaN: 0
+    }
   }
 
  private:
