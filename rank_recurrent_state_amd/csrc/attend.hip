@@ -312,14 +312,15 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
   constexpr int kTurn = (RW == 1 ? NW : 1) * L::kKeys;
   Where here{};
   const int start = from + (RW == 1 ? wave * L::kKeys : 0);
-  if (from < to) {
+  const bool any = RW == 1 ? start < to : from < to;  // a tile for this wavefront (256 requests of 100 keys: 18 us, with loads for all 20)
+  if (any) {
     here = find(start, look_up(start));
     load_rows(kb, here, K);
     if constexpr (RW > 1) load_rows(vb, here, Vr);
   }
   const uint32_t write_at = (mine + my_row) * L::kRow + ((my_piece ^ L::swap(mine) ^ L::swap(my_row)) << 4), read_at = l16 * L::kRow + ((g ^ L::swap(l16)) << 4);
   Pages ahead{};  // of the next turn: looked up a turn ahead too
-  if (from < to) ahead = look_up(start + kTurn);
+  if (any) ahead = look_up(start + kTurn);
   int turn = 0;
   for (int t0 = start; t0 < to; t0 += kTurn) {
     char* keys = sm.tiles + (RW == 1 ? wave * L::kTile : turn * 2 * L::kTile);
@@ -888,7 +889,7 @@ bool plan_attend(int32_t io_dtype, AttendArgs& a) {
   const int64_t turns = static_cast<int64_t>(a.c.batch) * a.row_blocks * ((span + step - 1) / step);  // at most, of a key head
   if (turns >= int64_t{1} << 30) return false;
   // Short spans in one launch, a workgroup each, of 4 wavefronts where those hold them in one turn (256 requests of 100
-  // keys 20 us, of 8 wavefronts 34; one request the same). One request of 300 keys: 7.4 us from 11.4 with shares and a join;
+  // keys 18 us, of 8 wavefronts 34; one request the same). One request of 300 keys: 7.4 us from 11.4 with shares and a join;
   // 64 requests of 1000 keys: 30 both; of 2000: 56 from 49 the other way. Wavefronts that share a tile take the keys one tile
   // after another: few are as fast where the units leave compute units idle, and more the more units there are, whose
   // requests the shares cut and join. 6 tokens of one request, 8 key heads: 250 keys (4 turns) 10.3 us, cut 12.1, 500 keys
