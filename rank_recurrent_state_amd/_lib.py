@@ -917,9 +917,9 @@ def seed_decode_attend(cache: Cache, lengths, q, o, offsets=None, max_tokens: in
     """Attention of every request's new tokens, q [tokens, heads, dim] (rows may be strided), over its cache,
     which holds them already, into o. lengths, offsets: as for seed_cache_append; max_tokens: the most new tokens
     of a request; max_length: the most tokens of a request (None: what the table holds; where all requests are
-    short, one close to them saves a launch); scale: None for
-    1 / sqrt(dim); window: positions a row sees, 0 for all; lse: float [tokens, heads] or None. ws: a workspace
-    of seed_attend_workspace_bytes bytes; without one, one is taken from torch's allocator when needed."""
+    short, one close to them saves a launch); scale: None for 1 / sqrt(dim); window: positions a row sees, 0 for
+    all; lse: float [tokens, heads] or None. ws: a workspace of seed_attend_workspace_bytes bytes; without one, one
+    is taken from torch's allocator when needed."""
     torch, _ = _io()
     c, i32 = cache.c, torch.int32
     a, dt, dim = _Args(torch), cache.dtype, c.dim

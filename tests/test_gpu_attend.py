@@ -466,6 +466,25 @@ def test_many_requests(batch, most):
     _check(rrs, torch, cache, "bf16", [0] * batch, lengths, 6)
 
 
+@pytest.mark.parametrize("most", [1, 4])
+def test_offsets_beyond_32_bits(most):
+    """Pages that lie more than 2^32 values behind the pool's start, stored to and read."""
+    rrs, torch = _rrs()
+    kh, heads, dim, page, stride = 2, 16, 128, 16, (1 << 32) // 2 + 64 * 8
+    size = 3 * stride + page * kh * dim
+    if torch.cuda.mem_get_info()[0] < 5 * size:  # keys and values of 2 bytes, and room
+        pytest.skip("memory")
+    pools = [torch.empty(size, dtype=torch.bfloat16, device="cuda").as_strided((4, page, kh, dim), (stride, kh * dim, dim, 1)) for _ in range(2)]
+    table = _i32(torch, [[2, 0, 3, 1]])
+    cache = rrs.Cache(*pools, table)
+    n, g = 57, _gen(torch, 6)
+    k, v = (torch.randn(n, kh, dim, generator=g, device="cuda").bfloat16() for _ in range(2))
+    rrs.seed_cache_append(cache, _i32(torch, [n]), k, v, offsets=_offsets(torch, [n]))
+    got_k, got_v = _gather(cache, 0, n)
+    assert torch.equal(got_k, k) and torch.equal(got_v, v)
+    _check(rrs, torch, cache, "bf16", [most], [n], heads)
+
+
 def test_a_refused_call_leaves_no_trace():
     """A scale of 0 is refused; the same call with another one runs."""
     rrs, torch = _rrs()
