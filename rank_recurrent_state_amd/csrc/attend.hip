@@ -655,9 +655,10 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend(const AttendArgs A
   // neighbouring heads, whose keys lie side by side, run at the same time
   const int kh = static_cast<int>(blockIdx.x % C.key_heads), me = static_cast<int>(blockIdx.x / C.key_heads);
   const int lane = threadIdx.x & 63;
+  auto of_block = [&](const Span& sp) { return sp.n > 0 ? sp.turns(kStep) + A.change : 0; };
   auto turns = [&](int i) {
     const Span sp = span_of(A, min(i, C.batch - 1));
-    return i < C.batch ? sp.turns(kStep) * ((sp.n * A.share + 16 * RW - 1) / (16 * RW)) : 0;
+    return i < C.batch ? of_block(sp) * ((sp.n * A.share + 16 * RW - 1) / (16 * RW)) : 0;
   };
   // every wavefront for itself: the sum of all turns, then the request in which this share begins. The lengths of up to
   // 256 requests are loaded at once (64 at a time: up to 2 us more for 256 requests; at once for one: 1 us more).
@@ -702,7 +703,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend(const AttendArgs A
   if (w0 >= w1) return;
   Span sp = span_of(A, b);
   for (int w = w0; w < w1;) {
-    const int each = sp.turns(kStep), blocks = (sp.n * A.share + 16 * RW - 1) / (16 * RW);
+    const int each = of_block(sp), blocks = (sp.n * A.share + 16 * RW - 1) / (16 * RW);
     const int rb = RW == 1 ? 0 : (w - begin) / each, t0 = w - begin - rb * each, n = min(each - t0, w1 - w);
     const bool whole = n == each;
     const int64_t place = (static_cast<int64_t>(me) * C.key_heads + kh) * 2 + (t0 == 0 ? 1 : 0);
@@ -712,12 +713,12 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend(const AttendArgs A
       note[1] = me + (each - n + share - 1) / share;
     }
     if (w > w0) __syncthreads();  // the last part's results have been read
-    const int from = sp.base + t0 * kStep;
-    const int to = static_cast<int>(min(static_cast<int64_t>(from) + static_cast<int64_t>(n) * kStep, static_cast<int64_t>(sp.k1)));
+    const int from = sp.base + max(t0 - A.change, 0) * kStep;
+    const int to = static_cast<int>(min(sp.base + static_cast<int64_t>(max(t0 + n - A.change, 0)) * kStep, static_cast<int64_t>(sp.k1)));
     attend_keys<DT, D, RW, kWaves>(A, sm, sp, b, kh, rb, from, to, whole ? nullptr : A.part + place * A.block_rows * D,
                                    A.stat + place * A.block_rows * 2);
     w += n;
-    while (w < w1 && w == begin + sp.turns(kStep) * ((sp.n * A.share + 16 * RW - 1) / (16 * RW))) {  // on to the next request with rows
+    while (w < w1 && w == begin + of_block(sp) * ((sp.n * A.share + 16 * RW - 1) / (16 * RW))) {  // on to the next request with rows
       begin = w;
       sp = span_of(A, ++b);
     }
@@ -886,7 +887,11 @@ bool plan_attend(int32_t io_dtype, AttendArgs& a) {
   const int64_t step = a.row_waves == 1 ? tile * kWaves : shared;  // keys of one turn of a workgroup
   int64_t span = a.capacity;
   if (a.window > 0) span = std::min(span, static_cast<int64_t>(a.window) + a.max_tokens - 1 + 31);
-  const int64_t turns = static_cast<int64_t>(a.c.batch) * a.row_blocks * ((span + step - 1) / step);  // at most, of a key head
+  // A change of rows (results written, the next queries, pages and first tile) counts as turns too, or the workgroups that
+  // have one end last: 6 tokens of 48 requests 69 us from 73 (1: 72, 2: 70, 4: 69), 32 rows of fp32 116 from 118 (4:
+  // 120). Own keys, whose turns are longer: 200 requests of 1500 keys 96.5 from 98 (3: 101), 64 of 16384 the same.
+  a.change = a.row_waves == 1 ? 1 : 3;
+  const int64_t turns = static_cast<int64_t>(a.c.batch) * a.row_blocks * ((span + step - 1) / step + a.change);  // at most, of a key head
   if (turns >= int64_t{1} << 30) return false;
   // Short spans in one launch, a workgroup each, of 4 wavefronts where those hold them in one turn (256 requests of 100
   // keys 18 us, of 8 wavefronts 34; one request the same). One request of 300 keys: 7.4 us from 11.4 with shares and a join;

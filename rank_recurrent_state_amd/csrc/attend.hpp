@@ -57,6 +57,7 @@ struct AttendArgs {
   int32_t row_waves;        // wavefronts of a workgroup that have rows of their own
   int32_t block_rows;       // rows that a workgroup takes at a time, of max_tokens share,
   int32_t row_blocks;       // and how many times
+  int32_t change;           // turns that a change of rows costs, counted with a row block's
   int32_t few;              // groups 0: as few keys as one turn of a small workgroup
   int32_t groups;           // workgroups that share a key head's turns; 0: a workgroup per request and key head
   int64_t q_stride, o_stride;
