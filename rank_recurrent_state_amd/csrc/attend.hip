@@ -16,7 +16,7 @@
 // unit, whose partial results a second launch joins; short ones stay whole and need no second launch.
 // Measured: 64 requests of up to 16384 tokens, 8 key heads of 128, 1.75 GB: 286 us, 6.1 TB/s (the kernel alone 6.2; a
 // kernel that only reads such pages 6.5 - 6.7); one request of 131072 tokens 92 us, 5.8 TB/s; 6 tokens of 48 requests
-// (48 rows of a key head of 256), 298 MB: 72 us, 4.2 TB/s, of which the join takes 8 and the first tiles' way 6; the loop
+// (48 rows of a key head of 256), 298 MB: 67 us, 4.5 TB/s, of which the join takes 8 and the first tiles' way 6; the loop
 // between reads 7.
 // bf16 weights enter as two pieces (p and p - bf16(p)), so that o is off by its own rounding only: with one
 // piece the weights' rounding, 2^-9 each, is as large as o's. The products are far from the matrix unit's rate.
@@ -35,8 +35,9 @@ namespace {
 constexpr int kWaves = 4;  // of a workgroup; short caches take kMany
 constexpr int kMany = 8;
 // Workgroups of a call that share its keys: two for each compute unit, as many as their registers and LDS admit. 6 tokens
-// of 48 requests 78 us, 85 with half as many and 91 with twice; 16 requests of 4096 keys 31, 33 and 33; one of 131072
-// keys 93, 92 and 94; each more part of a row is another one to write and to join.
+// of 48 requests 78 us, 85 with half as many and 91 with twice (before changes of rows were counted, now 67); 16 requests
+// of 4096 keys 31, 33 and 33; one of 131072 keys 93, 92 and 94; each more part of a row is another one to write and to
+// join.
 constexpr int64_t kGroups = 512;
 
 // Turns of a workgroup: equal shares of them all.
@@ -643,10 +644,10 @@ __global__ __launch_bounds__(NW* kWave, 2) void k_attend_whole(const AttendArgs 
   attend_keys<DT, D, RW, NW>(A, sm, sp, b, kh, rb, sp.base, sp.k1, nullptr, nullptr);
 }
 
-// The turns of all requests (of `step` keys, row block after row block) are cut into equal shares, one for each of
-// a key head's workgroups; the requests' lengths are known here only. A share that ends inside a row block leaves
-// partial results in the workgroup's second place, one that begins inside in its first; the workgroup that begins a
-// row block notes which ones hold it.
+// The turns of all requests (of kStep keys, row block after row block, each with `change` turns without keys before it)
+// are cut into equal shares, one for each of a key head's workgroups; the requests' lengths are known here only. A
+// share that ends inside a row block leaves partial results in the workgroup's second place, one that begins inside in
+// its first; the workgroup that begins a row block notes which ones hold it.
 template <int DT, int D, int RW>
 __global__ __launch_bounds__(kWaves * kWave, 2) void k_attend(const AttendArgs A) {
   __shared__ Shared<DT, D, RW, kWaves> sm;
