@@ -616,8 +616,8 @@ typedef struct seed_attend {
   float scale;         /* of the products q . k; finite and not 0                                */
 } seed_attend;
 
-/* Workspace bytes of seed_decode_attend (0: none needed, or invalid arguments): at most 512 row blocks of partial
- * results per key head's share, independent of the lengths. Host-only, pure. */
+/* Workspace bytes of seed_decode_attend (0: none needed, or invalid arguments): fp32 partial results of about 1024
+ * times up to 64 rows (up to 67 MB for heads of 256), whatever the lengths. Host-only, pure. */
 size_t seed_attend_workspace_bytes(const seed_cache *cache, const seed_tokens *tokens, const seed_attend *attend);
 
 /*
