@@ -16,7 +16,7 @@
 // unit, whose partial results a second launch joins; short ones stay whole and need no second launch.
 // Measured: 64 requests of up to 16384 tokens, 8 key heads of 128, 1.75 GB: 286 us, 6.1 TB/s (the kernel alone 6.2; a
 // kernel that only reads such pages 6.5 - 6.7); one request of 131072 tokens 92 us, 5.8 TB/s; 6 tokens of 48 requests
-// (48 rows of a key head of 256), 298 MB: 67 us, 4.5 TB/s, of which the join takes 8 and the first tiles' way 6; the loop
+// (48 rows of a key head of 256), 298 MB: 66 us, 4.5 TB/s, of which the join takes 8 and the first tiles' way 6; the loop
 // between reads 7.
 // bf16 weights enter as two pieces (p and p - bf16(p)), so that o is off by its own rounding only: with one
 // piece the weights' rounding, 2^-9 each, is as large as o's. The products are far from the matrix unit's rate.
@@ -282,7 +282,7 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
   const int my_row = lane / L::kLine, my_piece = lane % L::kLine;
   const uint32_t in_row = static_cast<uint32_t>(my_row * ts) + my_piece * 16;
   u32x4 K[kLoads], Vr[kLoads];
-  auto load_rows = [&](const char* pool, const Where& w, u32x4 (&x)[kLoads]) {
+  auto load_rows = [&](const char* pool, const Where& w, uint32_t in_row, u32x4 (&x)[kLoads]) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) x[i] = load<u32x4>(scalar(pool + w.at[i * L::kAtOnce / 16] + i * L::kAtOnce % 16 * ts) + in_row);
   };
@@ -316,8 +316,8 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
   const bool any = RW == 1 ? start < to : from < to;  // a tile for this wavefront (256 requests of 100 keys: 18 us, with loads for all 20)
   if (any) {
     here = find(start, look_up(start));
-    load_rows(kb, here, K);
-    if constexpr (RW > 1) load_rows(vb, here, Vr);
+    load_rows(kb, here, in_row, K);
+    if constexpr (RW > 1) load_rows(vb, here, in_row, Vr);
   }
   const uint32_t write_at = (mine + my_row) * L::kRow + ((my_piece ^ L::swap(mine) ^ L::swap(my_row)) << 4), read_at = l16 * L::kRow + ((g ^ L::swap(l16)) << 4);
   Pages ahead{};  // of the next turn: looked up a turn ahead too
@@ -360,9 +360,12 @@ __device__ __forceinline__ void attend_keys(const AttendArgs& A, Shared<DT, D, R
     }
     const Where next = find(t0 + kTurn, ahead);
     ahead = look_up(t0 + 2 * kTurn);
-    load_rows(kb, next, K);  // behind the last tile, of that: the loads on their way are then the same in number
+    // behind the last tile one piece of its rows, for all lanes: the loads on their way are then the same in number
+    // (256 requests of 700 keys 69 us, with the whole tile again 73)
+    const uint32_t in_next = t0 + kTurn < to ? in_row : 0;
+    load_rows(kb, next, in_next, K);
     if constexpr (RW > 1) {
-      load_rows(vb, next, Vr);
+      load_rows(vb, next, in_next, Vr);
       // the tile is whole; the other one is free once every wavefront is past this point in the next turn
       __syncthreads();
       turn ^= 1;
