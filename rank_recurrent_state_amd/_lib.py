@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libseed.so")
@@ -112,6 +113,18 @@ class seed_drafts(ctypes.Structure):
                 ("draft_stride", ctypes.c_int64)]
 
 
+def _packer(cls):
+    """The bytes of a cls with the given values (0 for a null pointer), for the entry points of single tokens' calls: they
+    take no ctypes object, whose making costs three times as much (0.9 us of a call's 7)."""
+    code = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_void_p: "P", ctypes.c_float: "f"}
+    packed = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_) + "0q")
+    assert packed.size == ctypes.sizeof(cls)
+    return packed.pack
+
+
+_ROWS, _TOKENS, _ATTEND, _DRAFTS = _packer(seed_rows), _packer(seed_tokens), _packer(seed_attend), _packer(seed_drafts)
+
+
 class seed_state(ctypes.Structure):
     _fields_ = [("a", ctypes.c_void_p), ("U", ctypes.c_void_p), ("V", ctypes.c_void_p),
                 ("scale", ctypes.c_void_p)]
@@ -190,15 +203,13 @@ def _load():
                                           ctypes.POINTER(seed_residual), P, P]),
         "seed_rotary_turns": (ctypes.c_int, [ctypes.POINTER(seed_rotary_scaling), ctypes.c_int32,
                                              ctypes.POINTER(ctypes.c_double)]),
-        "seed_rotate_rows": (ctypes.c_int, [ctypes.POINTER(seed_rows), ctypes.POINTER(seed_rotary), P, P, P, P]),
-        "seed_cache_append": (ctypes.c_int, [ctypes.POINTER(seed_cache), ctypes.POINTER(seed_tokens),
-                                             ctypes.POINTER(seed_rotary), P, P, P, P, P]),
-        "seed_attend_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(seed_cache), ctypes.POINTER(seed_tokens),
-                                                          ctypes.POINTER(seed_attend)]),
-        "seed_decode_attend": (ctypes.c_int, [ctypes.POINTER(seed_cache), ctypes.POINTER(seed_tokens),
-                                              ctypes.POINTER(seed_attend), P, P, P, P, ctypes.c_size_t, P]),
-        "seed_verify_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(seed_drafts)]),
-        "seed_verify_drafts": (ctypes.c_int, [ctypes.POINTER(seed_drafts), P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
+        # of a single token's calls: structures as bytes too (_packer), or by reference
+        "seed_rotate_rows": (ctypes.c_int, [P, P, P, P, P, P]),
+        "seed_cache_append": (ctypes.c_int, [P, P, P, P, P, P, P, P]),
+        "seed_attend_workspace_bytes": (ctypes.c_size_t, [P, P, P]),
+        "seed_decode_attend": (ctypes.c_int, [P, P, P, P, P, P, P, ctypes.c_size_t, P]),
+        "seed_verify_workspace_bytes": (ctypes.c_size_t, [P]),
+        "seed_verify_drafts": (ctypes.c_int, [P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
         "seed_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "seed_version": (ctypes.c_char_p, []),
     }
@@ -619,19 +630,19 @@ class _Args:
         return t.data_ptr()
 
     def rows(self, name, t, shape, width, dtype):
-        """Rows [shape[0], ...] of `width` contiguous elements each, which may be strided: the address
-        and the row stride in elements. (None, width) for None."""
+        """Rows [shape[0], ...] (None: as they are) of `width` contiguous elements each, which may be strided: the
+        address and the row stride in elements. (None, width) for None."""
         if t is None:
             return None, width
         if t.get_device() != self.device:
             self._on(name, t)
         if t.dtype is not dtype:
             raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-        if t.shape != shape:
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
         if t.is_contiguous():
             return t.data_ptr(), width
-        want, stride = 1, t.stride()
+        shape, want, stride = t.shape, 1, t.stride()
         for n, s in zip(reversed(shape[1:]), reversed(stride[1:])):
             if n != 1 and s != want:
                 raise ValueError(f"{name}: expected contiguous values inside a row")
@@ -795,6 +806,7 @@ class Rotary:
             raise ValueError("turns: expected a contiguous float64 device vector")
         self.turns = turns
         self.c = seed_rotary(2 * turns.numel(), 1 if interleaved else 0, amplitude, turns.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
 
 def make_rotary(dim: int, base: float = 10000.0, interleaved: bool = False, scaling: int = SEED_ROTARY_PLAIN,
@@ -859,12 +871,12 @@ def seed_rotate_rows(rotary: Rotary, x, positions, y, stream=None) -> None:
         raise ValueError(f"x: expected dtype float32 or bfloat16, got {dt}")
     rows, heads, dim = shape
     a, width = _Args(torch), heads * dim
-    xp, xs = a.rows("x", x, shape, width, dt)
+    xp, xs = a.rows("x", x, None, width, dt)
     yp, ys = a.rows("y", y, shape, width, dt)
-    a._on("rotary", rotary.turns)
-    a.launch("seed_rotate_rows", stream,
-             ctypes.byref(seed_rows(rows, heads, dim, SEED_F32 if dt is torch.float32 else SEED_BF16, xs, ys)),
-             ctypes.byref(rotary.c), xp, a.dense("positions", positions, rows, torch.int32), yp)
+    if rotary.turns.get_device() != a.device:
+        a._on("rotary", rotary.turns)
+    a.launch("seed_rotate_rows", stream, _ROWS(rows, heads, dim, SEED_F32 if dt is torch.float32 else SEED_BF16, xs, ys, 0, 0, 0),
+             rotary.ref, xp, a.dense("positions", positions, rows, torch.int32), yp)
 
 
 def seed_cache_append(cache: Cache, lengths, k, v, offsets=None, rotary: Rotary | None = None, q=None, q_out=None,
@@ -896,10 +908,10 @@ def seed_cache_append(cache: Cache, lengths, k, v, offsets=None, rotary: Rotary 
     if rotary is not None:
         if rotary.turns.get_device() != a.device:
             a._on("rotary", rotary.turns)
-        turn = ctypes.byref(rotary.c)
-    new = seed_tokens(n, a.dense("offsets", offsets, c.batch + 1, i32), a.dense("lengths", lengths, c.batch, i32), heads,
-                      q_stride, k_stride, v_stride, o_stride)
-    a.launch("seed_cache_append", stream, cache.ref, ctypes.byref(new), turn, qp, kp, vp, op)
+        turn = rotary.ref
+    new = _TOKENS(n, a.dense("offsets", offsets, c.batch + 1, i32) or 0, a.dense("lengths", lengths, c.batch, i32) or 0, heads,
+                  q_stride, k_stride, v_stride, o_stride)
+    a.launch("seed_cache_append", stream, cache.ref, new, turn, qp, kp, vp, op)
 
 
 def seed_attend_workspace_bytes(cache: Cache, tokens: int, heads: int, max_tokens: int = 1, max_length: int | None = None,
@@ -928,13 +940,13 @@ def seed_decode_attend(cache: Cache, lengths, q, o, offsets=None, max_tokens: in
     if len(shape) != 3 or shape[2] != dim:
         raise ValueError(f"q: expected [tokens, heads, {dim}], got {tuple(shape)}")
     n, heads = shape[0], shape[1]
-    qp, q_stride = a.rows("q", q, shape, heads * dim, dt)
+    qp, q_stride = a.rows("q", q, None, heads * dim, dt)
     op, o_stride = a.rows("o", o, shape, heads * dim, dt)
-    new = ctypes.byref(seed_tokens(n, a.dense("offsets", offsets, c.batch + 1, i32), a.dense("lengths", lengths, c.batch, i32),
-                                   heads, q_stride, 0, 0, o_stride))
+    new = _TOKENS(n, a.dense("offsets", offsets, c.batch + 1, i32) or 0, a.dense("lengths", lengths, c.batch, i32) or 0, heads,
+                  q_stride, 0, 0, o_stride)
     if max_length is None:
         max_length = c.page * c.width
-    how = ctypes.byref(seed_attend(max_tokens, max_length, window, dim ** -0.5 if scale is None else scale))
+    how = _ATTEND(max_tokens, max_length, window, dim ** -0.5 if scale is None else scale)
     lp = a.dense("lse", lse, n * heads, torch.float32)
     need = 0
     if ws is None:
@@ -943,7 +955,7 @@ def seed_decode_attend(cache: Cache, lengths, q, o, offsets=None, max_tokens: in
         if need is None:
             if len(cache.need) >= 1024:  # a serving loop's ever new sizes
                 cache.need.clear()
-            sizes = ctypes.byref(seed_attend(max_tokens, max_length, window, 1.0))  # the key's only: not a scale that is refused
+            sizes = _ATTEND(max_tokens, max_length, window, 1.0)  # the key's only: not a scale that is refused
             need = cache.need[key] = LIB.seed_attend_workspace_bytes(cache.ref, new, sizes)
     wp, size, ws = a.workspace(need, ws, stream)
     a.launch("seed_decode_attend", stream, cache.ref, new, how, qp, op, lp, wp, size)
@@ -967,10 +979,10 @@ def seed_verify_drafts(target, drafts, uniforms, draws, out, counts, offsets, dr
         raise ValueError(f"target: expected dtype float32 or bfloat16, got {dt}")
     a, shape, batch = _Args(torch), target.shape, counts.numel()
     n, vocab = shape
-    tp, t_stride = a.rows("target", target, shape, vocab, dt)
+    tp, t_stride = a.rows("target", target, None, vocab, dt)
     dp, d_stride = a.rows("draft", draft, shape, vocab, dt)
-    d = ctypes.byref(seed_drafts(batch, vocab, SEED_F32 if dt is f32 else SEED_BF16, n, a.dense("offsets", offsets, batch + 1, i32),
-                                 t_stride, d_stride))
+    d = _DRAFTS(batch, vocab, SEED_F32 if dt is f32 else SEED_BF16, n, a.dense("offsets", offsets, batch + 1, i32) or 0, t_stride,
+                d_stride)
     ptrs = (a.dense("drafts", drafts, n, i32), a.dense("uniforms", uniforms, n, f32), a.dense("draws", draws, batch, f32),
             a.dense("out", out, n, i32), a.dense("counts", counts, batch, i32))
     need = LIB.seed_verify_workspace_bytes(d) if ws is None else 0
