@@ -603,7 +603,7 @@ typedef struct seed_tokens {
  *   k, v    [tokens][key_heads][dim] rows (io_dtype).
  *   q       [tokens][heads][dim] rows, or NULL for none; q_out written, same shape (o_stride), may be q.
  * A row whose position is negative or beyond the table, or whose page is not there, is not stored (its q is still
- * turned, by that position). Rows of no request are not read or written.
+ * turned, by that position). Rows of no request may be read; nothing of them is stored, and their q_out is not written.
  */
 int seed_cache_append(const seed_cache *cache, const seed_tokens *tokens, const seed_rotary *rotary, const void *q,
                       const void *k, const void *v, void *q_out, void *stream);
