@@ -556,7 +556,7 @@ int seed_rotary_turns(const seed_rotary_scaling *scaling, int32_t dim, double *t
  * Rotary positions of rows x [rows][heads][dim] into y: row r is turned by positions[r] (int32
  * [rows], device memory, any value). Of `rows`, rows, heads, dim, io_dtype, x_stride and y_stride are used.
  * Queries and keys side by side in one buffer are one call over both heads' columns. y may be x (same
- * address and stride): then the values behind the rotated ones are not touched.
+ * address and stride). The values behind the rotated ones keep their bits.
  */
 int seed_rotate_rows(const seed_rows *rows, const seed_rotary *rotary, const void *x, const int32_t *positions,
                      void *y, void *stream);
