@@ -566,7 +566,8 @@ int seed_rotate_rows(const seed_rows *rows, const seed_rotary *rotary, const voi
  * head h of a slot is `dim` contiguous values at k (or v) + page_stride number + token_stride slot + head_stride h.
  * Pages are [page][key_heads][dim] (token_stride >= key_heads head_stride) or [key_heads][page][dim] (head_stride >=
  * page token_stride), without overlaps inside a page or between pages (else SEED_ERR_ARG), token_stride at most 2^24
- * elements (else SEED_ERR_UNSUPPORTED); k and v have the same strides and may lie side by side in one buffer.
+ * elements (else SEED_ERR_UNSUPPORTED); k and v have the same strides and may lie side by side in one buffer, sharing no
+ * byte (else SEED_ERR_ARG).
  * table entries are read on the device where a position needs them, and not checked on the host: one outside
  * 0 .. pages - 1 is a page that is not there. A page may be listed by several requests (a shared
  * prefix); only pages that receive new rows must belong to one.

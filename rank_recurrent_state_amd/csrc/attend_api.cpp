@@ -63,25 +63,40 @@ bool meets(const Rows& r, const seed_cache* c, const void* p) {
   const Rows q = pool(c, p);
   return !(r.hi() <= q.lo() || q.hi() <= r.lo());
 }
-// Whether k and v share a byte. Of one set of strides, they may lie side by side at every level: by
-// pages, and inside a page by tokens or by heads.
+// A pool's pages, the tokens (or heads) of a page, and the heads (tokens) of those: `count` blocks of `width` bytes,
+// `stride` bytes apart, which is at least the width where there is a second one.
+struct Level {
+  int64_t stride, count, width;
+};
+// Whether one of k's blocks and one of v's share a byte, v's first lying d bytes behind k's first. Blocks n of v and m of
+// k are d + (n - m) stride apart: only the two distances next to 0 are below a width.
+bool blocks_meet(const Level* level, int levels, int64_t d) {
+  const Level& l = *level;
+  if (l.count == 1) return d > -l.width && d < l.width && (levels == 1 || blocks_meet(level + 1, levels - 1, d));
+  int64_t steps = d / l.stride, rest = d % l.stride;
+  if (rest < 0) {
+    rest += l.stride;
+    --steps;
+  }
+  auto meet = [&](int64_t n, int64_t way) {
+    return n > -l.count && n < l.count && way > -l.width && way < l.width && (levels == 1 || blocks_meet(level + 1, levels - 1, way));
+  };
+  return meet(steps, rest) || meet(steps + 1, rest - l.stride);
+}
+// Whether k and v share a byte. Of one set of strides, they may lie side by side: by pages, tokens or heads, whether or not
+// one stride is a multiple of another.
 bool pools_meet(const seed_cache* c) {
   const Rows a = pool(c, c->k), b = pool(c, c->v);
   if (a.hi() <= b.lo() || b.hi() <= a.lo()) return false;
-  const uintptr_t e = static_cast<uintptr_t>(io_bytes(c->io_dtype));
-  const uintptr_t d = a.lo() <= b.lo() ? b.lo() - a.lo() : a.lo() - b.lo();
-  const int64_t dim = c->dim, heads = c->key_heads, page = c->page;
-  const bool by_token = c->token_stride >= (heads - 1) * c->head_stride + dim;
-  const int64_t stride[3] = {c->page_stride, by_token ? c->token_stride : c->head_stride, by_token ? c->head_stride : c->token_stride};
-  const int64_t count[3] = {c->pages, by_token ? page : heads, by_token ? heads : page};
-  const int64_t block[3] = {(page - 1) * c->token_stride + (heads - 1) * c->head_stride + dim,
-                            by_token ? (heads - 1) * c->head_stride + dim : (page - 1) * c->token_stride + dim, dim};
-  for (int i = 0; i < 3; ++i) {
-    if (count[i] == 1) continue;  // no second block at this level
-    const uintptr_t s = static_cast<uintptr_t>(stride[i]) * e, w = static_cast<uintptr_t>(block[i]) * e, r = d % s;
-    if (r >= w && r + w <= s) return false;
+  const int64_t e = io_bytes(c->io_dtype), d = static_cast<int64_t>(b.lo() - a.lo());
+  const int64_t head = c->dim * e, heads = c->key_heads, page = c->page, hs = c->head_stride * e, ts = c->token_stride * e;
+  const Level pages{c->page_stride * e, c->pages, page_bytes(c)};
+  if (ts >= (heads - 1) * hs + head) {  // by token
+    const Level levels[3] = {pages, {ts, page, (heads - 1) * hs + head}, {hs, heads, head}};
+    return blocks_meet(levels, 3, d);
   }
-  return true;
+  const Level levels[3] = {pages, {hs, heads, (page - 1) * ts + head}, {ts, page, head}};
+  return blocks_meet(levels, 3, d);
 }
 
 int check_tokens(const seed_cache* c, const seed_tokens* t, bool queries) {
