@@ -910,7 +910,7 @@ bool plan_attend(int32_t io_dtype, AttendArgs& a) {
                                          : std::min(std::max(units / per_turn, int64_t{4}), int64_t{64}) * step;
   a.groups = 0;
   a.few = span <= kWaves * tile;  // one turn of 4 wavefronts
-  if (span <= few) return true;
+  if (span <= few) return units <= most_blocks((a.row_waves == 1 && !a.few ? kMany : kWaves) * kWave);
   a.groups = static_cast<int32_t>(std::max(std::min((kGroups + a.c.key_heads - 1) / a.c.key_heads, turns), int64_t{1}));
   return true;
 }

@@ -10,6 +10,9 @@
 
 namespace seed {
 
+// Workgroups of a launch: it has fewer than 2^32 threads.
+constexpr int64_t most_blocks(int64_t threads) { return ((int64_t{1} << 32) - 1) / threads; }
+
 struct RotateArgs {
   int64_t rows;
   int32_t heads, dim, rot, interleaved;
@@ -86,12 +89,13 @@ struct VerifyArgs {
 
 hipError_t launch_rotate_rows(int32_t io_dtype, const RotateArgs& a, hipStream_t s);
 hipError_t launch_cache_append(int32_t io_dtype, const AppendArgs& a, hipStream_t s);
-// Sets row_waves, block_rows, row_blocks and groups from the sizes; false: more turns than are counted.
+// Sets row_waves, block_rows, row_blocks and groups from the sizes; false: more turns or workgroups than are counted.
 bool plan_attend(int32_t io_dtype, AttendArgs& a);
 int64_t attend_workspace(const AttendArgs& a);
 hipError_t launch_attend(int32_t io_dtype, AttendArgs a, void* ws, hipStream_t s);
 int32_t verify_segments(int32_t vocab);
 int32_t verify_alone();  // most segments of a request that one workgroup does without a workspace
+inline constexpr int32_t kAloneThreads = 1024;  // of that workgroup
 hipError_t launch_verify(int32_t io_dtype, const VerifyArgs& a, hipStream_t s);
 
 #ifdef __HIPCC__

@@ -12,7 +12,7 @@ namespace {
 
 using namespace seed;
 
-constexpr int64_t kMostBlocks = (int64_t{1} << 24) - 1;  // of 256 threads: a launch has fewer than 2^32
+constexpr int64_t kMostBlocks = most_blocks(256);
 constexpr int64_t kMostTokenStride = int64_t{1} << 24;   // 16 positions' bytes are 32-bit offsets
 constexpr int32_t kMostShare = 1 << 14;                  // a row's token is found in fp32
 constexpr int64_t kMostPositions = int64_t{1} << 30;     // positions and their tiles' ends are int32
@@ -161,7 +161,9 @@ int check_drafts(const seed_drafts* d) {
   if (!d || d->batch <= 0 || d->vocab <= 0 || d->rows < 0 || !io_ok(d->io_dtype)) return SEED_ERR_ARG;
   if (d->io_dtype == SEED_F16) return SEED_ERR_UNSUPPORTED;
   if (d->rows > kMostRows || d->vocab > (1 << 30)) return SEED_ERR_UNSUPPORTED;
-  if (verify_segments(d->vocab) > kMostBlocks / d->batch) return SEED_ERR_UNSUPPORTED;
+  const int32_t segments = verify_segments(d->vocab);
+  if (segments > kMostBlocks / d->batch) return SEED_ERR_UNSUPPORTED;
+  if (segments <= verify_alone() && d->batch > most_blocks(kAloneThreads)) return SEED_ERR_UNSUPPORTED;
   return SEED_OK;
 }
 int64_t verify_workspace(const seed_drafts* d) {

@@ -21,7 +21,7 @@ namespace {
 constexpr int kRun = 16;                  // tokens of a lane
 constexpr int kSegment = kWave * kRun;    // and of a segment
 constexpr int kWaves = 4;                 // of a workgroup that sums
-constexpr int kMany = 16;                 // of one that does a request alone
+constexpr int kMany = kAloneThreads / kWave;  // of one that does a request alone
 // Segments of such a request. One request of 16384 fp32 tokens: 7.1 us, in two launches 8.2; of 32768: 8.4 and 8.6; of
 // 65536: 11 and 8. 64 of 16384: 8 and 10; of 32768: 12 and 10; 200 of 32768: 13 and 14.
 constexpr int kMost = 32;
