@@ -617,8 +617,10 @@ typedef struct seed_attend {
   float scale;         /* of the products q . k; finite and not 0                                */
 } seed_attend;
 
-/* Workspace bytes of seed_decode_attend (0: none needed, or invalid arguments): fp32 partial results of about 1024
- * times up to 64 rows (up to 67 MB for heads of 256), whatever the lengths. Host-only, pure. */
+/* Workspace bytes of seed_decode_attend (0: none needed, or invalid arguments), whatever the lengths: fp32 partial
+ * results of up to 64 rows, dim + 2 values each, in at most 2 (511 + key_heads) places (1024 where key_heads divides
+ * 512: 68 MB for 64 rows of 256; none from 512 key heads on), and 8 bytes for each request and 16 rows of a key head.
+ * Host-only, pure. */
 size_t seed_attend_workspace_bytes(const seed_cache *cache, const seed_tokens *tokens, const seed_attend *attend);
 
 /*

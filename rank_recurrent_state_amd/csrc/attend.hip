@@ -915,15 +915,20 @@ bool plan_attend(int32_t io_dtype, AttendArgs& a) {
   return true;
 }
 
+namespace {
+// Rows of partial results: two places for each workgroup, none where one has all of a key head's turns.
+int64_t places_of(const AttendArgs& a) { return a.groups > 1 ? static_cast<int64_t>(a.groups) * a.c.key_heads * 2 * a.block_rows : 0; }
+}  // namespace
+
 int64_t attend_workspace(const AttendArgs& a) {
   if (a.groups == 0) return 0;
-  const int64_t places = static_cast<int64_t>(a.groups) * a.c.key_heads * 2 * a.block_rows;
+  const int64_t places = places_of(a);
   return places * (a.c.dim + 2) * 4 + static_cast<int64_t>(a.c.batch) * a.row_blocks * 8;
 }
 
 hipError_t launch_attend(int32_t io_dtype, AttendArgs a, void* ws, hipStream_t s) {
   if (a.groups > 0) {
-    const int64_t places = static_cast<int64_t>(a.groups) * a.c.key_heads * 2 * a.block_rows;
+    const int64_t places = places_of(a);
     a.part = static_cast<float*>(ws);
     a.stat = a.part + places * a.c.dim;
     a.notes = reinterpret_cast<int32_t*>(a.stat + places * 2);

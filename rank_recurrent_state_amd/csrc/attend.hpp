@@ -67,7 +67,7 @@ struct AttendArgs {
   const void* q;
   void* o;
   float* lse;      // nullptr: not written
-  float* part;     // [groups][key_heads][2][block_rows][dim]: accumulators of rows that several workgroups have,
+  float* part;     // [groups][key_heads][2][block_rows][dim]: accumulators of rows that several workgroups have (groups 1: none),
   float* stat;     // and their maximum and sum [..][block_rows][2]
   int32_t* notes;  // [batch][row_blocks][2]: the first and last workgroup of each
 };

@@ -43,3 +43,26 @@ def test_verification_workgroups():
 
     for batch, vocab in ((MOST // 1024 + 1, 1), (MOST // 1024 + 1, 32768), ((1 << 31) - 1, 2), (1 << 23, 32769), (1 << 22, 32768)):
         assert call(batch, vocab) == r.SEED_ERR_UNSUPPORTED, (batch, vocab)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("share,max_tokens", [(1, 1), (4, 6), (16, 32)])
+def test_attention_workspace_bound(io, dim, share, max_tokens):
+    """At most 2 (511 + key_heads) places of up to 64 rows, none from 512 key heads on, and 8 bytes for each request and
+    row block; whatever the lengths."""
+    r = _lib()
+    code = {"bf16": r.SEED_BF16, "f32": r.SEED_F32}[io]
+    for key_heads in (1, 2, 3, 7, 8, 100, 256, 257, 300, 510, 511, 512, 513, 1024, 4096):
+        for batch in (1, 5):
+            if batch * share * max_tokens * key_heads >= 1 << 24:
+                continue
+            for length in (4096, 1 << 20):
+                cache = r.seed_cache(batch, key_heads, dim, code, 16, 1 << 16, 4, 16 * key_heads * dim, key_heads * dim, dim, 16 * FAR, 32 * FAR, 48 * FAR)
+                new = r.seed_tokens(batch, FAR, 2 * FAR, share * key_heads, share * key_heads * dim, 0, 0, share * key_heads * dim)
+                how = r.seed_attend(max_tokens, length, 0, 0.1)
+                need = r.LIB.seed_attend_workspace_bytes(ctypes.byref(cache), ctypes.byref(new), ctypes.byref(how))
+                rows = min(share * max_tokens, 64)
+                notes = 8 * batch * -(-share * max_tokens // 16)
+                places = 2 * (511 + key_heads) if key_heads < 512 else 0
+                assert (length == 4096 or need > 0) and need <= places * rows * (dim + 2) * 4 + notes, (key_heads, batch, length)
