@@ -122,6 +122,7 @@ def _packer(cls):
     return packed.pack
 
 
+_NOT_PACKED = struct.error  # a number that its type does not hold, or none at all
 _ROWS, _TOKENS, _ATTEND, _DRAFTS = _packer(seed_rows), _packer(seed_tokens), _packer(seed_attend), _packer(seed_drafts)
 
 
@@ -875,8 +876,11 @@ def seed_rotate_rows(rotary: Rotary, x, positions, y, stream=None) -> None:
     yp, ys = a.rows("y", y, shape, width, dt)
     if rotary.turns.get_device() != a.device:
         a._on("rotary", rotary.turns)
-    a.launch("seed_rotate_rows", stream, _ROWS(rows, heads, dim, SEED_F32 if dt is torch.float32 else SEED_BF16, xs, ys, 0, 0, 0),
-             rotary.ref, xp, a.dense("positions", positions, rows, torch.int32), yp)
+    try:
+        sizes = _ROWS(rows, heads, dim, SEED_F32 if dt is torch.float32 else SEED_BF16, xs, ys, 0, 0, 0)
+    except _NOT_PACKED as e:
+        raise ValueError(f"x: {tuple(shape)}: {e}") from None
+    a.launch("seed_rotate_rows", stream, sizes, rotary.ref, xp, a.dense("positions", positions, rows, torch.int32), yp)
 
 
 def seed_cache_append(cache: Cache, lengths, k, v, offsets=None, rotary: Rotary | None = None, q=None, q_out=None,
@@ -919,9 +923,12 @@ def seed_attend_workspace_bytes(cache: Cache, tokens: int, heads: int, max_token
     """Workspace bytes of seed_decode_attend for `tokens` new rows of `heads` query heads (ragged: the call
     gets offsets); 0 also for invalid sizes."""
     c = cache.c
-    new = seed_tokens(tokens, c.table if ragged else None, c.table, heads, heads * c.dim, 0, 0, heads * c.dim)
-    how = seed_attend(max_tokens, c.page * c.width if max_length is None else max_length, window, 1.0)
-    return int(LIB.seed_attend_workspace_bytes(cache.ref, ctypes.byref(new), ctypes.byref(how)))
+    try:
+        new = _TOKENS(tokens, c.table if ragged else 0, c.table, heads, heads * c.dim, 0, 0, heads * c.dim)
+        how = _ATTEND(max_tokens, c.page * c.width if max_length is None else max_length, window, 1.0)
+    except _NOT_PACKED:
+        return 0
+    return int(LIB.seed_attend_workspace_bytes(cache.ref, new, how))
 
 
 def seed_decode_attend(cache: Cache, lengths, q, o, offsets=None, max_tokens: int = 1, max_length: int | None = None,
@@ -946,7 +953,10 @@ def seed_decode_attend(cache: Cache, lengths, q, o, offsets=None, max_tokens: in
                   q_stride, 0, 0, o_stride)
     if max_length is None:
         max_length = c.page * c.width
-    how = _ATTEND(max_tokens, max_length, window, dim ** -0.5 if scale is None else scale)
+    try:
+        how = _ATTEND(max_tokens, max_length, window, dim ** -0.5 if scale is None else scale)
+    except _NOT_PACKED as e:
+        raise ValueError(f"max_tokens {max_tokens}, max_length {max_length}, window {window}, scale {scale}: {e}") from None
     lp = a.dense("lse", lse, n * heads, torch.float32)
     need = 0
     if ws is None:
@@ -962,7 +972,11 @@ def seed_decode_attend(cache: Cache, lengths, q, o, offsets=None, max_tokens: in
 
 
 def seed_verify_workspace_bytes(batch: int, vocab: int) -> int:
-    return int(LIB.seed_verify_workspace_bytes(ctypes.byref(seed_drafts(batch, vocab, SEED_F32, 0, None, vocab, vocab))))
+    try:
+        d = _DRAFTS(batch, vocab, SEED_F32, 0, 0, vocab, vocab)
+    except _NOT_PACKED:
+        return 0
+    return int(LIB.seed_verify_workspace_bytes(d))
 
 
 def seed_verify_drafts(target, drafts, uniforms, draws, out, counts, offsets, draft=None, ws=None, stream=None) -> None:
@@ -981,8 +995,11 @@ def seed_verify_drafts(target, drafts, uniforms, draws, out, counts, offsets, dr
     n, vocab = shape
     tp, t_stride = a.rows("target", target, None, vocab, dt)
     dp, d_stride = a.rows("draft", draft, shape, vocab, dt)
-    d = _DRAFTS(batch, vocab, SEED_F32 if dt is f32 else SEED_BF16, n, a.dense("offsets", offsets, batch + 1, i32) or 0, t_stride,
-                d_stride)
+    ends = a.dense("offsets", offsets, batch + 1, i32) or 0
+    try:
+        d = _DRAFTS(batch, vocab, SEED_F32 if dt is f32 else SEED_BF16, n, ends, t_stride, d_stride)
+    except _NOT_PACKED as e:
+        raise ValueError(f"target: {tuple(shape)}: {e}") from None
     ptrs = (a.dense("drafts", drafts, n, i32), a.dense("uniforms", uniforms, n, f32), a.dense("draws", draws, batch, f32),
             a.dense("out", out, n, i32), a.dense("counts", counts, batch, i32))
     need = LIB.seed_verify_workspace_bytes(d) if ws is None else 0
