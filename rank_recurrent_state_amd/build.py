@@ -21,7 +21,7 @@ OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libseed.so")
 SOURCES = ["api.cpp", "decode.hip", "dense.hip", "compress.hip", "compress_wave.hip", "energy.hip", "chunk.hip",
            "prompt_api.cpp", "conv.hip", "scan.hip", "scan_chunk.hip", "norm_rows.hip",
-           "attend_api.cpp", "rotate.hip", "attend.hip", "verify.hip"]
+           "attend_api.cpp", "attend_plan.cpp", "rotate.hip", "attend.hip", "verify.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

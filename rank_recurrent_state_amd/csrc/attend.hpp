@@ -1,5 +1,5 @@
-// Internal launch interface of the attention layers (attend_api.cpp to rotate.hip, attend.hip and
-// verify.hip).
+// Internal launch interface of the attention layers (attend_api.cpp to attend_plan.cpp, rotate.hip, attend.hip
+// and verify.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -72,6 +72,13 @@ struct AttendArgs {
   int32_t* notes;  // [batch][row_blocks][2]: the first and last workgroup of each
 };
 
+// What the attention's plan and its kernels share.
+namespace plan {
+inline constexpr int kWaves = 4;  // of a workgroup; short caches take kMany
+inline constexpr int kMany = 8;
+inline constexpr int kShared = 16384;  // bytes of keys in a tile that the wavefronts share
+}  // namespace plan
+
 struct VerifyArgs {
   int32_t batch, vocab, segments;
   int64_t rows, target_stride, draft_stride;
@@ -89,8 +96,11 @@ struct VerifyArgs {
 
 hipError_t launch_rotate_rows(int32_t io_dtype, const RotateArgs& a, hipStream_t s);
 hipError_t launch_cache_append(int32_t io_dtype, const AppendArgs& a, hipStream_t s);
-// Sets row_waves, block_rows, row_blocks and groups from the sizes; false: more turns or workgroups than are counted.
+// Sets row_waves, block_rows, row_blocks, change, few and groups from the sizes; false: more turns or workgroups than are
+// counted.
 bool plan_attend(int32_t io_dtype, AttendArgs& a);
+// Rows of partial results: two places for each workgroup, none where one has all of a key head's turns.
+int64_t attend_places(const AttendArgs& a);
 int64_t attend_workspace(const AttendArgs& a);
 hipError_t launch_attend(int32_t io_dtype, AttendArgs a, void* ws, hipStream_t s);
 int32_t verify_segments(int32_t vocab);
