@@ -1,16 +1,19 @@
 // Verification of drafted tokens: a request's drafts x are kept in turn while u q(x) < p(x); the token at the
 // first refused row is the smallest t with draw W < w_0 + .. + w_t, w = max(p - q, 0) (behind the last draft: p).
 //
-// What bounds it: one row of p and one of q per request, read once from HBM; for few requests the latency of
+// What bounds it: one row of p, and one of q where a draft is refused, read once from HBM; for few requests the latency of
 // what follows from what: the row's number, a few drafts' probabilities, the row, the sums, the segment that holds
 // the draw. Rows are cut into segments of 1024 tokens, a wavefront each: it sums them (fp64: exact products and
 // differences, and borders between tokens that do not move with the order of the sums by more than 1e-13), then the
 // segment that holds the draw is read again and its tokens are walked. Every wavefront finds the request's first
 // refused row by itself, from a few gathered values, and no step needs more than one wavefront: a row that one
 // workgroup reads as fast as a second launch takes is summed and walked by it, larger ones in two launches.
-// Measured: 128 requests, 150001 tokens, fp32, 154 MB: 24 us, 6.4 TB/s; 200 requests, 65536 tokens, bf16, no drafts'
-// probabilities, 26 MB: 13 us, of which the sums take 9: four loads one after another lead to a row, and conversions and
-// sums in fp64 take as long as the reads (14 us with the choice of positive weights and of x in fp64 for all). Two segments a wavefront at once: the same or up to 1 us more.
+// Measured: 128 requests, 150001 tokens, fp32, of which 50 refuse a draft and read its row too, 107 MB: 24 us, 4.5 TB/s.
+// The sums take 19 to 21 (5.5 TB/s; wavefronts wait 63 % of their time, the vector unit is busy 27 % of it), the choice 5.
+// 200 requests, 65536 tokens, bf16, no drafts' probabilities, 26 MB: 13 us, the sums 9.5 (wavefronts wait 69 %, vector unit
+// 45 %: neither it nor HBM is the bound, but what waits one after another), the choice 4 to 5, both launches' starts and
+// ends among them. The loads that lead to the refused row are 1 us of it (no drafts: 10.4 us from 11.5, captured). 14 us
+// with the choice of positive weights and of x in fp64 for all. Two segments a wavefront at once: the same or up to 1 us more.
 #include "attend.hpp"
 #include "common.hpp"
 
