@@ -637,7 +637,8 @@ size_t seed_attend_workspace_bytes(const seed_cache *cache, const seed_tokens *t
  * Short caches (by max_length and the other sizes) are one launch; the keys of longer ones are cut into equal shares
  * by the requests' lengths, on the device, and joined by a second launch. max_length may be far above the lengths;
  * close to short ones it saves the second launch and the workspace. Weights, up to 2^8, and sums are fp32, and a sum of
- * weights times values that leaves fp32 is an infinity; bf16 weights enter the products in two pieces. The same call gives the same bits, on any stream and in a replayed graph too.
+ * weights times values that leaves fp32 is an infinity; bf16 weights enter the products in two pieces. The same call
+ * gives the same bits, on any stream and in a replayed graph too.
  */
 int seed_decode_attend(const seed_cache *cache, const seed_tokens *tokens, const seed_attend *attend, const void *q,
                        void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
